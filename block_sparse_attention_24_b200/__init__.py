@@ -29,7 +29,8 @@ EXPORTED = ("veda_layout", "veda_permute", "veda_trippool", "veda_permute_trippo
             "veda_tile_scores_noalloc",
             "veda_topk_mask", "veda_tile_scores_topk", "veda_tile_scores_heads", "veda_topk_mask_heads", "veda_score_cache_step", "veda_score_cache_ws_bytes", "veda_sparse_attn", "veda_sparse_attn_unpermute", "veda_sparse_attn_tokens", "veda_full_attn_tilemax", "veda_full_attn_tilemax_ws_bytes", "veda_tilemap_kl", "veda_tilemap_recall",
             "veda_check_status",
-            "veda_estimator_grad", "veda_estimator_grad_ws_bytes", "veda_output_sq_error", "veda_selftest_wait_timeout", "veda_last_error")
+            "veda_estimator_grad", "veda_estimator_grad_ws_bytes", "veda_output_sq_error", "veda_selftest_wait_timeout", "veda_last_error",
+            "veda_kv_append", "veda_kv_advance", "veda_kv_attn", "veda_kv_attn_ws_bytes", "veda_kv_evict", "veda_kv_check_status")
 
 
 class VedaError(RuntimeError):
@@ -55,6 +56,12 @@ class _Layer(ctypes.Structure):
     _fields_ = [("B", ctypes.c_int32), ("heads", ctypes.c_int32), ("d", ctypes.c_int32), ("T", ctypes.c_int32),
                 ("H", ctypes.c_int32), ("W", ctypes.c_int32), ("tile", ctypes.c_int32),
                 ("tilings", ctypes.POINTER(_Tiling)), ("dev_status", ctypes.c_void_p)]
+
+
+class _KvCache(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int32) for n in ("B", "heads_kv", "d", "tile", "n_slots", "nb_cap")] +
+                [(n, ctypes.c_void_p) for n in ("k8", "v8", "table", "pos", "k_scale", "v_scale", "weight", "len",
+                                                "next_pos", "dev_status")])
 
 
 _P = ctypes.c_void_p
@@ -90,11 +97,20 @@ _lib.veda_estimator_grad_ws_bytes.restype = ctypes.c_size_t
 _lib.veda_output_sq_error.argtypes = [_LP, _P, _P, _P, _P]
 _lib.veda_check_status.argtypes = [_LP, _P]
 _lib.veda_selftest_wait_timeout.argtypes = [_LP, ctypes.c_uint32, _P]
+_CP = ctypes.POINTER(_KvCache)
+_lib.veda_kv_append.argtypes = [_CP, _P, _P, _P, _P, _I, _P, _P]
+_lib.veda_kv_advance.argtypes = [_CP, _I, _P, _P]
+_lib.veda_kv_attn.argtypes = [_CP, _P, _P, _I, _I, _P, _I, _I, _I, _I, _F, _P, _P, _P, _P, _F, _P, _P]
+_lib.veda_kv_attn_ws_bytes.argtypes = [_CP, _I, _I, _I]
+_lib.veda_kv_attn_ws_bytes.restype = ctypes.c_size_t
+_lib.veda_kv_evict.argtypes = [_CP, _P, _I, _I, _CP, _P]
+_lib.veda_kv_check_status.argtypes = [_CP, _P]
 _lib.veda_last_error.restype = ctypes.c_char_p
 for _name in EXPORTED:
     getattr(_lib, _name)
     if _name not in ("veda_last_error", "veda_tile_scores_ws_bytes", "veda_estimator_grad_ws_bytes",
-                     "veda_full_attn_tilemax_ws_bytes", "veda_score_cache_ws_bytes"):
+                     "veda_full_attn_tilemax_ws_bytes", "veda_score_cache_ws_bytes",
+                     "veda_kv_attn_ws_bytes"):
         getattr(_lib, _name).restype = ctypes.c_int
 
 
@@ -320,6 +336,172 @@ def veda_check_status(layer: Layer, stream=None):
 
 def veda_selftest_wait_timeout(layer: Layer, limit_ms: int, stream=None):
     _check(_lib.veda_selftest_wait_timeout(layer.ref, int(limit_ms), _stream(stream)))
+
+
+class KVCache:
+    """An 8-bit K/V tile cache (veda_kv_cache) and the tensors it is made of:
+    k8, v8 [n_slots, tile, d] float8_e4m3fn; table, pos (int32), k_scale,
+    v_scale, weight (fp32) [B, heads_kv, nb_cap]; len [B, heads_kv] and
+    next_pos [B] (int32). Those not given are allocated: an empty cache whose
+    table names slot (b * heads_kv + h) * nb_cap + i for tile i. Tensors are
+    used where they are (no copy) and are the caller's to look at and to
+    change between calls."""
+
+    _META = (("table", torch.int32), ("pos", torch.int32), ("k_scale", torch.float32), ("v_scale", torch.float32),
+             ("weight", torch.float32))
+
+    def __init__(self, B: int, heads_kv: int, d: int, tile: int, nb_cap: int, device, k8=None, v8=None, table=None,
+                 pos=None, k_scale=None, v_scale=None, weight=None, len=None, next_pos=None):
+        self.B, self.heads_kv, self.d, self.tile, self.nb_cap = B, heads_kv, d, tile, nb_cap
+        if min(B, heads_kv, d, tile, nb_cap) < 1:
+            raise ValueError("B, heads_kv, d, tile and nb_cap must be positive")
+        device = torch.device(device)
+        given = dict(k8=k8, v8=v8, table=table, pos=pos, k_scale=k_scale, v_scale=v_scale, weight=weight, len=len,
+                     next_pos=next_pos)
+        n_slots = B * heads_kv * nb_cap
+        for name in ("k8", "v8"):
+            if given[name] is not None:
+                n_slots = given[name].shape[0]
+        shape = (B, heads_kv, nb_cap)
+        spec = {"k8": ((n_slots, tile, d), torch.float8_e4m3fn), "v8": ((n_slots, tile, d), torch.float8_e4m3fn),
+                "len": (shape[:2], torch.int32), "next_pos": (shape[:1], torch.int32)}
+        spec.update({name: (shape, dtype) for name, dtype in self._META})
+        for name, (shp, dtype) in spec.items():
+            t = given[name]
+            if t is None:
+                if name == "table":
+                    if n_slots < B * heads_kv * nb_cap:
+                        raise ValueError("a pool smaller than B * heads_kv * nb_cap slots needs a table")
+                    t = torch.arange(B * heads_kv * nb_cap, dtype=dtype, device=device).view(shape)
+                elif name in ("k8", "v8"):
+                    t = torch.zeros(shp, dtype=torch.uint8, device=device).view(dtype)
+                else:
+                    t = torch.zeros(shp, dtype=dtype, device=device)
+            _expect(t, name, shp, dtype, None)
+            if device.type == "cuda" and device.index is None and t.device.type == "cuda":
+                device = t.device
+            if t.device != device:
+                raise ValueError(f"{name} is on {t.device}, not on {device}")
+            setattr(self, name, t)
+        self.device = device
+        self.n_slots = n_slots
+        self.status = torch.zeros(4, dtype=torch.int32, device=device)
+        self._c = _KvCache(B, heads_kv, d, tile, n_slots, nb_cap,
+                           *[getattr(self, n).data_ptr() for n in ("k8", "v8", "table", "pos", "k_scale", "v_scale",
+                                                                   "weight", "len", "next_pos", "status")])
+
+    @property
+    def ref(self):
+        return ctypes.byref(self._c)
+
+
+def _expect(t, name: str, shape, dtype, device, contiguous: bool = True):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a tensor")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, not {t.dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} is on {t.device}, not on {device}")
+    if contiguous and not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _rows(t: torch.Tensor, name: str, shape, cache: KVCache):
+    """Pointer and strides of a [B, n, heads, d] bf16 tensor whose last
+    dimension is contiguous."""
+    _expect(t, name, shape, torch.bfloat16, cache.device, contiguous=False)
+    st = [s if n > 1 else 0 for s, n in zip(t.stride()[:3], t.shape[:3])]
+    if t.numel() and t.stride(3) != 1:
+        raise ValueError(f"{name}: the last dimension must be contiguous")
+    return ctypes.c_void_p(t.data_ptr()), (ctypes.c_int64 * 3)(*st)
+
+
+def _kv_call(cache: KVCache, stream, call):
+    """`call(stream pointer)` on the cache's device, on `stream` or that
+    device's current one."""
+    if stream is not None and stream.device != cache.device:
+        raise ValueError(f"the stream is on {stream.device}, the cache on {cache.device}")
+    if cache.device.type != "cuda":
+        raise ValueError("the cache is not on a CUDA device")
+    with torch.cuda.device(cache.device):
+        _check(call(_stream(stream)))
+
+
+def _n_new(cache: KVCache, n_new):
+    if n_new is None:
+        return None
+    _expect(n_new, "n_new", (cache.B,), torch.int32, cache.device)
+    return ctypes.c_void_p(n_new.data_ptr())
+
+
+def veda_kv_append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, n_new: Optional[torch.Tensor] = None,
+                   stream=None):
+    """K and V [B, n, heads_kv, d] of n new tokens into the cache, as pending
+    tokens behind those it holds (n_new [B]: how many of each sequence's rows
+    are real)."""
+    if not isinstance(k, torch.Tensor) or k.dim() != 4:
+        raise ValueError("k must be a [B, n, heads_kv, d] tensor")
+    n = k.shape[1]
+    kp, ks = _rows(k, "k", (cache.B, n, cache.heads_kv, cache.d), cache)
+    vp, vs = _rows(v, "v", (cache.B, n, cache.heads_kv, cache.d), cache)
+    nn = _n_new(cache, n_new)
+    _kv_call(cache, stream, lambda s: _lib.veda_kv_append(cache.ref, kp, ks, vp, vs, n, nn, s))
+
+
+def veda_kv_advance(cache: KVCache, n: int, n_new: Optional[torch.Tensor] = None, stream=None):
+    """Take the n (or n_new[b]) pending tokens in."""
+    nn = _n_new(cache, n_new)
+    _kv_call(cache, stream, lambda s: _lib.veda_kv_advance(cache.ref, int(n), nn, s))
+
+
+def veda_kv_attn_ws_bytes(cache: KVCache, heads: int, n_q: int, with_weight: bool = False) -> int:
+    return int(_lib.veda_kv_attn_ws_bytes(cache.ref, heads, n_q, int(with_weight)))
+
+
+def veda_kv_attn(cache: KVCache, q: torch.Tensor, o: torch.Tensor, scale: float, ws: torch.Tensor,
+                 causal: bool = True, window: int = 0, sinks: int = 0, n_new: Optional[torch.Tensor] = None,
+                 pending: bool = True, lse: Optional[torch.Tensor] = None, weight: Optional[torch.Tensor] = None,
+                 decay: float = 1.0, stream=None):
+    """Attention of q [B, n_q, heads, d] over the cache, into o. ws: device
+    scratch of veda_kv_attn_ws_bytes(cache, heads, n_q, weight is not None)
+    bytes. weight: [B, heads_kv, nb_cap], e.g. cache.weight."""
+    if not isinstance(q, torch.Tensor) or q.dim() != 4:
+        raise ValueError("q must be a [B, n_q, heads, d] tensor")
+    n, heads = q.shape[1], q.shape[2]
+    shape = (cache.B, n, heads, cache.d)
+    qp, qs = _rows(q, "q", shape, cache)
+    op, os_ = _rows(o, "o", shape, cache)
+    if lse is not None:
+        _expect(lse, "lse", (cache.B, heads, n), torch.float32, cache.device)
+    if weight is not None:
+        _expect(weight, "weight", (cache.B, cache.heads_kv, cache.nb_cap), torch.float32, cache.device)
+    need = veda_kv_attn_ws_bytes(cache, heads, n, weight is not None)
+    if not isinstance(ws, torch.Tensor) or ws.device != cache.device or not ws.is_contiguous():
+        raise ValueError("ws must be a contiguous tensor on the cache's device")
+    if ws.numel() * ws.element_size() < need:
+        raise ValueError(f"ws holds {ws.numel() * ws.element_size()} bytes, {need} are needed")
+    nn = _n_new(cache, n_new)
+    _kv_call(cache, stream, lambda s: _lib.veda_kv_attn(
+        cache.ref, qp, qs, heads, n, nn, int(pending), int(causal), int(window), int(sinks), float(scale), op, os_,
+        _ptr(lse), _ptr(weight), float(decay), _ptr(ws), s))
+
+
+def veda_kv_evict(cache: KVCache, keep: Sequence[int], sink: int, recent: int, out: Optional[KVCache] = None,
+                  stream=None):
+    """Drop each head's least attended tiles, down to keep[h] (one per K/V
+    head), in place or into `out`, whose arrays of tiles are others."""
+    if len(keep) != cache.heads_kv:
+        raise ValueError(f"keep must have {cache.heads_kv} entries, not {len(keep)}")
+    if out is not None and out.device != cache.device:
+        raise ValueError(f"out is on {out.device}, the cache on {cache.device}")
+    _kv_call(cache, stream, lambda s: _lib.veda_kv_evict(cache.ref, _host_i32(keep), int(sink), int(recent),
+                                                         None if out is None else out.ref, s))
+
+
+def veda_kv_check_status(cache: KVCache, stream=None):
+    _kv_call(cache, stream, lambda s: _lib.veda_kv_check_status(cache.ref, s))
 
 
 def library_path() -> str:

@@ -6,6 +6,7 @@
 #include <cstring>
 #include <string>
 
+#include "kv_internal.cuh"
 #include "veda_internal.cuh"
 
 namespace {
@@ -93,6 +94,75 @@ int check_ptr(const void* p, const char* name) {
     int _rc = (expr);           \
     if (_rc != VEDA_OK) return _rc; \
   } while (0)
+
+// Fills `g` from the cache and validates its geometry and pointers.
+int build_kv(const veda_kv_cache* C, veda::KvGeom* g, const char* what) {
+  if (!C) return fail(VEDA_ERR_INVALID_ARG, "%s is NULL", what);
+  if (C->B < 1 || C->B > 65535) return fail(VEDA_ERR_INVALID_ARG, "B=%d outside [1, 65535]", C->B);
+  if (C->heads_kv < 1 || C->heads_kv > VEDA_MAX_HEADS)
+    return fail(VEDA_ERR_INVALID_ARG, "heads_kv=%d outside [1, %d]", C->heads_kv, VEDA_MAX_HEADS);
+  if (C->d != 64 && C->d != 128) return fail(VEDA_ERR_UNSUPPORTED, "d=%d: only 64 and 128 are built", C->d);
+  if (C->tile != 64 && C->tile != 128)
+    return fail(VEDA_ERR_UNSUPPORTED, "tile=%d: only 64 and 128 are built", C->tile);
+  if (C->nb_cap < 1) return fail(VEDA_ERR_INVALID_ARG, "nb_cap=%d must be >= 1", C->nb_cap);
+  if (C->nb_cap > VEDA_KV_MAX_NB)
+    return fail(VEDA_ERR_UNSUPPORTED, "nb_cap=%d exceeds %d", C->nb_cap, VEDA_KV_MAX_NB);
+  if (C->n_slots < 1 || (long long)C->n_slots * C->tile > 0x7fffffffll)
+    return fail(VEDA_ERR_INVALID_ARG, "n_slots=%d outside [1, 2^31 / tile)", C->n_slots);
+  VEDA_TRY(check_ptr(C->k8, "k8"));
+  VEDA_TRY(check_ptr(C->v8, "v8"));
+  VEDA_TRY(check_ptr(C->table, "table"));
+  VEDA_TRY(check_ptr(C->pos, "pos"));
+  VEDA_TRY(check_ptr(C->k_scale, "k_scale"));
+  VEDA_TRY(check_ptr(C->v_scale, "v_scale"));
+  VEDA_TRY(check_ptr(C->len, "len"));
+  VEDA_TRY(check_ptr(C->next_pos, "next_pos"));
+  if (C->weight) VEDA_TRY(check_ptr(C->weight, "weight"));
+  g->B = C->B;
+  g->hkv = C->heads_kv;
+  g->d = C->d;
+  g->tile = C->tile;
+  g->n_slots = C->n_slots;
+  g->nb_cap = C->nb_cap;
+  g->k8 = static_cast<uint8_t*>(C->k8);
+  g->v8 = static_cast<uint8_t*>(C->v8);
+  g->table = C->table;
+  g->pos = C->pos;
+  g->k_scale = C->k_scale;
+  g->v_scale = C->v_scale;
+  g->weight = C->weight;
+  g->len = C->len;
+  g->next_pos = C->next_pos;
+  g->dev_status = C->dev_status;
+  return VEDA_OK;
+}
+
+int check_rows(int n, const char* name) {
+  if (n < 0) return fail(VEDA_ERR_INVALID_ARG, "%s=%d is negative", name, n);
+  if (n > (1 << 22)) return fail(VEDA_ERR_UNSUPPORTED, "%s=%d exceeds %d", name, n, 1 << 22);
+  return VEDA_OK;
+}
+
+// Strides of a [B, n, heads, d] tensor (NULL: contiguous).
+int rows_strides(const int64_t* st, int n, int heads, int d, const char* name, int64_t out[3]) {
+  out[0] = st ? st[0] : (int64_t)n * heads * d;
+  out[1] = st ? st[1] : (int64_t)heads * d;
+  out[2] = st ? st[2] : d;
+  for (int i = 0; i < 3; ++i)
+    if (out[i] % 8) return fail(VEDA_ERR_INVALID_ARG, "%s: strides must be multiples of 8 elements", name);
+  return VEDA_OK;
+}
+
+int kv_rows(const void* p, const int64_t* st, int n, int heads, int d, const char* name, veda::KvRows* out) {
+  VEDA_TRY(check_ptr(p, name));
+  int64_t s[3];
+  VEDA_TRY(rows_strides(st, n, heads, d, name, s));
+  out->p = static_cast<const __nv_bfloat16*>(p);
+  out->sb = s[0];
+  out->sn = s[1];
+  out->sh = s[2];
+  return VEDA_OK;
+}
 
 int after_launch(cudaError_t e, const char* where) {
   if (e != cudaSuccess) return cuda_fail(e, where);
@@ -562,6 +632,114 @@ int veda_check_status(const veda_layer* L, cudaStream_t stream) {
   }
   g_last_error.clear();
   return VEDA_OK;
+}
+
+int veda_kv_append(const veda_kv_cache* C, const void* k, const int64_t* k_strides, const void* v,
+                   const int64_t* v_strides, int32_t n, const int32_t* n_new, cudaStream_t stream) {
+  veda::KvGeom g;
+  VEDA_TRY(build_kv(C, &g, "cache"));
+  VEDA_TRY(check_rows(n, "n"));
+  if (n == 0) return after_launch(cudaSuccess, "");
+  veda::KvRows kr, vr;
+  VEDA_TRY(kv_rows(k, k_strides, n, g.hkv, g.d, "k", &kr));
+  VEDA_TRY(kv_rows(v, v_strides, n, g.hkv, g.d, "v", &vr));
+  return after_launch(veda::launch_kv_append(g, kr, vr, n, n_new, stream), "veda_kv_append");
+}
+
+int veda_kv_advance(const veda_kv_cache* C, int32_t n, const int32_t* n_new, cudaStream_t stream) {
+  veda::KvGeom g;
+  VEDA_TRY(build_kv(C, &g, "cache"));
+  VEDA_TRY(check_rows(n, "n"));
+  if (n == 0) return after_launch(cudaSuccess, "");
+  return after_launch(veda::launch_kv_advance(g, n, n_new, stream), "veda_kv_advance");
+}
+
+// heads and n_q of an attention call, without its tensors.
+static int check_kv_heads(const veda::KvGeom& g, int heads, int n_q) {
+  if (heads < 1 || heads > 4096 || heads % g.hkv)
+    return fail(VEDA_ERR_INVALID_ARG, "heads=%d must be a multiple of heads_kv=%d in [1, 4096]", heads, g.hkv);
+  return check_rows(n_q, "n_q");
+}
+
+size_t veda_kv_attn_ws_bytes(const veda_kv_cache* C, int32_t heads, int32_t n_q, int32_t with_weight) {
+  veda::KvGeom g;
+  if (build_kv(C, &g, "cache") != VEDA_OK || check_kv_heads(g, heads, n_q) != VEDA_OK || n_q == 0) return 0;
+  return veda::kv_attn_ws_bytes(g, heads, n_q, with_weight != 0);
+}
+
+int veda_kv_attn(const veda_kv_cache* C, const void* q, const int64_t* q_strides, int32_t heads, int32_t n_q,
+                 const int32_t* n_new, int32_t pending, int32_t causal, int32_t window, int32_t sinks, float scale,
+                 void* o, const int64_t* o_strides, float* lse, float* weight, float decay, void* ws,
+                 cudaStream_t stream) {
+  veda::KvGeom g;
+  VEDA_TRY(build_kv(C, &g, "cache"));
+  VEDA_TRY(check_kv_heads(g, heads, n_q));
+  if (window < 0 || sinks < 0) return fail(VEDA_ERR_INVALID_ARG, "window=%d and sinks=%d must be >= 0", window, sinks);
+  if (n_q == 0) return after_launch(cudaSuccess, "");
+  veda::KvAttnParams p = {};
+  VEDA_TRY(kv_rows(q, q_strides, n_q, heads, g.d, "q", &p.q));
+  VEDA_TRY(check_ptr(o, "o"));
+  int64_t os[3];
+  VEDA_TRY(rows_strides(o_strides, n_q, heads, g.d, "o", os));
+  if ((os[0] == 0 && g.B > 1) || (os[1] == 0 && n_q > 1) || (os[2] == 0 && heads > 1))
+    return fail(VEDA_ERR_INVALID_ARG, "o: rows overlap (a stride is 0)");
+  if (lse) VEDA_TRY(check_ptr(lse, "lse"));
+  if (weight) VEDA_TRY(check_ptr(weight, "weight"));
+  VEDA_TRY(check_ptr(ws, "ws"));
+  p.o = static_cast<__nv_bfloat16*>(o);
+  p.o_sb = os[0];
+  p.o_sn = os[1];
+  p.o_sh = os[2];
+  p.heads = heads;
+  p.group = heads / g.hkv;
+  p.n_q = n_q;
+  p.n_new = n_new;
+  p.pending = pending != 0;
+  p.causal = causal != 0;
+  p.window = window;
+  p.sinks = sinks;
+  p.scale_log2 = scale * 1.4426950408889634f;
+  p.lse = lse;
+  p.weight = weight;
+  p.decay = decay;
+  return after_launch(veda::launch_kv_attn(g, p, ws, stream), "veda_kv_attn");
+}
+
+int veda_kv_evict(const veda_kv_cache* C, const int32_t* keep, int32_t sink, int32_t recent,
+                  const veda_kv_cache* out, cudaStream_t stream) {
+  veda::KvGeom g, t;
+  VEDA_TRY(build_kv(C, &g, "cache"));
+  if (!C->weight) return fail(VEDA_ERR_INVALID_ARG, "weight is NULL");
+  if (!keep) return fail(VEDA_ERR_INVALID_ARG, "keep is NULL");
+  if (sink < 0 || recent < 1)
+    return fail(VEDA_ERR_INVALID_ARG, "sink=%d must be >= 0 and recent=%d >= 1", sink, recent);
+  for (int h = 0; h < g.hkv; ++h)
+    if (keep[h] < (long long)sink + recent)
+      return fail(VEDA_ERR_INVALID_ARG, "keep[%d]=%d is below sink + recent = %lld", h, keep[h],
+                  (long long)sink + recent);
+  t = g;
+  if (out) {
+    VEDA_TRY(build_kv(out, &t, "out"));
+    if (t.B != g.B || t.hkv != g.hkv || t.d != g.d || t.tile != g.tile || t.nb_cap != g.nb_cap)
+      return fail(VEDA_ERR_INVALID_ARG, "out has another geometry than the cache");
+    if (!t.weight) return fail(VEDA_ERR_INVALID_ARG, "out: weight is NULL");
+    const void* a[7] = {g.table, g.pos, g.k_scale, g.v_scale, g.weight, g.len, g.next_pos};
+    const void* b[7] = {t.table, t.pos, t.k_scale, t.v_scale, t.weight, t.len, t.next_pos};
+    int shared = 0;
+    for (const void* x : a)
+      for (const void* y : b) shared += x == y;
+    bool same = true;
+    for (int i = 0; i < 7; ++i) same = same && a[i] == b[i];
+    if (shared && !same) return fail(VEDA_ERR_INVALID_ARG, "out shares some of the cache's arrays");
+  }
+  return after_launch(veda::launch_kv_evict(g, keep, sink, recent, t, stream), "veda_kv_evict");
+}
+
+int veda_kv_check_status(const veda_kv_cache* C, cudaStream_t stream) {
+  if (!C || !C->dev_status) return fail(VEDA_ERR_INVALID_ARG, "cache or dev_status is NULL");
+  veda_layer L = {};
+  L.dev_status = C->dev_status;
+  return veda_check_status(&L, stream);
 }
 
 }  // extern "C"

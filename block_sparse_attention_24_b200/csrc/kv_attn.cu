@@ -1,0 +1,452 @@
+// Attention over the 8-bit K/V tile cache, for few query rows.
+//
+// Row r of a K/V head is query token r / group, query head h*group + r % group.
+// With c the codes, s the tile scales and x_ij = scale*log2(e) * (q_i . ck_j)
+// * sk + log2(sv):
+//   P_ij = 2^(x_ij - M_i + OFF),  O_i = sum_j P_ij cv_j / sum_j P_ij / sv.
+// The V scale is part of the exponent, so P V runs on the bare codes and tiles
+// of any scale add up in one accumulator; dividing P by sv again for the sum is
+// exact for powers of two. M is a reference, not the maximum: it moves only
+// when some x passes it by MARGIN, so that P stays within 2^(MARGIN + OFF) and
+// fp16 (which has 11 bits of significand against bf16's 8, and is what an e4m3
+// pair converts to in one instruction) holds it. OFF keeps what lies 2^-31
+// below the reference out of fp16's zero: even a million such keys add less
+// than a part in a thousand. Sums, references and O are fp32.
+#include "kv_internal.cuh"
+
+namespace veda {
+namespace {
+
+constexpr int ROWS = 16;    // query rows per CTA (the M of one mma)
+constexpr int PIECE = 32;   // keys a warp takes at a time
+constexpr int WARPS = 4;
+constexpr float OFF = 7.f, MARGIN = 8.f;
+constexpr float LN2 = 0.69314718055994531f;
+
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void ldsm4_t(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+// two f16 pairs from four e4m3 codes
+__device__ __forceinline__ void codes_f16(uint32_t c, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+      : "=r"(lo), "=r"(hi) : "r"(c));
+}
+__device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+               : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+               : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// 16-byte chunk `ch` of row r of a piece in shared memory: chunks are permuted
+// inside each 128 bytes so that eight rows' chunks fall into different banks.
+template <int D>
+__device__ __forceinline__ int swz(int r, int ch) {
+  return D == 128 ? r * 128 + ((ch ^ (r & 7)) << 4) : r * 64 + ((ch ^ ((r >> 1) & 3)) << 4);
+}
+
+// Simple form: each warp copies its piece of K and V through registers into
+// its own shared memory, then computes; nothing is loaded ahead.
+template <int D>
+__global__ void __launch_bounds__(WARPS * 32)
+    kv_attn_rows_kernel(const KvGeom g, const KvAttnParams p) {
+  constexpr int KS = D / 16;  // 16-wide steps over the head dimension
+  __shared__ __align__(128) uint8_t buf[WARPS][2][PIECE * D];
+  __shared__ float sm_m[WARPS][ROWS], sm_l[WARPS][ROWS];
+  __shared__ int sm_cnt[3];
+  const int mt = blockIdx.x % p.row_tiles, sp = blockIdx.x / p.row_tiles, h = blockIdx.y, b = blockIdx.z;
+  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, gr = lane >> 2, c4 = lane & 3;
+  int n_b, held, total;
+  if (!kv_counts(g, b, h, p.n_q, p.n_new, p.pending, n_b, held, total)) return;
+  const int rows = n_b * p.group;
+  if (mt * ROWS >= rows) return;
+  const int bh = b * g.hkv + h;
+  const long long trow = (long long)bh * g.nb_cap;
+  const int t0 = g.next_pos[b];
+  const int t_lo = t0 + mt * ROWS / p.group, t_hi = t0 + (min(rows, mt * ROWS + ROWS) - 1) / p.group;
+
+  // the tiles this CTA's queries see: [0, n_first) and [from, upto) of the table
+  const int nb = (total + g.tile - 1) / g.tile;
+  int n_first = 0, from = 0, upto = nb;
+  if (p.window > 0 || p.causal) {
+    if (tid < 3) sm_cnt[tid] = 0;
+    __syncthreads();
+    int a = 0, f = 0, u = 0;
+    for (int i = tid; i < nb; i += WARPS * 32) {
+      const int ps = g.pos[trow + i];
+      const bool ahead = p.causal && ps > t_hi;
+      u += !ahead;
+      if (p.window > 0 && !ahead) {
+        a += ps < p.sinks;
+        f += (long long)ps + g.tile - 1 <= (long long)t_lo - p.window;
+      }
+    }
+    a = __reduce_add_sync(0xffffffffu, a);
+    f = __reduce_add_sync(0xffffffffu, f);
+    u = __reduce_add_sync(0xffffffffu, u);
+    if (lane == 0) {
+      atomicAdd(&sm_cnt[0], a);
+      atomicAdd(&sm_cnt[1], f);
+      atomicAdd(&sm_cnt[2], u);
+    }
+    __syncthreads();
+    upto = sm_cnt[2];
+    from = sm_cnt[1];
+    n_first = min(sm_cnt[0], from);
+  }
+  const int ppt = g.tile / PIECE;
+  const int pieces = (n_first + upto - from) * ppt;
+  const int per = (pieces + p.splits - 1) / p.splits;
+  const int p_lo = sp * per, p_hi = min(pieces, p_lo + per);
+
+  // Q as fp16 fragments, each row times a power of two that puts its largest
+  // value into [2^13, 2^14): bf16's range fits, and its 8 bits are kept down
+  // to 2^-37 of the row's largest
+  const int r0 = mt * ROWS + gr, r1 = r0 + 8;
+  uint32_t qa[KS][4];
+  float qs[2];
+  int tq[2];
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    const int r = e ? r1 : r0;
+    tq[e] = t0 + r / p.group;
+    uint2 w[KS];
+    uint32_t top = 0;
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) {
+      w[ks] = make_uint2(0, 0);
+      if (r < rows)
+        w[ks] = *reinterpret_cast<const uint2*>(p.q.p + b * p.q.sb + (long long)(r / p.group) * p.q.sn +
+                                                (long long)(h * p.group + r % p.group) * p.q.sh + ks * 16 + c4 * 4);
+      top = max(max(top, max((w[ks].x << 16) & 0x7fffffffu, w[ks].x & 0x7fff0000u)),
+                max((w[ks].y << 16) & 0x7fffffffu, w[ks].y & 0x7fff0000u));
+    }
+    top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+    top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+    // exponent field of the multiplier: 127 + 13 - (exponent of the largest); none for inf and NaN
+    int ex = 127 + 13 - ((int)(top >> 23) - 127);
+    if (top >= 0x7f800000u) ex = 127;
+    if (ex > 253) ex = 253;
+    const float mul = __uint_as_float((uint32_t)ex << 23);
+    qs[e] = __uint_as_float((uint32_t)(254 - ex) << 23) * p.scale_log2;
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) {
+      qa[ks][e] = pack_f16x2(__uint_as_float(w[ks].x << 16) * mul, __uint_as_float(w[ks].x & 0xffff0000u) * mul);
+      qa[ks][2 + e] = pack_f16x2(__uint_as_float(w[ks].y << 16) * mul, __uint_as_float(w[ks].y & 0xffff0000u) * mul);
+    }
+  }
+
+  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+  float o[KS][2][4];
+#pragma unroll
+  for (int c = 0; c < KS; ++c)
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+#pragma unroll
+      for (int x = 0; x < 4; ++x) o[c][e][x] = 0.f;
+  uint8_t* kb = buf[warp][0];
+  uint8_t* vb = buf[warp][1];
+  const uint32_t ka = smem_u32(kb), va = smem_u32(vb);
+
+  for (int pc = p_lo + warp; pc < p_hi; pc += WARPS) {
+    const int vt = pc / ppt, sub = pc - vt * ppt;
+    const int i = vt < n_first ? vt : vt - n_first + from;
+    const int key0 = i * g.tile + sub * PIECE;  // place among the head's tokens
+    if (key0 >= total) continue;
+    const int slot = g.table[trow + i];
+    if (slot < 0 || slot >= g.n_slots) {
+      if (lane == 0) {
+        report(g.dev_status, VEDA_ERR_BAD_INDEX);
+        if (p.lw)
+          for (int r = mt * ROWS; r < min(rows, mt * ROWS + ROWS); ++r)
+            p.lw[((long long)bh * p.n_q * p.group + r) * p.pieces_cap + i * ppt + sub] = -INFINITY;
+      }
+      continue;
+    }
+    const uint8_t* ks = g.k8 + ((long long)slot * g.tile + sub * PIECE) * D;
+    const uint8_t* vs = g.v8 + ((long long)slot * g.tile + sub * PIECE) * D;
+    const int left = total - key0;  // keys of the piece that exist
+    __syncwarp();
+#pragma unroll
+    for (int j = 0; j < PIECE * D / 16 / 32; ++j) {
+      const int x = j * 32 + lane, r = x / (D / 16), ch = x % (D / 16);
+      const uint4 z = make_uint4(0, 0, 0, 0);
+      // rows behind the last token are zeroes: their codes may be anything
+      *reinterpret_cast<uint4*>(kb + swz<D>(r, ch)) = r < left ? *reinterpret_cast<const uint4*>(ks + x * 16) : z;
+      *reinterpret_cast<uint4*>(vb + swz<D>(r, ch)) = r < left ? *reinterpret_cast<const uint4*>(vs + x * 16) : z;
+    }
+    __syncwarp();
+    float s[4][4];
+#pragma unroll
+    for (int nt = 0; nt < 4; ++nt) {
+#pragma unroll
+      for (int x = 0; x < 4; ++x) s[nt][x] = 0.f;
+#pragma unroll
+      for (int q4 = 0; q4 < KS / 4; ++q4) {
+        uint32_t f[4];
+        ldsm4(f, ka + swz<D>(nt * 8 + (lane & 7), q4 * 4 + (lane >> 3)));
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          uint32_t b0, b1;
+          codes_f16(f[x], b0, b1);
+          mma(s[nt], qa[q4 * 4 + x], b0, b1);
+        }
+      }
+    }
+    const float sk = g.k_scale[trow + i], sv = g.v_scale[trow + i];
+    const float ev = log2f(sv), rv = 1.0f / sv;
+    const int pos0 = g.pos[trow + i] + sub * PIECE;
+    const float co[2] = {qs[0] * sk, qs[1] * sk};
+    const bool whole = left >= PIECE && kv_seen(pos0 + PIECE - 1, t_lo, p.causal, 0, 0) &&
+                       (p.window <= 0 || pos0 + PIECE <= p.sinks || (long long)pos0 > (long long)t_hi - p.window);
+    bool over = false;
+#pragma unroll
+    for (int nt = 0; nt < 4; ++nt)
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        const int e = x >> 1, kk = nt * 8 + c4 * 2 + (x & 1);
+        float v = s[nt][x] * co[e] + ev;
+        if (!whole && !(kk < left && kv_seen(pos0 + kk, tq[e], p.causal, p.window, p.sinks))) v = -INFINITY;
+        s[nt][x] = v;
+        over |= v > m[e] + MARGIN;
+      }
+    if (__any_sync(0xffffffffu, over)) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float mx = m[e];
+#pragma unroll
+        for (int nt = 0; nt < 4; ++nt) mx = fmaxf(mx, fmaxf(s[nt][2 * e], s[nt][2 * e + 1]));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+        const float al = mx == m[e] ? 1.f : fast_exp2(m[e] - mx);
+        m[e] = mx;
+        l[e] *= al;
+#pragma unroll
+        for (int c = 0; c < KS; ++c)
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            o[c][y][2 * e] *= al;
+            o[c][y][2 * e + 1] *= al;
+          }
+      }
+    }
+    float ls[2] = {0.f, 0.f};
+    uint32_t pa[2][4];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const float base = OFF - (m[e] == -INFINITY ? 0.f : m[e]);
+#pragma unroll
+      for (int nt = 0; nt < 4; ++nt) {
+        const float x0 = fast_exp2(s[nt][2 * e] + base), x1 = fast_exp2(s[nt][2 * e + 1] + base);
+        ls[e] += x0 + x1;
+        pa[nt >> 1][(nt & 1) * 2 + e] = pack_f16x2(x0, x1);
+      }
+      // the sum without sv; NaN scales reach the rows that see the tile through P, and no other
+      l[e] += ls[e] == 0.f ? 0.f : ls[e] * rv;
+    }
+    if (p.lw) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float t = ls[e] + __shfl_xor_sync(0xffffffffu, ls[e], 1);
+        t += __shfl_xor_sync(0xffffffffu, t, 2);
+        const int r = e ? r1 : r0;
+        if (c4 == 0 && r < rows)
+          p.lw[((long long)bh * p.n_q * p.group + r) * p.pieces_cap + i * ppt + sub] =
+              t == 0.f ? -INFINITY : log2f(t) + (m[e] - OFF - ev);
+      }
+    }
+#pragma unroll
+    for (int ch = 0; ch < KS; ++ch) {
+      uint32_t f[4], ev_f[4], od_f[4];
+      ldsm4_t(f, va + swz<D>(lane, ch));
+#pragma unroll
+      for (int x = 0; x < 4; ++x) codes_f16(__byte_perm(f[x], 0, 0x3120), ev_f[x], od_f[x]);
+      mma(o[ch][0], pa[0], ev_f[0], ev_f[1]);
+      mma(o[ch][1], pa[0], od_f[0], od_f[1]);
+      mma(o[ch][0], pa[1], ev_f[2], ev_f[3]);
+      mma(o[ch][1], pa[1], od_f[2], od_f[3]);
+    }
+  }
+
+  // join the warps: references, then sums and O in warp order
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    l[e] += __shfl_xor_sync(0xffffffffu, l[e], 1);
+    l[e] += __shfl_xor_sync(0xffffffffu, l[e], 2);
+    if (c4 == 0) sm_m[warp][gr + 8 * e] = m[e];
+  }
+  __syncthreads();
+  float mx[2], f[2];
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    mx[e] = sm_m[0][gr + 8 * e];
+#pragma unroll
+    for (int w = 1; w < WARPS; ++w) mx[e] = fmaxf(mx[e], sm_m[w][gr + 8 * e]);
+    f[e] = m[e] == -INFINITY ? (l[e] == l[e] ? 0.f : 1.f) : fast_exp2(m[e] - mx[e]);
+    if (c4 == 0) sm_l[warp][gr + 8 * e] = l[e] * f[e];
+  }
+  __syncthreads();
+  float* acc = reinterpret_cast<float*>(buf);  // [ROWS][D]
+  for (int w = 0; w < WARPS; ++w) {
+    if (warp == w) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+#pragma unroll
+        for (int ch = 0; ch < KS; ++ch) {
+          float4* a = reinterpret_cast<float4*>(acc + (gr + 8 * e) * D + ch * 16 + c4 * 4);
+          float4 v = w ? *a : make_float4(0.f, 0.f, 0.f, 0.f);
+          v.x += o[ch][0][2 * e] * f[e];
+          v.y += o[ch][1][2 * e] * f[e];
+          v.z += o[ch][0][2 * e + 1] * f[e];
+          v.w += o[ch][1][2 * e + 1] * f[e];
+          *a = v;
+        }
+    }
+    __syncthreads();
+  }
+  const long long prow = (((long long)bh * p.splits + sp) * p.row_tiles + mt) * ROWS;
+  for (int x = tid; x < ROWS * D / 4; x += WARPS * 32) {
+    const int r = x / (D / 4), c = x % (D / 4);
+    *reinterpret_cast<float4*>(p.part_o + (prow + r) * D + c * 4) = *reinterpret_cast<float4*>(acc + r * D + c * 4);
+  }
+  if (tid < ROWS) {
+    float lsum = 0.f, mm = sm_m[0][tid];
+    for (int w = 0; w < WARPS; ++w) {
+      lsum += sm_l[w][tid];
+      mm = fmaxf(mm, sm_m[w][tid]);
+    }
+    p.part_ml[prow + tid] = make_float2(mm, lsum);
+  }
+}
+
+// Joins the splits of a row: a warp per row.
+template <int D>
+__global__ void __launch_bounds__(128) kv_join_kernel(const KvGeom g, const KvAttnParams p) {
+  const int lane = threadIdx.x % 32, h = blockIdx.y, b = blockIdx.z;
+  const int r = blockIdx.x * 4 + threadIdx.x / 32;
+  int n_b, held, total;
+  if (!kv_counts(g, b, h, p.n_q, p.n_new, p.pending, n_b, held, total)) return;
+  if (r >= n_b * p.group) return;
+  const int bh = b * g.hkv + h;
+  const long long rows = (long long)p.row_tiles * ROWS;
+  const float2* ml = p.part_ml + (long long)bh * p.splits * rows + r;
+  float m = -INFINITY;
+  for (int s = 0; s < p.splits; ++s) m = fmaxf(m, ml[s * rows].x);
+  float l = 0.f, o[D / 32];
+#pragma unroll
+  for (int e = 0; e < D / 32; ++e) o[e] = 0.f;
+  for (int s = 0; s < p.splits; ++s) {
+    const float2 x = ml[s * rows];
+    const float f = x.x == -INFINITY ? (x.y == x.y ? 0.f : 1.f) : fast_exp2(x.x - m);
+    l += x.y * f;
+    const float* src = p.part_o + (((long long)bh * p.splits + s) * rows + r) * D + lane * (D / 32);
+#pragma unroll
+    for (int e = 0; e < D / 32; ++e) o[e] += src[e] * f;
+  }
+  const bool none = l == 0.f;
+  const float inv = none ? 0.f : 1.0f / l;
+  const int i = r / p.group, qh = h * p.group + r % p.group;
+  __nv_bfloat16* dst = p.o + b * p.o_sb + (long long)i * p.o_sn + (long long)qh * p.o_sh + lane * (D / 32);
+  uint32_t w[D / 64];
+#pragma unroll
+  for (int e = 0; e < D / 64; ++e) w[e] = pack_bf16x2_rn(o[2 * e] * inv, o[2 * e + 1] * inv);
+#pragma unroll
+  for (int e = 0; e < D / 64; ++e) reinterpret_cast<uint32_t*>(dst)[e] = w[e];
+  if (lane == 0) {
+    const float l2 = none ? -INFINITY : log2f(l) + (m - OFF);
+    if (p.lse) p.lse[((long long)b * p.heads + qh) * p.n_q + i] = l2 * LN2;
+    if (p.lse2) p.lse2[(long long)bh * p.n_q * p.group + r] = l2;
+  }
+}
+
+// weight[tile] = decay * weight[tile] + sum over rows and the tile's pieces of
+// 2^(lw - lse2): a warp per tile, the rows in a fixed order over its lanes.
+__global__ void __launch_bounds__(128) kv_weight_kernel(const KvGeom g, const KvAttnParams p, const int piece,
+                                                        const int rows_per_tile) {
+  const int lane = threadIdx.x % 32, h = blockIdx.y, b = blockIdx.z;
+  const int i = blockIdx.x * 4 + threadIdx.x / 32;
+  int n_b, held, total;
+  if (!kv_counts(g, b, h, p.n_q, p.n_new, p.pending, n_b, held, total)) return;
+  const int nb = (total + g.tile - 1) / g.tile;
+  if (i >= nb || n_b == 0) return;
+  const int bh = b * g.hkv + h, ppt = g.tile / piece;
+  const long long entry = (long long)bh * g.nb_cap + i;
+  const int rows = n_b * p.group, t0 = g.next_pos[b], ps = g.pos[entry];
+  float w = 0.f;
+  for (int r = lane; r < rows; r += 32) {
+    // only tiles that the row's whole CTA could see were visited
+    const int m0 = r / rows_per_tile * rows_per_tile, m1 = min(rows, m0 + rows_per_tile) - 1;
+    const bool seen = kv_tile_seen(ps, g.tile, t0 + m0 / p.group, t0 + m1 / p.group, p.causal, p.window, p.sinks);
+    const float z = p.lse2[(long long)bh * p.n_q * p.group + r];
+    if (!seen || z == -INFINITY) continue;
+    const float* x = p.lw + ((long long)bh * p.n_q * p.group + r) * p.pieces_cap + (long long)i * ppt;
+    for (int k = 0; k < ppt && i * g.tile + k * piece < total; ++k) w += fast_exp2(x[k] - z);
+  }
+#pragma unroll
+  for (int d = 16; d; d >>= 1) w += __shfl_xor_sync(0xffffffffu, w, d);
+  if (lane == 0) p.weight[entry] = p.decay == 0.f ? w : p.decay * p.weight[entry] + w;
+}
+
+}  // namespace
+
+size_t kv_attn_plan(const KvGeom& g, KvAttnParams& p, bool weights, uint8_t* ws) {
+  const long long rows = (long long)p.n_q * p.group;
+  p.row_tiles = (int)((rows + ROWS - 1) / ROWS);
+  const long long ctas = (long long)g.B * g.hkv * p.row_tiles;
+  const long long want = (148 * 6 + ctas - 1) / ctas;
+  const long long most = ((long long)g.nb_cap * g.tile / PIECE + WARPS - 1) / WARPS;
+  p.splits = (int)(want < most ? want : most);
+  if (p.splits < 1) p.splits = 1;
+  p.pieces_cap = g.nb_cap * (g.tile / PIECE);
+  size_t off = 0;
+  auto take = [&](size_t bytes) {
+    uint8_t* at = ws ? ws + off : nullptr;
+    off += (bytes + 255) / 256 * 256;
+    return at;
+  };
+  const size_t prows = (size_t)g.B * g.hkv * p.splits * p.row_tiles * ROWS;
+  p.part_o = reinterpret_cast<float*>(take(prows * g.d * 4));
+  p.part_ml = reinterpret_cast<float2*>(take(prows * 8));
+  p.lse2 = nullptr;
+  p.lw = nullptr;
+  if (weights) {
+    p.lse2 = reinterpret_cast<float*>(take((size_t)g.B * g.hkv * rows * 4));
+    p.lw = reinterpret_cast<float*>(take((size_t)g.B * g.hkv * rows * p.pieces_cap * 4));
+  }
+  return off;
+}
+
+size_t kv_attn_ws_bytes(const KvGeom& g, int heads, int n_q, bool weights) {
+  KvAttnParams p = {};
+  p.heads = heads;
+  p.group = heads / g.hkv;
+  p.n_q = n_q;
+  return kv_attn_plan(g, p, weights, nullptr);
+}
+
+cudaError_t launch_kv_attn(const KvGeom& g, KvAttnParams p, void* ws, cudaStream_t s) {
+  kv_attn_plan(g, p, p.weight != nullptr, static_cast<uint8_t*>(ws));
+  const dim3 grid(p.row_tiles * p.splits, g.hkv, g.B);
+  if (g.d == 128) kv_attn_rows_kernel<128><<<grid, WARPS * 32, 0, s>>>(g, p);
+  else kv_attn_rows_kernel<64><<<grid, WARPS * 32, 0, s>>>(g, p);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  const dim3 jg((p.n_q * p.group + 3) / 4, g.hkv, g.B);
+  if (g.d == 128) kv_join_kernel<128><<<jg, 128, 0, s>>>(g, p);
+  else kv_join_kernel<64><<<jg, 128, 0, s>>>(g, p);
+  e = cudaGetLastError();
+  if (e != cudaSuccess || !p.weight) return e;
+  kv_weight_kernel<<<dim3((g.nb_cap + 3) / 4, g.hkv, g.B), 128, 0, s>>>(g, p, PIECE, ROWS);
+  return cudaGetLastError();
+}
+
+}  // namespace veda

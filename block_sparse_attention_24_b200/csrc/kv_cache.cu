@@ -1,0 +1,309 @@
+// The 8-bit K/V tile cache: writing new tokens into it (append), taking them
+// in (advance) and dropping its least used tiles (evict).
+//
+// A cached value is code * scale with an e4m3 code and one scale per (sequence,
+// K/V head, tile), separate for K and V. The scale is a power of two, so that
+// dividing by it, changing it later and folding it into an exponent are exact;
+// a floating-point code loses no precision by that, only range, of which 448
+// to 2^-9 leaves plenty.
+#include "kv_internal.cuh"
+
+namespace veda {
+namespace {
+
+constexpr int APPEND_THREADS = 256;
+constexpr int EVICT_THREADS = 256;
+
+// The least power of two s with 448 s >= a (a >= 0), at least 2^-40; NaN
+// where a is not finite or s would pass 2^80. 448 = 1.75 * 2^8, so the
+// exponent is that of a, less 8, and one more where a's significand passes
+// 1.75.
+__device__ __forceinline__ float scale_of(float a) {
+  const uint32_t u = __float_as_uint(a);
+  int e = (int)(u >> 23) - 127 - 8 + ((u & 0x7fffffu) > 0x600000u ? 1 : 0);
+  if (e < -40) e = -40;
+  if (u >= 0x7f800000u || e > 80) return __uint_as_float(0x7fffffffu);
+  return __uint_as_float((uint32_t)(e + 127) << 23);
+}
+
+__device__ __forceinline__ uint32_t pack_e4m3x4(float a, float b, float c, float d) {
+  uint16_t lo, hi;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(b), "f"(a));
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(d), "f"(c));
+  return (uint32_t)lo | ((uint32_t)hi << 16);
+}
+
+__device__ __forceinline__ float2 unpack_e4m3x2(uint16_t c) {
+  uint32_t h;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(c));
+  return __half22float2(*reinterpret_cast<__half2*>(&h));
+}
+
+__device__ __forceinline__ float bf_lo(uint32_t u) { return __uint_as_float(u << 16); }
+__device__ __forceinline__ float bf_hi(uint32_t u) { return __uint_as_float(u & 0xffff0000u); }
+
+// One tile of K or of V of one head: scale' = max(old scale, the new tokens'),
+// old codes moved to it (rounded once more where it grew), new ones quantised,
+// the rows behind the last token zeroed. The tile's bf16 rows are held in
+// registers between the maximum and the rounding, so they are read once:
+// 2 bytes in and 1 out per value.
+template <int D>
+__global__ void __launch_bounds__(APPEND_THREADS)
+    kv_append_kernel(const KvGeom g, const KvRows kr, const KvRows vr, const int n, const int32_t* n_new) {
+  constexpr int VPR = D / 8;                           // 8-value vectors per row
+  constexpr int PT = 128 * VPR / APPEND_THREADS;       // vectors per thread at tile 128
+  const int h = blockIdx.y >> 1, is_v = blockIdx.y & 1, b = blockIdx.z;
+  int n_b, held, total;
+  if (!kv_counts(g, b, h, n, n_new, true, n_b, held, total)) return;
+  const int i = held / g.tile + blockIdx.x;            // the tile's place in the table
+  const int row0 = i * g.tile - held;                  // new token in its first row (negative: that row is older)
+  if (n_b == 0 || row0 >= n_b) return;
+  const long long entry = ((long long)b * g.hkv + h) * g.nb_cap + i;
+  const int slot = g.table[entry];
+  if (slot < 0 || slot >= g.n_slots) {
+    if (threadIdx.x == 0) report(g.dev_status, VEDA_ERR_BAD_INDEX);
+    return;
+  }
+  uint8_t* codes = (is_v ? g.v8 : g.k8) + (long long)slot * g.tile * D;
+  float* scale = (is_v ? g.v_scale : g.k_scale) + entry;
+  const KvRows& x = is_v ? vr : kr;
+  const __nv_bfloat16* src = x.p + b * x.sb + h * x.sh;
+  const bool fresh = row0 >= 0;
+  const float s_old = fresh ? 0.f : *scale;
+
+  uint4 val[PT];
+  float amax = 0.f;
+#pragma unroll
+  for (int j = 0; j < PT; ++j) {
+    const int vec = threadIdx.x + j * APPEND_THREADS, r = vec / VPR, c = vec % VPR, t = row0 + r;
+    val[j] = make_uint4(0, 0, 0, 0);
+    if (r < g.tile && t >= 0 && t < n_b) val[j] = *reinterpret_cast<const uint4*>(src + (long long)t * x.sn + c * 8);
+  }
+  // the largest |x| by its bits: infinities and NaN come out above every finite value
+  uint32_t top = 0;
+#pragma unroll
+  for (int j = 0; j < PT; ++j) {
+    const uint32_t w[4] = {val[j].x, val[j].y, val[j].z, val[j].w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) top = max(top, max((w[e] << 16) & 0x7fffffffu, w[e] & 0x7fff0000u));
+  }
+  __shared__ uint32_t warp_top[APPEND_THREADS / 32];
+  top = __reduce_max_sync(0xffffffffu, top);
+  if (threadIdx.x % 32 == 0) warp_top[threadIdx.x / 32] = top;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < APPEND_THREADS / 32; ++w) top = max(top, warp_top[w]);
+  amax = __uint_as_float(top);
+  const float s_new = scale_of(amax);
+  const float s = fresh ? s_new : ((s_new != s_new || s_old != s_old) ? s_new + s_old : fmaxf(s_new, s_old));
+  const bool fine = s == s;
+  const float inv = fine ? 1.0f / s : 0.f;
+
+#pragma unroll
+  for (int j = 0; j < PT; ++j) {
+    const int vec = threadIdx.x + j * APPEND_THREADS, r = vec / VPR, c = vec % VPR, t = row0 + r;
+    if (r >= g.tile) continue;
+    uint2* dst = reinterpret_cast<uint2*>(codes + r * D + c * 8);
+    if (t >= 0) {
+      uint2 o = make_uint2(0, 0);
+      if (t < n_b && fine) {
+        o.x = pack_e4m3x4(bf_lo(val[j].x) * inv, bf_hi(val[j].x) * inv, bf_lo(val[j].y) * inv, bf_hi(val[j].y) * inv);
+        o.y = pack_e4m3x4(bf_lo(val[j].z) * inv, bf_hi(val[j].z) * inv, bf_lo(val[j].w) * inv, bf_hi(val[j].w) * inv);
+      }
+      *dst = o;
+    } else if (fine && s != s_old) {
+      const float f = s_old * inv;
+      const uint2 w = *dst;
+      const float2 a = unpack_e4m3x2((uint16_t)w.x), e = unpack_e4m3x2((uint16_t)(w.x >> 16));
+      const float2 p = unpack_e4m3x2((uint16_t)w.y), q = unpack_e4m3x2((uint16_t)(w.y >> 16));
+      *dst = make_uint2(pack_e4m3x4(a.x * f, a.y * f, e.x * f, e.y * f), pack_e4m3x4(p.x * f, p.y * f, q.x * f, q.y * f));
+    }
+  }
+  if (threadIdx.x == 0) {
+    *scale = s;
+    if (fresh && !is_v) {
+      g.pos[entry] = g.next_pos[b] + row0;
+      if (g.weight) g.weight[entry] = 0.f;
+    }
+  }
+}
+
+__global__ void kv_advance_kernel(const KvGeom g, const int n, const int32_t* n_new) {
+  const int i = blockIdx.x * blockDim.x + threadIdx.x;
+  if (i >= g.B * g.hkv) return;
+  const int b = i / g.hkv, h = i - b * g.hkv;
+  int n_b, held, total;
+  const bool ok = kv_counts(g, b, h, n, n_new, true, n_b, held, total);
+  if (ok) g.len[i] = total;
+  if (h == 0 && n_b >= 0 && n_b <= n) g.next_pos[b] += n_b;
+}
+
+struct KvKeep {
+  int32_t k[VEDA_MAX_HEADS];
+};
+
+// fp32 bits -> unsigned keys that rank as the values do; -0 as +0, NaN first.
+__device__ __forceinline__ uint32_t rank_key(float w) {
+  if (w != w) return 0xffffffffu;
+  const uint32_t u = __float_as_uint(w + 0.0f);
+  return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+}
+
+// Exclusive prefix of `flag` over the block, and its total.
+__device__ __forceinline__ int block_prefix(bool flag, int* warp_n, int& total) {
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const uint32_t m = __ballot_sync(0xffffffffu, flag);
+  __syncthreads();  // the last call's counts have been read
+  if (lane == 0) warp_n[warp] = __popc(m);
+  __syncthreads();
+  int before = 0;
+  total = 0;
+#pragma unroll
+  for (int w = 0; w < EVICT_THREADS / 32; ++w) {
+    const int c = warp_n[w];
+    before += w < warp ? c : 0;
+    total += c;
+  }
+  return before + __popc(m & ((1u << lane) - 1u));
+}
+
+// One (sequence, head): the row of the table is read whole into shared
+// memory, the weight of the last tile that stays is found by radix selection
+// (8 bits at a time), and the row is written back with the tiles that stay
+// first, in their order, then those that go, then the free ones. Nothing of
+// the codes moves. A few microseconds of latency, no bandwidth to speak of.
+__global__ void __launch_bounds__(EVICT_THREADS)
+    kv_evict_kernel(const KvGeom g, const KvGeom out, const KvKeep keeps, const int sink, const int recent) {
+  extern __shared__ uint32_t sm[];
+  uint32_t* f_table = sm;
+  uint32_t* f_pos = sm + g.nb_cap;
+  uint32_t* f_ks = sm + 2 * g.nb_cap;
+  uint32_t* f_vs = sm + 3 * g.nb_cap;
+  uint32_t* f_w = sm + 4 * g.nb_cap;
+  __shared__ int hist[256];
+  __shared__ int warp_n[EVICT_THREADS / 32];
+  __shared__ uint32_t sh_prefix;
+  __shared__ int sh_want;
+  const int h = blockIdx.x, b = blockIdx.y, tid = threadIdx.x;
+  const int bh = b * g.hkv + h;
+  const long long row = (long long)bh * g.nb_cap;
+  const int held = g.len[bh];
+  const bool bad = held < 0 || (long long)held > (long long)g.nb_cap * g.tile;
+  if (bad && tid == 0) report(g.dev_status, VEDA_ERR_BAD_INDEX);
+  const int nb = bad ? 0 : (int)(((long long)held + g.tile - 1) / g.tile);
+  const int keep = keeps.k[h];
+  const bool cut = nb > keep;
+  const bool same = out.table == g.table;
+  if (!cut && same) return;
+  for (int i = tid; i < g.nb_cap; i += EVICT_THREADS) {
+    f_table[i] = (uint32_t)g.table[row + i];
+    f_pos[i] = (uint32_t)g.pos[row + i];
+    f_ks[i] = __float_as_uint(g.k_scale[row + i]);
+    f_vs[i] = __float_as_uint(g.v_scale[row + i]);
+    f_w[i] = __float_as_uint(g.weight[row + i]);
+  }
+  __syncthreads();
+  auto put = [&](int i, int to) {
+    out.table[row + to] = (int32_t)f_table[i];
+    out.pos[row + to] = (int32_t)f_pos[i];
+    out.k_scale[row + to] = __uint_as_float(f_ks[i]);
+    out.v_scale[row + to] = __uint_as_float(f_vs[i]);
+    out.weight[row + to] = __uint_as_float(f_w[i]);
+  };
+  if (h == 0 && tid == 0 && !same) out.next_pos[b] = g.next_pos[b];
+  if (!cut) {
+    for (int i = tid; i < g.nb_cap; i += EVICT_THREADS) put(i, i);
+    if (tid == 0) out.len[bh] = held;
+    return;
+  }
+  // the key of the last tile that stays among [sink, nb - recent), and how
+  // many with exactly that key stay
+  const int lo = sink, hi = nb - recent;
+  int want = keep - sink - recent;
+  uint32_t prefix = 0;
+  if (want > 0) {
+    for (int shift = 24; shift >= 0; shift -= 8) {
+      for (int i = tid; i < 256; i += EVICT_THREADS) hist[i] = 0;
+      __syncthreads();
+      for (int i = lo + tid; i < hi; i += EVICT_THREADS) {
+        const uint32_t k = rank_key(__uint_as_float(f_w[i]));
+        if (shift == 24 || (k >> (shift + 8)) == (prefix >> (shift + 8))) atomicAdd(&hist[(k >> shift) & 255u], 1);
+      }
+      __syncthreads();
+      if (tid < 32) {  // bins from the top, eight per lane
+        int c[8], sum = 0;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) sum += c[e] = hist[255 - (tid * 8 + e)];
+        int incl = sum;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+          const int v = __shfl_up_sync(0xffffffffu, incl, d);
+          if (tid >= d) incl += v;
+        }
+        int above = incl - sum;
+        if (above < want && want <= incl) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            if (above < want && want <= above + c[e]) {
+              sh_prefix = prefix | ((uint32_t)(255 - (tid * 8 + e)) << shift);
+              sh_want = want - above;
+            }
+            above += c[e];
+          }
+        }
+      }
+      __syncthreads();
+      prefix = sh_prefix;
+      want = sh_want;
+      __syncthreads();
+    }
+  }
+  int stays = 0, goes = 0, ties = 0;
+  for (int base = 0; base < nb; base += EVICT_THREADS) {
+    const int i = base + tid;
+    const bool mid = i >= lo && i < hi, in = i < nb;
+    const uint32_t k = mid ? rank_key(__uint_as_float(f_w[i])) : 0;
+    const bool none = keep - sink - recent == 0;
+    const bool tie = mid && !none && k == prefix;
+    int n_tie, n_stay;
+    const int t = block_prefix(tie, warp_n, n_tie);
+    const bool stay = in && (!mid || (!none && (k > prefix || (tie && ties + t < want))));
+    const int r = block_prefix(stay, warp_n, n_stay);
+    if (in) put(i, stay ? stays + r : keep + goes + (tid - r));
+    ties += n_tie;
+    stays += n_stay;
+    goes += min(EVICT_THREADS, nb - base) - n_stay;
+  }
+  if (!same)
+    for (int i = nb + tid; i < g.nb_cap; i += EVICT_THREADS) put(i, i);
+  if (tid == 0) out.len[bh] = held - (nb - keep) * g.tile;
+}
+
+}  // namespace
+
+cudaError_t launch_kv_append(const KvGeom& g, const KvRows& k, const KvRows& v, int n, const int32_t* n_new,
+                             cudaStream_t s) {
+  const long long tiles = ((long long)n + g.tile - 2) / g.tile + 1;  // n tokens from any row of a tile on
+  const dim3 grid((unsigned)(tiles < g.nb_cap ? tiles : g.nb_cap), 2 * g.hkv, g.B);
+  if (g.d == 128) kv_append_kernel<128><<<grid, APPEND_THREADS, 0, s>>>(g, k, v, n, n_new);
+  else kv_append_kernel<64><<<grid, APPEND_THREADS, 0, s>>>(g, k, v, n, n_new);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_kv_advance(const KvGeom& g, int n, const int32_t* n_new, cudaStream_t s) {
+  kv_advance_kernel<<<(g.B * g.hkv + 127) / 128, 128, 0, s>>>(g, n, n_new);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_kv_evict(const KvGeom& g, const int32_t* keep, int sink, int recent, const KvGeom& out,
+                            cudaStream_t s) {
+  KvKeep keeps;
+  for (int h = 0; h < g.hkv; ++h) keeps.k[h] = keep[h];
+  const int smem = 5 * 4 * g.nb_cap;  // at most 160 KB
+  const cudaError_t e = cudaFuncSetAttribute(kv_evict_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  kv_evict_kernel<<<dim3(g.hkv, g.B), EVICT_THREADS, smem, s>>>(g, out, keeps, sink, recent);
+  return cudaGetLastError();
+}
+
+}  // namespace veda

@@ -1,0 +1,94 @@
+// Definitions shared by the kernels of the 8-bit K/V tile cache: its geometry
+// as the kernels take it, which tokens a call covers and which tiles a query
+// can see.
+#pragma once
+
+#include <cuda_fp16.h>
+
+#include "veda_internal.cuh"
+
+#define VEDA_KV_MAX_NB 8192  // table entries per (sequence, K/V head)
+
+namespace veda {
+
+struct KvGeom {
+  int32_t B, hkv, d, tile, n_slots, nb_cap;
+  uint8_t* k8;     // [n_slots, tile, d] e4m3
+  uint8_t* v8;
+  int32_t* table;  // [B, hkv, nb_cap]
+  int32_t* pos;
+  float* k_scale;
+  float* v_scale;
+  float* weight;
+  int32_t* len;       // [B, hkv]
+  int32_t* next_pos;  // [B]
+  int32_t* dev_status;
+};
+
+// bf16 rows [B, n, heads, d] with element strides (the last dimension is contiguous).
+struct KvRows {
+  const __nv_bfloat16* p;
+  int64_t sb, sn, sh;
+};
+
+struct KvAttnParams {
+  KvRows q;
+  __nv_bfloat16* o;
+  int64_t o_sb, o_sn, o_sh;
+  int32_t heads, group, n_q;
+  const int32_t* n_new;
+  int32_t pending, causal, window, sinks;
+  float scale_log2;
+  float* lse;     // [B, heads, n_q] natural log, or NULL
+  float* weight;  // [B, hkv, nb_cap] or NULL
+  float decay;
+  // workspace
+  int32_t splits, row_tiles, pieces_cap;
+  float* part_o;   // [B, hkv, splits, row_tiles * rows, d]
+  float2* part_ml; // [B, hkv, splits, row_tiles * rows]: reference (log2) and sum
+  float* lse2;     // [B, hkv, n_q * group] log2
+  float* lw;       // [B, hkv, n_q * group, pieces_cap] log2 of a piece's sum
+};
+
+// New tokens of sequence b (n_new == NULL: all n), and the tokens its head h
+// then holds; false, with VEDA_ERR_BAD_INDEX recorded, where the counts are
+// outside what the call or the cache can hold. Every kernel of a step decides
+// by this, so a head that is skipped is skipped by all of them.
+__device__ __forceinline__ bool kv_counts(const KvGeom& g, int b, int h, int n, const int32_t* n_new, bool pending,
+                                          int& n_b, int& held, int& total) {
+  n_b = n_new ? n_new[b] : n;
+  held = g.len[b * g.hkv + h];
+  const long long t = (long long)held + (pending ? n_b : 0);
+  total = (int)t;
+  if (n_b < 0 || n_b > n || held < 0 || t > (long long)g.nb_cap * g.tile) {
+    report(g.dev_status, VEDA_ERR_BAD_INDEX);
+    return false;
+  }
+  return true;
+}
+
+// Whether any query at a position in [t_lo, t_hi] sees any token of a tile
+// that starts at position p. Sums in 64 bits: positions may be near the ends
+// of the range.
+__device__ __forceinline__ bool kv_tile_seen(int p, int tile, int t_lo, int t_hi, int causal, int window, int sinks) {
+  if (causal && p > t_hi) return false;
+  return window <= 0 || p < sinks || (long long)p + tile - 1 > (long long)t_lo - window;
+}
+
+// Whether the query at position t sees the token at position p.
+__device__ __forceinline__ bool kv_seen(int p, int t, int causal, int window, int sinks) {
+  if (causal && p > t) return false;
+  return window <= 0 || p < sinks || (long long)p > (long long)t - window;
+}
+
+cudaError_t launch_kv_append(const KvGeom& g, const KvRows& k, const KvRows& v, int n, const int32_t* n_new,
+                             cudaStream_t s);
+cudaError_t launch_kv_advance(const KvGeom& g, int n, const int32_t* n_new, cudaStream_t s);
+cudaError_t launch_kv_evict(const KvGeom& g, const int32_t* keep, int sink, int recent, const KvGeom& out,
+                            cudaStream_t s);
+size_t kv_attn_ws_bytes(const KvGeom& g, int heads, int n_q, bool weights);
+cudaError_t launch_kv_attn(const KvGeom& g, KvAttnParams p, void* ws, cudaStream_t s);
+// workspace of the call, and its pointers and split into the parameters
+size_t kv_attn_plan(const KvGeom& g, KvAttnParams& p, bool weights, uint8_t* ws);
+
+}  // namespace veda

@@ -342,6 +342,114 @@ int veda_estimator_grad(const veda_layer* L, const float* dq, const float* dk,
  * output under one candidate tiling). Fixed-order reduction. */
 int veda_output_sq_error(const veda_layer* L, const void* a, const void* b, float* err, cudaStream_t stream);
 
+/* An 8-bit K/V tile cache for attention over a stream: chunk after chunk of
+ * video, or token after token. (The pages have no counterpart: their layer
+ * holds one whole clip in bf16. The tile stays the unit, as in 2.2 and 2.3:
+ * it has a scale, an entry in the table and an attention weight of its own.)
+ *   A cached value is code * scale: e4m3 codes in pools k8 and v8 [n_slots,
+ *   tile, d], of which table[b, h, i] names the slot of the i-th tile of
+ *   sequence b and K/V head h, and one positive fp32 scale per (b, h, tile)
+ *   for K and one for V. A scale that is NaN makes every value of its tile
+ *   NaN.
+ *   len[b, h]    tokens that the head holds: its first ceil(len / tile) table
+ *                entries, the last of them filled up to len
+ *   pos[b, h, i] position in the stream of a tile's first token; the tile's
+ *                others follow it. Ascending in i over the tiles in use.
+ *   next_pos[b]  position of the sequence's next token (len lags behind it
+ *                once tiles have been evicted)
+ *   weight       attention that the tile has received (veda_kv_attn); may be
+ *                NULL where it is neither taken nor used
+ * All pointers are DEVICE memory, 16-byte aligned, all arrays contiguous;
+ * nb_cap <= 8192, heads_kv <= 128, B <= 65535, positions below 2^31 - tile.
+ * A tile that append writes to has a slot of its own; tiles that are only
+ * read may share one. Calls on one cache are ordered by the caller (one
+ * stream, or events between streams).
+ *
+ * A step is append, attention, advance: the new tokens are pending (written
+ * behind the len tokens and seen by attention) until veda_kv_advance takes
+ * them in, so appending again replaces them, as when a chunk's K and V change
+ * from one denoising step to the next.
+ *
+ * n_new (may be NULL = n for all): DEVICE int32 [B], the number of rows of
+ * each sequence that are real in a padded batch, 0 <= n_new[b] <= n. A head
+ * whose counts are outside their range, or whose tiles cannot hold the new
+ * tokens, is left as it is by every call, and a table entry outside [0,
+ * n_slots) is treated as an absent tile; both record VEDA_ERR_BAD_INDEX in
+ * dev_status.
+ *
+ * Strides (may be NULL = contiguous): HOST int64 [3], elements between batch
+ * elements, tokens and heads of a [B, n, heads, d] bf16 tensor; multiples of
+ * 8, the last dimension contiguous. */
+typedef struct {
+  int32_t B, heads_kv, d, tile; /* d and tile: 64 or 128 */
+  int32_t n_slots, nb_cap;      /* pool size; table entries per (b, head) */
+  void *k8, *v8;
+  int32_t *table, *pos;          /* [B, heads_kv, nb_cap] */
+  float *k_scale, *v_scale, *weight;
+  int32_t* len;                  /* [B, heads_kv] */
+  int32_t* next_pos;             /* [B] */
+  int32_t* dev_status;           /* as in veda_layer */
+} veda_kv_cache;
+
+/* Writes n new tokens' K and V (bf16 [B, n, heads_kv, d]) behind the tokens
+ * held, as pending ones. A tile's scale is the least power of two s >= 2^-40
+ * with 448 s >= the largest |x| of the tokens it gets, and NaN where one is
+ * not finite or above 448 * 2^80; codes are x / s rounded to nearest even.
+ * Tokens that join a tile already begun raise its scale at most: the older
+ * codes are then rounded once more, to the new scale (exact for all but
+ * values near e4m3's subnormals). Rows of a touched tile behind the last
+ * token become zero; a tile that is begun gets its pos, and weight 0. */
+int veda_kv_append(const veda_kv_cache* C, const void* k, const int64_t* k_strides, const void* v,
+                   const int64_t* v_strides, int32_t n, const int32_t* n_new, cudaStream_t stream);
+
+/* Takes the n pending tokens in: len[b, h] += n_new[b], next_pos[b] +=
+ * n_new[b]. */
+int veda_kv_advance(const veda_kv_cache* C, int32_t n, const int32_t* n_new, cudaStream_t stream);
+
+/* Attention of n_q query tokens per sequence over the cache:
+ *   O_i = sum_j softmax_j(scale * q_i . k_j) v_j over the visible keys j.
+ * q, o: bf16 [B, n_q, heads, d], heads a multiple of heads_kv (query head x
+ * reads K/V head x / (heads / heads_kv)), heads <= 4096. Query i of sequence b
+ * is at position t = next_pos[b] + i. Visible are the len[b, h] tokens held
+ * and, where `pending` is not 0, the n_new[b] behind them (then n_new and n_q
+ * are those of the append), of these
+ *   causal != 0:  the positions p <= t only;
+ *   window > 0:   the positions p > t - window or p < sinks only.
+ * A query that sees nothing gets zeros and lse = -inf. Rows i >= n_new[b] of
+ * o and lse are not written.
+ *   lse (may be NULL) [B, heads, n_q] fp32: natural-log softmax normaliser.
+ *   weight (may be NULL) [B, heads_kv, nb_cap] fp32, e.g. C->weight: for each
+ *     tile in use weight = decay * weight + (the softmax weight that this
+ *     call's queries, over the head's whole group, gave its tokens); decay 0
+ *     overwrites. Sequences without new rows keep theirs. Summed in a fixed
+ *     order.
+ * Tiles that no query sees are not read. q K^T is exact products summed in
+ * fp32; P is rounded to fp16, the sums and O are fp32.
+ * ws: veda_kv_attn_ws_bytes(C, heads, n_q, weight != NULL) bytes of device
+ * scratch, not shared by calls that may run at the same time. */
+size_t veda_kv_attn_ws_bytes(const veda_kv_cache* C, int32_t heads, int32_t n_q, int32_t with_weight);
+int veda_kv_attn(const veda_kv_cache* C, const void* q, const int64_t* q_strides, int32_t heads, int32_t n_q,
+                 const int32_t* n_new, int32_t pending, int32_t causal, int32_t window, int32_t sinks, float scale,
+                 void* o, const int64_t* o_strides, float* lse, float* weight, float decay, void* ws,
+                 cudaStream_t stream);
+
+/* Drops the tiles that received the least attention: of a head with more than
+ * keep[h] tiles in use (keep: HOST array [heads_kv], keep[h] >= sink +
+ * recent), the first `sink` and the last `recent` >= 1 tiles stay, and of the
+ * others the keep[h] - sink - recent with the largest weight (ties: the lower
+ * index; NaN ranks first). The entries of table, pos, k_scale, v_scale and
+ * weight are permuted: tiles that stay first, in their order, then the ones
+ * that go, in theirs (their slots are free again), then the free ones as they
+ * were; len is reduced by whole tiles. Pending tokens must have been taken in
+ * (veda_kv_advance). `out` (NULL = in place): a cache of the same geometry
+ * whose table, pos, scales, weight, len and next_pos receive the result while
+ * C's stay; its arrays are all others than C's. Pools are not touched. */
+int veda_kv_evict(const veda_kv_cache* C, const int32_t* keep, int32_t sink, int32_t recent,
+                  const veda_kv_cache* out, cudaStream_t stream);
+
+/* veda_check_status for a cache. */
+int veda_kv_check_status(const veda_kv_cache* C, cudaStream_t stream);
+
 /* Diagnostic (no counterpart on the pages): launches one thread that waits,
  * through the bounded wait every pipeline kernel uses, on a barrier nothing
  * arrives on. After limit_ms (1..10000) the wait gives up and records

@@ -1,0 +1,587 @@
+"""The 8-bit K/V tile cache against its fp64 oracle: append, attention,
+advance and evict alone at the sizes and masks where each can go wrong, then
+together as a stream uses them.
+
+Tolerances of attention, per element. K and V are exact (codes times scales).
+  logits  products of fp16 and e4m3 values are exact in fp32; summing d of
+          them (and two factors) costs at most d * 2^-23 of sum |q||k| =: S
+          (the tensor core may truncate each partial sum, hence 2^-23), and
+          the exponent's argument, at most 2 S in magnitude next to its
+          reference, and ex2 another 2^-22 * (1 + 4 S): D = 2^-16 * (1 + S)
+          covers both for d <= 128.
+  P       fp16, relative to the largest p_j sv_j =: R of the row, which is at
+          2^7 or above: 2^-11 of each weight, and 2^-25 where it is subnormal,
+          that is 2^-32 R per key, times a code of up to 448 in any channel
+          (that key's, so A, which may be small in that channel, does not
+          bound it).
+  O       with A = sum p |v|: (2^-11 + 4 D) * A + keys * 2^-32 * 448 * R before
+          its own bf16 rounding of 2^-8 |O| (half a step).
+  lse     D + 2^-22 * |lse|.
+  weight  (4 D + 2^-20) of itself."""
+import numpy as np
+import pytest
+import torch
+
+import block_sparse_attention_24_b200 as V
+from oracle.kv_oracle import Cache
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+
+
+def host(t):
+    return t.detach().float().cpu().double().numpy() if t.is_floating_point() else t.cpu().numpy()
+
+
+def oracle_of(c: V.KVCache) -> Cache:
+    return Cache(c.tile, **{f: host(getattr(c, f)) for f in Cache.FIELDS})
+
+
+def random_cache(seed, B, hkv, d, tile, nb_cap, lens, spread=1.0, gaps=False, shuffle=True, n_slots=None):
+    """A cache that holds lens[b] tokens per head, tile scales apart by a
+    normal power of two of deviation `spread`; codes behind len are random
+    bytes (NaN codes among them)."""
+    g = torch.Generator().manual_seed(seed)
+    n = n_slots or B * hkv * nb_cap
+    order = torch.randperm(n, generator=g) if shuffle else torch.arange(n)
+    c = V.KVCache(B, hkv, d, tile, nb_cap, DEV,
+                  k8=torch.zeros((n, tile, d), dtype=torch.uint8, device=DEV).view(torch.float8_e4m3fn),
+                  v8=torch.zeros((n, tile, d), dtype=torch.uint8, device=DEV).view(torch.float8_e4m3fn),
+                  table=order[:B * hkv * nb_cap].to(torch.int32).view(B, hkv, nb_cap).to(DEV))
+    for codes, scale in ((c.k8, c.k_scale), (c.v8, c.v_scale)):
+        x = torch.randn((B, hkv, nb_cap, tile, d), generator=g) * 60
+        u8 = x.to(torch.float8_e4m3fn).view(torch.uint8)
+        behind = torch.arange(nb_cap * tile).view(1, nb_cap, tile) >= torch.tensor(lens).view(B, 1, 1)
+        junk = torch.randint(0, 256, u8.shape, generator=g).to(torch.uint8)
+        junk[..., ::5] = 0x7f
+        u8 = torch.where(behind[:, None, :, :, None], junk, u8)
+        codes.view(torch.uint8)[c.table.long()] = u8.to(DEV)
+        e = torch.round(torch.randn((B, hkv, nb_cap), generator=g) * spread) - 6
+        scale.copy_(torch.exp2(e))
+    at = torch.arange(nb_cap) * tile
+    skip = torch.zeros((B, hkv, nb_cap), dtype=torch.long)
+    if gaps:
+        skip = torch.randint(0, 3, (B, hkv, nb_cap), generator=g).cumsum(-1)
+        last = (torch.tensor(lens) // tile).clamp(max=nb_cap - 1)
+        for b in range(B):
+            top = skip[b, :, last[b]].max()
+            skip[b] = torch.minimum(skip[b], top)
+            skip[b, :, last[b]:] = top
+    c.pos.copy_((skip * tile + at).to(torch.int32))
+    c.len.copy_(torch.tensor(lens, dtype=torch.int32).view(B, 1).expand(B, hkv))
+    c.next_pos.copy_(torch.tensor([lens[b] + int(skip[b, 0, min(lens[b] // tile, nb_cap - 1)]) * tile for b in range(B)],
+                                  dtype=torch.int32))
+    c.weight.copy_(torch.rand((B, hkv, nb_cap), generator=g))
+    return c
+
+
+def assert_same_state(c: V.KVCache, want: Cache, codes=True):
+    for f in Cache.FIELDS:
+        if f in ("k8", "v8") and not codes:
+            continue
+        np.testing.assert_array_equal(host(getattr(c, f)), getattr(want, f), err_msg=f)
+
+
+def workspace(c, heads, n, weight):
+    size = V.veda_kv_attn_ws_bytes(c, heads, n, weight)
+    assert size > 0
+    return torch.full((size,), 0xff, dtype=torch.uint8, device=DEV)   # NaN everywhere
+
+
+def bf16(seed, *shape, size=1.0):
+    g = torch.Generator().manual_seed(seed)
+    return (torch.randn(shape, generator=g) * size).to(torch.bfloat16).to(DEV)
+
+
+def check_attention(c, q, news=None, causal=True, window=0, sinks=0, pending=True, weight=True, decay=0.5, scale=None,
+                    o=None):
+    B, n, heads, d = q.shape
+    scale = d ** -0.5 if scale is None else scale
+    o = torch.full_like(q, 7.0) if o is None else o
+    before = o.clone()
+    lse = torch.full((B, heads, n), 7.0, device=DEV)
+    w0 = host(c.weight)
+    want_o, want_l, want_w, wrote, A, S, R = oracle_of(c).attend(host(q), [n] * B if news is None else news, scale,
+                                                                 causal, window, sinks, pending)
+    nn = None if news is None else torch.tensor(news, dtype=torch.int32, device=DEV)
+    V.veda_kv_attn(c, q, o, scale, workspace(c, heads, n, weight), causal=causal, window=window, sinks=sinks, n_new=nn,
+                   pending=pending, lse=lse, weight=c.weight if weight else None, decay=decay)
+    V.veda_kv_check_status(c)
+    keys = c.nb_cap * c.tile
+    D = 2.0 ** -16 * (1 + S)                                             # [B, heads, n]
+    for b in range(B):
+        m = n if news is None else news[b]
+        # rows behind the sequence's own are left as they were
+        np.testing.assert_array_equal(host(o[b, m:]), host(before[b, m:]))
+        np.testing.assert_array_equal(host(lse[b, :, m:]), 7.0)
+        go, gl = host(o[b, :m]), host(lse[b, :, :m])
+        wo, wl, a, dd = want_o[b, :m], want_l[b, :, :m], A[b, :m], D[b, :, :m]
+        np.testing.assert_array_equal(np.isnan(go), np.isnan(wo))
+        np.testing.assert_array_equal(np.isnan(gl), np.isnan(wl))
+        fin = np.isfinite(wl)
+        np.testing.assert_array_equal(gl[~fin], wl[~fin])
+        assert np.all(np.abs(gl[fin] - wl[fin]) <= (dd + 2.0 ** -22 * np.abs(wl))[fin])
+        tol = ((2.0 ** -11 + 4 * dd.transpose(1, 0)[..., None]) * a + 2.0 ** -8 * np.abs(wo)
+               + keys * 2.0 ** -32 * 448 * R[b, :, :m].transpose(1, 0)[..., None])
+        ok = np.isnan(wo) | (np.abs(go - wo) <= tol)
+        assert ok.all(), f"batch {b}: {np.max((np.abs(go - wo) - tol)[~np.isnan(wo)])} over"
+    if weight:
+        gw, ww = host(c.weight), np.where(wrote, decay * w0 + want_w, w0)
+        np.testing.assert_array_equal(np.isnan(gw), np.isnan(ww))
+        fin = ~np.isnan(ww)
+        rel = 4 * np.max(D, where=np.isfinite(D), initial=0.0) + 2.0 ** -20    # rows that see a NaN have no bound
+        assert np.all(np.abs(gw - ww)[fin] <= rel * np.abs(ww)[fin] + 2.0 ** -40)
+    else:
+        np.testing.assert_array_equal(host(c.weight), w0)
+    return o, lse
+
+
+# ------------------------------------------------------------------ append
+
+@pytest.mark.parametrize("d,tile", [(64, 64), (64, 128), (128, 64), (128, 128)])
+@pytest.mark.parametrize("lens,n,news", [
+    ([0], 1, None), ([0, 5, 63], 1, None), ([0, 64, 128], 64, None), ([1, 127, 200], 129, [129, 0, 1]),
+    ([130, 30], 300, [300, 171]),
+])
+def test_append_codes_scales_and_positions(d, tile, lens, n, news):
+    B, hkv = len(lens), 3
+    c = random_cache(1, B, hkv, d, tile, 8, lens, spread=2.0, gaps=True)
+    want = oracle_of(c)
+    size = torch.randint(-8, 9, (B, n, 1, 1), generator=torch.Generator().manual_seed(3)).float()
+    k = bf16(2, B, n, hkv, d) * torch.exp2(size).to(DEV)
+    v = bf16(4, B, n, hkv, d, size=1e-3)
+    k, v = k.to(torch.bfloat16), v.to(torch.bfloat16)
+    nn = None if news is None else torch.tensor(news, dtype=torch.int32, device=DEV)
+    V.veda_kv_append(c, k, v, n_new=nn)
+    V.veda_kv_check_status(c)
+    want.append(host(k), host(v), [n] * B if news is None else news)
+    assert_same_state(c, want)
+    V.veda_kv_advance(c, n, n_new=nn)
+    want.advance(np.array([n] * B if news is None else news))
+    assert_same_state(c, want)
+
+
+def test_append_token_by_token_raises_the_scale_and_keeps_the_older_codes():
+    c = V.KVCache(2, 2, 64, 64, 3, DEV)
+    want = oracle_of(c)
+    for i in range(70):
+        size = 2.0 ** ((i * 5) % 13 - 6)
+        k, v = bf16(100 + i, 2, 1, 2, 64, size=size), bf16(200 + i, 2, 1, 2, 64, size=1 / size)
+        V.veda_kv_append(c, k, v)
+        V.veda_kv_advance(c, 1)
+        want.append(host(k), host(v), [1, 1])
+        want.advance(np.array([1, 1]))
+    V.veda_kv_check_status(c)
+    assert_same_state(c, want)
+
+
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), -float("inf"), 3e38, 448.0 * 2 ** 80, 2.0 ** -133, 0.0,
+                                   449.0, 448.0, 450.0])
+def test_append_of_extreme_values(value):
+    """Not finite, or beyond what the largest scale holds: the scale is NaN;
+    all others by the formula (448 * 2^80 is the last that fits)."""
+    c = V.KVCache(1, 2, 64, 64, 2, DEV)
+    k = torch.zeros((1, 10, 2, 64), dtype=torch.bfloat16, device=DEV)
+    k[0, 3, 1, 17] = value
+    want = oracle_of(c)
+    V.veda_kv_append(c, k, -k)
+    want.append(host(k), -host(k), [10])
+    assert_same_state(c, want)
+    assert torch.isnan(c.k_scale[0, 1, 0]).item() == (not np.isfinite(value) or value > 448.0 * 2.0 ** 80)
+    # a tile without a scale stays so while tokens join it
+    V.veda_kv_advance(c, 10)
+    want.advance(np.array([10]))
+    V.veda_kv_append(c, torch.ones_like(k), k)
+    want.append(np.ones(k.shape), host(k), [10])
+    assert_same_state(c, want)
+
+
+def test_append_again_replaces_the_pending_tokens():
+    c = random_cache(5, 1, 2, 128, 64, 6, [70])
+    want = oracle_of(c)
+    for seed, n in ((1, 200), (2, 33)):
+        k, v = bf16(seed, 1, n, 2, 128), bf16(seed + 10, 1, n, 2, 128)
+        V.veda_kv_append(c, k, v)
+        want.append(host(k), host(v), [n])
+    # the second, shorter chunk touches tiles 1 only; the first chunk's other tiles are not looked at
+    assert_same_state(c, want)
+
+
+def test_append_reads_strided_rows():
+    c, e = V.KVCache(2, 3, 64, 64, 4, DEV), V.KVCache(2, 3, 64, 64, 4, DEV)
+    qkv = bf16(7, 2, 90, 3, 3, 64)                      # fused projections
+    k, v = qkv[:, :, 1], qkv[:, :, 2].transpose(1, 2).contiguous().transpose(1, 2)
+    assert not k.is_contiguous() and not v.is_contiguous()
+    V.veda_kv_append(c, k, v)
+    V.veda_kv_append(e, k.contiguous(), v.contiguous())
+    for f in Cache.FIELDS:
+        assert torch.equal(getattr(c, f).view(torch.uint8), getattr(e, f).view(torch.uint8)), f
+    V.veda_kv_append(c, k[:, :1].expand(2, 5, 3, 64), v[:1].expand(2, 90, 3, 64)[:, :5])    # broadcast tokens, sequences
+    V.veda_kv_append(e, k[:, :1].expand(2, 5, 3, 64).contiguous(), v[:1].expand(2, 90, 3, 64)[:, :5].contiguous())
+    for f in Cache.FIELDS:
+        assert torch.equal(getattr(c, f).view(torch.uint8), getattr(e, f).view(torch.uint8)), f
+
+
+def bad_status(c):
+    with pytest.raises(V.VedaError) as e:
+        V.veda_kv_check_status(c)
+    assert e.value.code == V.VEDA_ERR_BAD_INDEX
+    V.veda_kv_check_status(c)                           # cleared
+
+
+def test_full_cache_and_bad_counts_leave_the_sequence_alone():
+    c = random_cache(8, 3, 2, 64, 64, 2, [100, 10, 0])
+    want = oracle_of(c)
+    k = bf16(9, 3, 30, 2, 64)
+    news = [30, 31, 30]                                 # full; more than there are rows; fine
+    nn = torch.tensor(news, dtype=torch.int32, device=DEV)
+    V.veda_kv_append(c, k, k, n_new=nn)
+    bad_status(c)
+    want.append(host(k), host(k), [30, 0, 30])
+    assert_same_state(c, want)
+    q, o = bf16(10, 3, 30, 4, 64), torch.full((3, 30, 4, 64), 5.0, dtype=torch.bfloat16, device=DEV)
+    V.veda_kv_attn(c, q, o, 0.125, workspace(c, 4, 30, True), n_new=nn, weight=c.weight)
+    bad_status(c)
+    assert (o[:2] == 5).all() and not (o[2] == 5).any()
+    V.veda_kv_advance(c, 30, n_new=nn)
+    bad_status(c)
+    assert c.len.tolist() == [[100, 100], [10, 10], [30, 30]]
+    for n_bad in ([-1, 0, 0], [0, 1 << 30, 0]):
+        V.veda_kv_append(c, k, k, n_new=torch.tensor(n_bad, dtype=torch.int32, device=DEV))
+        bad_status(c)
+
+
+def test_table_entries_outside_the_pool_are_absent_tiles():
+    c = random_cache(11, 1, 2, 64, 64, 5, [200], shuffle=False)
+    c.table[0, 0, 1] = c.n_slots
+    c.table[0, 1, 0] = -1
+    q = bf16(12, 1, 3, 4, 64)
+    want = oracle_of(c).attend(host(q), [3], 0.125, False, 0, 0, pending=False)
+    o, w = torch.empty_like(q), torch.zeros_like(c.weight)
+    V.veda_kv_attn(c, q, o, 0.125, workspace(c, 4, 3, True), causal=False, pending=False, weight=w)
+    bad_status(c)
+    np.testing.assert_allclose(host(o), want[0], rtol=2.0 ** -7, atol=2.0 ** -6)
+    assert w[0, 0, 1] == 0 and w[0, 1, 0] == 0
+    k = bf16(13, 1, 10, 2, 64)
+    c.table[0, 0, 3] = c.n_slots + 5
+    before = c.k8.view(torch.uint8).clone()
+    V.veda_kv_append(c, k, k)
+    bad_status(c)
+    changed = (c.k8.view(torch.uint8) != before).flatten(1).any(1).nonzero().flatten().tolist()
+    assert changed == [8]                               # head 1's tail tile only
+
+
+# --------------------------------------------------------------- attention
+
+@pytest.mark.parametrize("d,tile", [(64, 64), (64, 128), (128, 64), (128, 128)])
+@pytest.mark.parametrize("heads,hkv,n", [(2, 2, 1), (8, 2, 1), (3, 1, 2), (16, 1, 1), (32, 1, 1), (10, 2, 5), (6, 3, 9),
+                                         (4, 2, 40), (5, 1, 67), (2, 2, 131)])
+def test_attention_of_few_and_of_many_rows(d, tile, heads, hkv, n):
+    lens = [0, 1, 3 * tile - n % 7, 700]
+    nb_cap = -(-(700 + n) // tile)
+    c = random_cache(20 + n, 4, hkv, d, tile, nb_cap, [x + n for x in lens], gaps=False)
+    c.len.sub_(n)                                       # the last n are pending
+    c.next_pos.sub_(n)
+    check_attention(c, bf16(21, 4, n, heads, d, size=2.0))
+    check_attention(c, bf16(22, 4, n, heads, d), news=[n, max(0, n - 1), 0, (n + 1) // 2], causal=False, decay=0.0)
+
+
+@pytest.mark.parametrize("n", [1, 4, 33, 150])
+@pytest.mark.parametrize("window,sinks", [(1, 0), (1, 1), (5, 0), (64, 4), (200, 64), (129, 65), (5000, 3), (300, 10 ** 6)])
+@pytest.mark.parametrize("causal", [True, False])
+def test_window_and_first_tokens(n, window, sinks, causal):
+    lens = [900, 130, 0]
+    c = random_cache(30 + n, 3, 2, 64, 64, -(-(900 + n) // 64), [x + n for x in lens], gaps=True)
+    c.len.sub_(n)
+    c.next_pos.sub_(n)
+    check_attention(c, bf16(31, 3, n, 6, 64, size=2.0), causal=causal, window=window, sinks=sinks)
+    check_attention(c, bf16(32, 3, n, 6, 64), causal=causal, window=window, sinks=sinks, pending=False, weight=False)
+
+
+@pytest.mark.parametrize("n", [1, 20, 200])
+def test_queries_that_see_nothing(n):
+    """No tokens held and none pending; a window that evicted tiles fill; all
+    keys after the query."""
+    c = random_cache(40, 2, 2, 128, 128, 4, [0, 300])
+    o, lse = check_attention(c, bf16(41, 2, n, 4, 128), pending=False)
+    assert (o[0] == 0).all() and torch.isinf(lse[0]).all() and (lse[0] < 0).all()
+    c.next_pos[1] = 1 << 20
+    o, lse = check_attention(c, bf16(42, 2, n, 4, 128), pending=False, window=50)
+    assert (o == 0).all() and (lse == -float("inf")).all()
+    c.next_pos[1] = -(1 << 20)
+    o, lse = check_attention(c, bf16(43, 2, n, 4, 128), pending=False)
+    assert (o == 0).all() and (lse == -float("inf")).all()
+
+
+@pytest.mark.parametrize("n", [1, 3, 40, 300])
+def test_long_cache_is_split(n):
+    c = random_cache(50, 1, 1, 128, 128, 81, [10000 + n], spread=3.0)
+    c.len.sub_(n)
+    c.next_pos.sub_(n)
+    check_attention(c, bf16(51, 1, n, 4, 128, size=1.5))
+
+
+@pytest.mark.parametrize("n", [1, 40, 300])
+def test_tile_scales_far_apart(n):
+    """K scales that give one tile all the weight or none, V scales from one
+    end of their range to the other."""
+    c = random_cache(60, 1, 2, 64, 64, 16, [700 + n])
+    c.len.sub_(n)
+    c.next_pos.sub_(n)
+    g = torch.Generator().manual_seed(61)
+    c.v_scale.copy_(torch.exp2(torch.randint(-40, 81, c.v_scale.shape, generator=g).float()))
+    check_attention(c, bf16(62, 1, n, 4, 64), weight=True)
+    c.v_scale.fill_(2.0 ** -40)
+    c.k_scale.copy_(torch.exp2(torch.randint(-12, 0, c.k_scale.shape, generator=g).float()))
+    check_attention(c, bf16(63, 1, n, 4, 64, size=3.0))
+
+
+@pytest.mark.parametrize("size", [2.0 ** -100, 2.0 ** -30, 2.0 ** 30, 2.0 ** 100])
+@pytest.mark.parametrize("n", [1, 150])
+def test_query_magnitudes_beyond_fp16(size, n):
+    c = random_cache(70, 1, 2, 64, 64, 8, [300 + n])
+    c.len.sub_(n)
+    c.next_pos.sub_(n)
+    q = bf16(71, 1, n, 2, 64) * size
+    check_attention(c, q.to(torch.bfloat16), scale=0.125 / size)
+
+
+@pytest.mark.parametrize("n", [1, 5, 40, 150])
+def test_nan_tiles_reach_only_the_queries_that_see_them(n):
+    c = random_cache(80, 1, 2, 64, 64, 12, [700], gaps=False)
+    c.len.sub_(n)
+    c.next_pos.sub_(n)
+    c.k_scale[0, 0, 3] = float("nan")                   # outside the window of all
+    c.v_scale[0, 1, 2] = float("nan")
+    for codes, slot in ((c.k8, c.table[0, 0, 2]), (c.v8, c.table[0, 1, 1])):
+        codes.view(torch.uint8)[slot.long()] = 0x7f     # NaN codes where no query looks
+    o, _ = check_attention(c, bf16(81, 1, n, 4, 64), window=250, sinks=10)
+    assert not torch.isnan(o).any()
+    c.v_scale[0, 0, 11 - (60 + n) // 64] = float("nan")  # inside some queries' windows, behind others' if n is large
+    c.k_scale[0, 1, 10] = float("nan")
+    o, _ = check_attention(c, bf16(82, 1, n, 4, 64), window=30, sinks=10)
+    o, _ = check_attention(c, bf16(83, 1, n, 4, 64), causal=False)
+    assert torch.isnan(o).any()
+
+
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+def test_queries_that_are_not_finite_stay_alone(value):
+    for n in (2, 160):
+        c = random_cache(85, 1, 1, 64, 64, 6, [200 + n])
+        c.len.sub_(n)
+        c.next_pos.sub_(n)
+        q = bf16(86, 1, n, 2, 64)
+        clean = torch.empty_like(q)
+        V.veda_kv_attn(c, q, clean, 0.125, workspace(c, 2, n, False))
+        q[0, 1, 1, 5] = value
+        o = torch.empty_like(q)
+        V.veda_kv_attn(c, q, o, 0.125, workspace(c, 2, n, False))
+        assert torch.isnan(o[0, 1, 1]).all()
+        o[0, 1, 1] = clean[0, 1, 1]
+        assert torch.equal(o, clean)
+
+
+def test_attention_reads_and_writes_strided_rows():
+    for n in (1, 70):
+        c = random_cache(90, 2, 2, 64, 64, 5, [200 + n, 100 + n])
+        c.len.sub_(n)
+        c.next_pos.sub_(n)
+        fused = bf16(91, 2, n, 3, 4, 64)
+        room = torch.full((2, 4, n + 3, 64), 9.0, dtype=torch.bfloat16, device=DEV)
+        o = room.transpose(1, 2)[:, 1:n + 1]
+        check_attention(c, fused[:, :, 0], o=o)
+        assert (room[:, :, 0] == 9).all() and (room[:, :, n + 1:] == 9).all()
+
+
+@pytest.mark.parametrize("n", [1, 140])
+def test_slots_past_two_gigabytes(n):
+    """Code offsets that do not fit 31 bits."""
+    tile, d = 128, 128
+    n_slots = (1 << 31) // (tile * d) + 40
+    k8 = torch.zeros((n_slots, tile, d), dtype=torch.uint8, device=DEV).view(torch.float8_e4m3fn)
+    v8 = torch.zeros_like(k8.view(torch.uint8)).view(torch.float8_e4m3fn)
+    table = torch.tensor([[n_slots - 1 - 7 * i for i in range(4)]], dtype=torch.int32, device=DEV).view(1, 1, 4)
+    c = V.KVCache(1, 1, d, tile, 4, DEV, k8=k8, v8=v8, table=table)
+    small = V.KVCache(1, 1, d, tile, 4, DEV)
+    k, v, q = bf16(95, 1, 300 + n, 1, d), bf16(96, 1, 300 + n, 1, d), bf16(97, 1, n, 2, d)
+    got = []
+    for cache in (c, small):
+        V.veda_kv_append(cache, k[:, :300], v[:, :300])
+        V.veda_kv_advance(cache, 300)
+        V.veda_kv_append(cache, k[:, 300:], v[:, 300:])
+        o = torch.empty_like(q)
+        V.veda_kv_attn(cache, q, o, 0.1, workspace(cache, 2, n, True), weight=cache.weight)
+        got.append((o, cache.weight.clone()))
+    V.veda_kv_check_status(c)
+    assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
+    assert (got[0][0] != 0).any()
+    # a table near the end of the pool, rows of it read in place
+    np.testing.assert_array_equal(host(c.k8[table.long().view(-1)]), host(small.k8))
+
+
+def test_shared_slots():
+    """Two sequences read one prefix."""
+    for n in (1, 70):
+        c = random_cache(98, 2, 1, 64, 64, 5, [256, 256])
+        c.table[1, 0, :3] = c.table[0, 0, :3]
+        check_attention(c, bf16(99, 2, n, 2, 64), pending=False)
+
+
+def test_attention_is_repeatable():
+    for n in (1, 90):
+        c = random_cache(100, 2, 2, 128, 128, 20, [2000, 1500])
+        q = bf16(101, 2, n, 8, 128)
+        got = []
+        for _ in range(3):
+            o, w, l = torch.empty_like(q), torch.zeros_like(c.weight), torch.empty((2, 8, n), device=DEV)
+            V.veda_kv_attn(c, q, o, 0.1, workspace(c, 8, n, True), pending=False, weight=w, lse=l)
+            got.append((o, w, l))
+        for x in got[1:]:
+            assert all(torch.equal(a, b) for a, b in zip(x, got[0]))
+
+
+# ------------------------------------------------------------------- evict
+
+def evict_cache(seed, B, hkv, nb_cap, lens, weights):
+    c = random_cache(seed, B, hkv, 64, 64, nb_cap, lens, gaps=True) if nb_cap < 100 else V.KVCache(
+        B, hkv, 64, 64, nb_cap, DEV, k8=torch.zeros((B * hkv * nb_cap, 64, 64), dtype=torch.uint8, device=DEV).view(
+            torch.float8_e4m3fn), v8=torch.zeros((B * hkv * nb_cap, 64, 64), dtype=torch.uint8, device=DEV).view(
+                torch.float8_e4m3fn))
+    c.len.copy_(torch.tensor(lens, dtype=torch.int32).view(B, 1).expand(B, hkv))
+    c.weight.copy_(weights.to(DEV))
+    if nb_cap >= 100:
+        g = torch.Generator().manual_seed(seed)
+        for t in (c.k_scale, c.v_scale):
+            t.copy_(torch.rand(t.shape, generator=g))
+        c.pos.copy_((torch.arange(nb_cap) * 64).to(torch.int32).expand_as(c.pos))
+    return c
+
+
+CASES = [
+    # nb_cap, lens, keep, sink, recent
+    (9, [9 * 64, 8 * 64 + 1, 300], [5, 6], 1, 2), (9, [576, 10, 0], [3, 9], 1, 2), (9, [576, 512, 511], [1, 2], 0, 1),
+    (9, [576, 512, 511], [4, 8], 3, 1), (700, [700 * 64, 40000, 17001], [300, 513], 4, 100),
+    (8192, [8192 * 64, 8191 * 64 + 1, 200000], [4000, 8191], 0, 1),
+]
+
+
+@pytest.mark.parametrize("nb_cap,lens,keep,sink,recent", CASES)
+@pytest.mark.parametrize("kind", ["random", "ties", "odd"])
+def test_evict_in_place_and_into_another(nb_cap, lens, keep, sink, recent, kind):
+    g = torch.Generator().manual_seed(nb_cap)
+    w = torch.rand((3, 2, nb_cap), generator=g) ** 8 * 1e3
+    if kind == "ties":
+        w = torch.randint(0, 3, w.shape, generator=g).float()
+    elif kind == "odd":
+        special = torch.tensor([float("nan"), float("inf"), -float("inf"), -0.0, 0.0, -1.0, 1e-42, -1e-42, 3e38])
+        w = torch.where(torch.rand(w.shape, generator=g) < 0.6, special[torch.randint(0, 9, w.shape, generator=g)], w)
+    c = evict_cache(110, 3, 2, nb_cap, lens, w)
+    meta = {f: getattr(c, f).clone() for f in ("table", "pos", "k_scale", "v_scale", "weight", "len", "next_pos")}
+    out = V.KVCache(3, 2, 64, 64, nb_cap, DEV, k8=c.k8, v8=c.v8, **{f: t.clone().fill_(3) for f, t in meta.items()})
+    want = oracle_of(c) if nb_cap < 100 else Cache(64, k8=np.zeros((1, 64, 64)), v8=np.zeros((1, 64, 64)),
+                                                   **{f: host(t) for f, t in meta.items()})
+    want.evict(keep, sink, recent)
+    V.veda_kv_evict(c, keep, sink, recent, out=out)
+    for f, t in meta.items():
+        np.testing.assert_array_equal(host(getattr(c, f)), host(t), err_msg=f)     # as it was
+    assert_same_state(out, want, codes=False)
+    V.veda_kv_evict(c, keep, sink, recent)
+    assert_same_state(c, want, codes=False)
+    V.veda_kv_evict(c, keep, sink, recent)                                         # nothing more to drop
+    assert_same_state(c, want, codes=False)
+    V.veda_kv_check_status(c)
+
+
+# ---------------------------------------------------------------- together
+
+def stream_step(c, k, v, q, o, lse, ws, n_new=None, keep=None, causal=True, window=0, sinks=0):
+    n = q.shape[1]
+    V.veda_kv_append(c, k, v, n_new=n_new)
+    V.veda_kv_attn(c, q, o, q.shape[-1] ** -0.5, ws, causal=causal, window=window, sinks=sinks, n_new=n_new, lse=lse,
+                   weight=c.weight, decay=0.9)
+    V.veda_kv_advance(c, n, n_new=n_new)
+    if keep:
+        V.veda_kv_evict(c, keep, 1, 2)
+
+
+@pytest.mark.parametrize("n,d,tile,window", [(1, 64, 64, 0), (48, 64, 64, 0), (200, 128, 128, 300), (130, 128, 64, 0)])
+def test_a_stream_of_steps(n, d, tile, window):
+    """Append, attention, advance, evict, step after step, against the oracle
+    that does the same: after eviction the heads hold different tiles."""
+    B, hkv, heads, keep = 2, 2, 4, [4, 5]
+    c = V.KVCache(B, hkv, d, tile, 6 + -(-n // tile), DEV)
+    for step in range(8 if n > 1 else 3):
+        k, v = bf16(300 + step, B, n, hkv, d), bf16(400 + step, B, n, hkv, d)
+        q = bf16(500 + step, B, n, heads, d, size=2.0)
+        news = [n, n if step % 3 else n // 2]
+        want = oracle_of(c)
+        nn = torch.tensor(news, dtype=torch.int32, device=DEV)
+        V.veda_kv_append(c, k, v, n_new=nn)
+        want.append(host(k), host(v), news)
+        assert_same_state(c, want)
+        check_attention(c, q, news=news, window=window, sinks=3, decay=0.9)
+        want = oracle_of(c)
+        V.veda_kv_advance(c, n, n_new=nn)
+        want.advance(np.array(news))
+        V.veda_kv_evict(c, keep, 1, 2)
+        want.evict(keep, 1, 2)
+        assert_same_state(c, want)
+
+
+@pytest.mark.parametrize("n", [1, 70])
+def test_captured_steps_equal_eager_ones(n):
+    """One captured step, replayed over new inputs in the same buffers, and two
+    captured graphs that share a workspace, replayed in turn."""
+    B, hkv, heads, d, tile = 2, 2, 4, 64, 64
+    ins = [(bf16(600 + s, B, n, hkv, d), bf16(610 + s, B, n, hkv, d), bf16(620 + s, B, n, heads, d)) for s in range(6)]
+    make = lambda: V.KVCache(B, hkv, d, tile, 12, DEV)
+    a, e = make(), make()
+    ws = workspace(a, heads, n, True)
+    k, v, q = (t.clone() for t in ins[0])
+    o, lse = torch.zeros_like(q), torch.zeros((B, heads, n), device=DEV)
+    first = make()                                      # loads every kernel before the capture
+    stream_step(first, k, v, q, o, lse, ws, keep=[3, 3])
+    graphs = []
+    side = torch.cuda.Stream()
+    for _ in range(2):
+        gr = torch.cuda.CUDAGraph()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.graph(gr, stream=side):
+            stream_step(a, k, v, q, o, lse, ws, keep=[3, 3])
+        graphs.append(gr)
+    eo, el = torch.zeros_like(q), torch.zeros_like(lse)
+    for s, (k1, v1, q1) in enumerate(ins):
+        k.copy_(k1), v.copy_(v1), q.copy_(q1)
+        graphs[s % 2].replay()
+        stream_step(e, k1, v1, q1, eo, el, ws.clone(), keep=[3, 3])
+        torch.cuda.synchronize()
+        assert torch.equal(o, eo) and torch.equal(lse, el)
+        for f in Cache.FIELDS:
+            assert torch.equal(getattr(a, f).view(torch.uint8), getattr(e, f).view(torch.uint8)), f
+    V.veda_kv_check_status(a)
+
+
+def test_steps_on_two_streams_at_once():
+    B, hkv, heads, d, tile, n = 1, 2, 4, 128, 128, 64
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    caches = [V.KVCache(B, hkv, d, tile, 40, DEV) for _ in range(4)]
+    ins = [(bf16(700 + s, B, n, hkv, d), bf16(710 + s, B, n, hkv, d), bf16(720 + s, B, n, heads, d)) for s in range(4)]
+    outs = [torch.zeros((B, n, heads, d), dtype=torch.bfloat16, device=DEV) for _ in range(4)]
+    wss = [workspace(caches[0], heads, n, True) for _ in range(4)]
+    torch.cuda.synchronize()
+    for step in range(4):
+        for j, st in ((0, s1), (1, s2)):
+            k, v, q = ins[(step + j) % 4]
+            V.veda_kv_append(caches[j], k, v, stream=st)
+            V.veda_kv_attn(caches[j], q, outs[j], 0.1, wss[j], weight=caches[j].weight, stream=st)
+            V.veda_kv_advance(caches[j], n, stream=st)
+    torch.cuda.synchronize()
+    for step in range(4):
+        for j in (0, 1):
+            k, v, q = ins[(step + j) % 4]
+            V.veda_kv_append(caches[2 + j], k, v)
+            V.veda_kv_attn(caches[2 + j], q, outs[2 + j], 0.1, wss[2 + j], weight=caches[2 + j].weight)
+            V.veda_kv_advance(caches[2 + j], n)
+    torch.cuda.synchronize()
+    for j in (0, 1):
+        assert torch.equal(outs[j], outs[2 + j]) and torch.equal(caches[j].weight, caches[2 + j].weight)
