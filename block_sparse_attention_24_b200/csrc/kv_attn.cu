@@ -36,8 +36,14 @@ __device__ __forceinline__ void codes_f16(uint32_t c, uint32_t& lo, uint32_t& hi
   asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
       : "=r"(lo), "=r"(hi) : "r"(c));
 }
+__device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* map, uint64_t* bar, int c0, int c1) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(
+          smem_u32(dst)), "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1)
+      : "memory");
+}
 __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
@@ -47,22 +53,55 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   return r;
 }
 
+// The power of two that takes a row whose largest |value| has the bits `top`
+// into [2^13, 2^14) (1 for infinities and NaN), and its inverse.
+__device__ __forceinline__ void q_scale(uint32_t top, float& mul, float& inv) {
+  int ex = top >= 0x7f800000u ? 127 : 127 + 13 - ((int)(top >> 23) - 127);
+  if (ex > 253) ex = 253;
+  mul = __uint_as_float((uint32_t)ex << 23);
+  inv = __uint_as_float((uint32_t)(254 - ex) << 23);
+}
+
 // 16-byte chunk `ch` of row r of a piece in shared memory: chunks are permuted
-// inside each 128 bytes so that eight rows' chunks fall into different banks.
+// inside each 128 bytes so that eight rows' chunks fall into different banks
+// (TMA's 128- and 64-byte swizzles).
 template <int D>
 __device__ __forceinline__ int swz(int r, int ch) {
   return D == 128 ? r * 128 + ((ch ^ (r & 7)) << 4) : r * 64 + ((ch ^ ((r >> 1) & 3)) << 4);
 }
 
-// Simple form: each warp copies its piece of K and V through registers into
-// its own shared memory, then computes; nothing is loaded ahead.
+// The two code pools as [n_slots * tile, d] bytes, boxes of one piece.
+struct KvMaps {
+  CUtensorMap k, v;
+};
+
+// A CTA has 16 query rows of one K/V head and a range of its tiles, in pieces
+// of 32 keys; warp w takes every fourth piece and keeps its own reference, sum
+// and O, so that no warp waits for another before the end. Pieces reach the
+// warp through its own ring of STAGES TMA copies on mbarriers: the bound is HBM
+// (1 byte per K and V value, each used by up to 16 rows), so what matters is
+// that enough copies are in flight, not which warp asks for them. Table
+// entries, positions and scales of the warp's next 32 pieces sit in its lanes.
 template <int D>
-__global__ void __launch_bounds__(WARPS * 32)
-    kv_attn_rows_kernel(const KvGeom g, const KvAttnParams p) {
+struct RowsCfg {
+  static constexpr int STAGES = D == 128 ? 2 : 3;
+  static constexpr int PB = PIECE * D;                                   // bytes of a piece of K or V
+  static constexpr int SMEM = WARPS * STAGES * 2 * PB + 1024;            // and alignment
+  static constexpr int CTAS = D == 128 ? 3 : 4;                          // per SM, by registers
+};
+
+template <int D>
+__global__ void __launch_bounds__(WARPS * 32, RowsCfg<D>::CTAS)
+    kv_attn_rows_kernel(const KvGeom g, const KvAttnParams p, const __grid_constant__ KvMaps maps) {
+  using Cfg = RowsCfg<D>;
   constexpr int KS = D / 16;  // 16-wide steps over the head dimension
-  __shared__ __align__(128) uint8_t buf[WARPS][2][PIECE * D];
+  constexpr int ST = Cfg::STAGES;
+  extern __shared__ uint8_t smem_raw[];
   __shared__ float sm_m[WARPS][ROWS], sm_l[WARPS][ROWS];
   __shared__ int sm_cnt[3];
+  __shared__ int sm_abort;
+  __shared__ __align__(8) uint64_t bars[WARPS][ST];
+  uint8_t* smem = smem_raw + (((smem_u32(smem_raw) + 1023u) & ~1023u) - smem_u32(smem_raw));
   const int mt = blockIdx.x % p.row_tiles, sp = blockIdx.x / p.row_tiles, h = blockIdx.y, b = blockIdx.z;
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, gr = lane >> 2, c4 = lane & 3;
   int n_b, held, total;
@@ -73,13 +112,16 @@ __global__ void __launch_bounds__(WARPS * 32)
   const long long trow = (long long)bh * g.nb_cap;
   const int t0 = g.next_pos[b];
   const int t_lo = t0 + mt * ROWS / p.group, t_hi = t0 + (min(rows, mt * ROWS + ROWS) - 1) / p.group;
+  if (tid < WARPS * ST) mbar_init(&bars[tid / ST][tid % ST], 1);
+  if (tid < 3) sm_cnt[tid] = 0;
+  if (tid == 0) sm_abort = 0;
+  fence_mbar_init();
+  __syncthreads();
 
   // the tiles this CTA's queries see: [0, n_first) and [from, upto) of the table
   const int nb = (total + g.tile - 1) / g.tile;
   int n_first = 0, from = 0, upto = nb;
-  if (p.window > 0 || p.causal) {
-    if (tid < 3) sm_cnt[tid] = 0;
-    __syncthreads();
+  if (p.window > 0 || (p.causal && t_hi < t0 + n_b - 1)) {
     int a = 0, f = 0, u = 0;
     for (int i = tid; i < nb; i += WARPS * 32) {
       const int ps = g.pos[trow + i];
@@ -104,9 +146,45 @@ __global__ void __launch_bounds__(WARPS * 32)
     n_first = min(sm_cnt[0], from);
   }
   const int ppt = g.tile / PIECE;
-  const int pieces = (n_first + upto - from) * ppt;
+  // pieces behind the last token, where its tile is among them
+  const int tail = upto == nb && (from < nb || n_first == nb) ? (nb * g.tile - total) / PIECE : 0;
+  const int pieces = max(0, (n_first + upto - from) * ppt - tail);
   const int per = (pieces + p.splits - 1) / p.splits;
   const int p_lo = sp * per, p_hi = min(pieces, p_lo + per);
+  const int mine = p_hi - p_lo > warp ? (p_hi - p_lo - warp + WARPS - 1) / WARPS : 0;  // this warp's pieces
+  // place of the warp's k-th piece: its tile's entry, and which part of the tile
+  auto place = [&](int k, int& sub) {
+    const int pc = p_lo + warp + k * WARPS, vt = pc / ppt;
+    sub = pc - vt * ppt;
+    return vt < n_first ? vt : vt - n_first + from;
+  };
+  uint8_t* ring = smem + warp * ST * 2 * Cfg::PB;
+  int row_of = 0;  // lane j: pool row of the piece issued (32-blockwise) j-th, -1 for none
+  auto issue = [&](int k) {
+    if ((k & 31) == 0) {
+      row_of = -1;
+      if (k + lane < mine) {
+        int sub;
+        const int i = place(k + lane, sub);
+        const int slot = g.table[trow + i];
+        if (slot >= 0 && slot < g.n_slots) row_of = slot * g.tile + sub * PIECE;
+        else report(g.dev_status, VEDA_ERR_BAD_INDEX);
+      }
+    }
+    const int row = __shfl_sync(0xffffffffu, row_of, k & 31);
+    if (lane == 0 && row >= 0) {
+      uint64_t* bar = &bars[warp][k % ST];
+      uint8_t* dst = ring + (k % ST) * 2 * Cfg::PB;
+      mbar_expect_tx(bar, 2 * Cfg::PB);
+      tma_load_2d(dst, &maps.k, bar, 0, row);
+      tma_load_2d(dst + Cfg::PB, &maps.v, bar, 0, row);
+    }
+    return row >= 0;
+  };
+  uint32_t there = 0;  // bit s: stage s holds a piece (not an absent tile)
+  int issued = 0;
+  for (; issued < ST && issued < mine; ++issued)
+    if (issue(issued)) there |= 1u << issued;
 
   // Q as fp16 fragments, each row times a power of two that puts its largest
   // value into [2^13, 2^14): bf16's range fits, and its 8 bits are kept down
@@ -132,12 +210,9 @@ __global__ void __launch_bounds__(WARPS * 32)
     }
     top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
     top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-    // exponent field of the multiplier: 127 + 13 - (exponent of the largest); none for inf and NaN
-    int ex = 127 + 13 - ((int)(top >> 23) - 127);
-    if (top >= 0x7f800000u) ex = 127;
-    if (ex > 253) ex = 253;
-    const float mul = __uint_as_float((uint32_t)ex << 23);
-    qs[e] = __uint_as_float((uint32_t)(254 - ex) << 23) * p.scale_log2;
+    float mul;
+    q_scale(top, mul, qs[e]);
+    qs[e] *= p.scale_log2;
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks) {
       qa[ks][e] = pack_f16x2(__uint_as_float(w[ks].x << 16) * mul, __uint_as_float(w[ks].x & 0xffff0000u) * mul);
@@ -153,38 +228,43 @@ __global__ void __launch_bounds__(WARPS * 32)
     for (int e = 0; e < 2; ++e)
 #pragma unroll
       for (int x = 0; x < 4; ++x) o[c][e][x] = 0.f;
-  uint8_t* kb = buf[warp][0];
-  uint8_t* vb = buf[warp][1];
-  const uint32_t ka = smem_u32(kb), va = smem_u32(vb);
 
-  for (int pc = p_lo + warp; pc < p_hi; pc += WARPS) {
-    const int vt = pc / ppt, sub = pc - vt * ppt;
-    const int i = vt < n_first ? vt : vt - n_first + from;
-    const int key0 = i * g.tile + sub * PIECE;  // place among the head's tokens
-    if (key0 >= total) continue;
-    const int slot = g.table[trow + i];
-    if (slot < 0 || slot >= g.n_slots) {
-      if (lane == 0) {
-        report(g.dev_status, VEDA_ERR_BAD_INDEX);
-        if (p.lw)
-          for (int r = mt * ROWS; r < min(rows, mt * ROWS + ROWS); ++r)
-            p.lw[((long long)bh * p.n_q * p.group + r) * p.pieces_cap + i * ppt + sub] = -INFINITY;
-      }
-      continue;
+  int pos_of = 0;  // lane j: as row_of, for the piece computed j-th
+  float sk_of = 0.f, sv_of = 0.f;
+  bool ok = true;
+  uint32_t phase = 0;  // bit s: parity of stage s
+  for (int k = 0; k < mine; ++k) {
+    const int st = k % ST;
+    int sub;
+    const int i = place(k, sub);
+    if ((k & 31) == 0 && k + lane < mine) {
+      int sb;
+      const long long e = trow + place(k + lane, sb);
+      pos_of = g.pos[e] + sb * PIECE;
+      sk_of = g.k_scale[e];
+      sv_of = g.v_scale[e];
     }
-    const uint8_t* ks = g.k8 + ((long long)slot * g.tile + sub * PIECE) * D;
-    const uint8_t* vs = g.v8 + ((long long)slot * g.tile + sub * PIECE) * D;
-    const int left = total - key0;  // keys of the piece that exist
-    __syncwarp();
-#pragma unroll
-    for (int j = 0; j < PIECE * D / 16 / 32; ++j) {
-      const int x = j * 32 + lane, r = x / (D / 16), ch = x % (D / 16);
-      const uint4 z = make_uint4(0, 0, 0, 0);
-      // rows behind the last token are zeroes: their codes may be anything
-      *reinterpret_cast<uint4*>(kb + swz<D>(r, ch)) = r < left ? *reinterpret_cast<const uint4*>(ks + x * 16) : z;
-      *reinterpret_cast<uint4*>(vb + swz<D>(r, ch)) = r < left ? *reinterpret_cast<const uint4*>(vs + x * 16) : z;
+    const int pos0 = __shfl_sync(0xffffffffu, pos_of, k & 31);
+    const float sk = __shfl_sync(0xffffffffu, sk_of, k & 31), sv = __shfl_sync(0xffffffffu, sv_of, k & 31);
+    if (!(there >> st & 1u)) {
+      if (p.lw && lane < ROWS && mt * ROWS + lane < rows)
+        p.lw[((long long)bh * p.n_q * p.group + mt * ROWS + lane) * p.pieces_cap + i * ppt + sub] = -INFINITY;
+    } else {
+    if (!__all_sync(0xffffffffu, mbar_wait(&bars[warp][st], phase >> st & 1u, &sm_abort, g.dev_status))) {
+      ok = false;
+      break;
     }
-    __syncwarp();
+    phase ^= 1u << st;
+    const uint32_t ka = smem_u32(ring + st * 2 * Cfg::PB), va = ka + Cfg::PB;
+    const int left = total - (i * g.tile + sub * PIECE);  // keys of the piece that exist
+    if (left < PIECE) {
+      // V rows behind the last token become zeroes: their codes may be anything
+      for (int x = left * D / 16 + lane; x < Cfg::PB / 16; x += 32)
+        *reinterpret_cast<uint4*>(ring + st * 2 * Cfg::PB + Cfg::PB + swz<D>(x / (D / 16), x % (D / 16))) =
+            make_uint4(0, 0, 0, 0);
+      fence_proxy_async_smem();
+      __syncwarp();
+    }
     float s[4][4];
 #pragma unroll
     for (int nt = 0; nt < 4; ++nt) {
@@ -202,9 +282,7 @@ __global__ void __launch_bounds__(WARPS * 32)
         }
       }
     }
-    const float sk = g.k_scale[trow + i], sv = g.v_scale[trow + i];
     const float ev = log2f(sv), rv = 1.0f / sv;
-    const int pos0 = g.pos[trow + i] + sub * PIECE;
     const float co[2] = {qs[0] * sk, qs[1] * sk};
     const bool whole = left >= PIECE && kv_seen(pos0 + PIECE - 1, t_lo, p.causal, 0, 0) &&
                        (p.window <= 0 || pos0 + PIECE <= p.sinks || (long long)pos0 > (long long)t_hi - p.window);
@@ -275,7 +353,16 @@ __global__ void __launch_bounds__(WARPS * 32)
       mma(o[ch][0], pa[1], ev_f[2], ev_f[3]);
       mma(o[ch][1], pa[1], od_f[2], od_f[3]);
     }
+    }
+    if (issued < mine) {
+      __syncwarp();  // every lane has read the stage
+      there = issue(issued) ? there | 1u << st : there & ~(1u << st);
+      ++issued;
+    }
   }
+  if (!ok)  // let every copy that was started land
+    for (int s = 0; s < ST; ++s)
+      if (there >> s & 1u) mbar_wait_drain(&bars[warp][s], phase >> s & 1u, VEDA_WAIT_LIMIT_NS);
 
   // join the warps: references, then sums and O in warp order
 #pragma unroll
@@ -285,38 +372,34 @@ __global__ void __launch_bounds__(WARPS * 32)
     if (c4 == 0) sm_m[warp][gr + 8 * e] = m[e];
   }
   __syncthreads();
-  float mx[2], f[2];
+  float* acc = reinterpret_cast<float*>(smem);  // [WARPS][ROWS][D], in the ring
 #pragma unroll
   for (int e = 0; e < 2; ++e) {
-    mx[e] = sm_m[0][gr + 8 * e];
+    float mx = sm_m[0][gr + 8 * e];
 #pragma unroll
-    for (int w = 1; w < WARPS; ++w) mx[e] = fmaxf(mx[e], sm_m[w][gr + 8 * e]);
-    f[e] = m[e] == -INFINITY ? (l[e] == l[e] ? 0.f : 1.f) : fast_exp2(m[e] - mx[e]);
-    if (c4 == 0) sm_l[warp][gr + 8 * e] = l[e] * f[e];
+    for (int w = 1; w < WARPS; ++w) mx = fmaxf(mx, sm_m[w][gr + 8 * e]);
+    const float f = m[e] == -INFINITY ? (l[e] == l[e] ? 0.f : 1.f) : fast_exp2(m[e] - mx);
+    if (c4 == 0) sm_l[warp][gr + 8 * e] = l[e] * f;
+#pragma unroll
+    for (int ch = 0; ch < KS; ++ch)
+      *reinterpret_cast<float4*>(acc + (warp * ROWS + gr + 8 * e) * D + ch * 16 + c4 * 4) = make_float4(
+          o[ch][0][2 * e] * f, o[ch][1][2 * e] * f, o[ch][0][2 * e + 1] * f, o[ch][1][2 * e + 1] * f);
   }
   __syncthreads();
-  float* acc = reinterpret_cast<float*>(buf);  // [ROWS][D]
-  for (int w = 0; w < WARPS; ++w) {
-    if (warp == w) {
-#pragma unroll
-      for (int e = 0; e < 2; ++e)
-#pragma unroll
-        for (int ch = 0; ch < KS; ++ch) {
-          float4* a = reinterpret_cast<float4*>(acc + (gr + 8 * e) * D + ch * 16 + c4 * 4);
-          float4 v = w ? *a : make_float4(0.f, 0.f, 0.f, 0.f);
-          v.x += o[ch][0][2 * e] * f[e];
-          v.y += o[ch][1][2 * e] * f[e];
-          v.z += o[ch][0][2 * e + 1] * f[e];
-          v.w += o[ch][1][2 * e + 1] * f[e];
-          *a = v;
-        }
-    }
-    __syncthreads();
-  }
   const long long prow = (((long long)bh * p.splits + sp) * p.row_tiles + mt) * ROWS;
   for (int x = tid; x < ROWS * D / 4; x += WARPS * 32) {
-    const int r = x / (D / 4), c = x % (D / 4);
-    *reinterpret_cast<float4*>(p.part_o + (prow + r) * D + c * 4) = *reinterpret_cast<float4*>(acc + r * D + c * 4);
+    const int r = x / (D / 4), c = x % (D / 4) * 4;
+    if (mt * ROWS + r >= rows) break;
+    float4 v = *reinterpret_cast<float4*>(acc + r * D + c);
+#pragma unroll
+    for (int w = 1; w < WARPS; ++w) {
+      const float4 u = *reinterpret_cast<float4*>(acc + (w * ROWS + r) * D + c);
+      v.x += u.x;
+      v.y += u.y;
+      v.z += u.z;
+      v.w += u.w;
+    }
+    *reinterpret_cast<float4*>(p.part_o + (prow + r) * D + c) = v;
   }
   if (tid < ROWS) {
     float lsum = 0.f, mm = sm_m[0][tid];
@@ -396,13 +479,28 @@ __global__ void __launch_bounds__(128) kv_weight_kernel(const KvGeom g, const Kv
   if (lane == 0) p.weight[entry] = p.decay == 0.f ? w : p.decay * p.weight[entry] + w;
 }
 
+template <int D>
+cudaError_t launch_rows(const KvGeom& g, const KvAttnParams& p, dim3 grid, cudaStream_t s) {
+  KvMaps maps;
+  const uint64_t rows = (uint64_t)g.n_slots * g.tile;
+  if (encode_tensor_map_2d_u8(&maps.k, g.k8, D, rows, PIECE) != CUDA_SUCCESS ||
+      encode_tensor_map_2d_u8(&maps.v, g.v8, D, rows, PIECE) != CUDA_SUCCESS)
+    return cudaErrorInvalidValue;
+  const cudaError_t e =
+      cudaFuncSetAttribute(kv_attn_rows_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, RowsCfg<D>::SMEM);
+  if (e != cudaSuccess) return e;
+  kv_attn_rows_kernel<D><<<grid, WARPS * 32, RowsCfg<D>::SMEM, s>>>(g, p, maps);
+  return cudaGetLastError();
+}
+
 }  // namespace
 
 size_t kv_attn_plan(const KvGeom& g, KvAttnParams& p, bool weights, uint8_t* ws) {
   const long long rows = (long long)p.n_q * p.group;
   p.row_tiles = (int)((rows + ROWS - 1) / ROWS);
   const long long ctas = (long long)g.B * g.hkv * p.row_tiles;
-  const long long want = (148 * 6 + ctas - 1) / ctas;
+  const long long tgt = 148 * 6;
+  const long long want = (tgt + ctas - 1) / ctas;
   const long long most = ((long long)g.nb_cap * g.tile / PIECE + WARPS - 1) / WARPS;
   p.splits = (int)(want < most ? want : most);
   if (p.splits < 1) p.splits = 1;
@@ -436,9 +534,7 @@ size_t kv_attn_ws_bytes(const KvGeom& g, int heads, int n_q, bool weights) {
 cudaError_t launch_kv_attn(const KvGeom& g, KvAttnParams p, void* ws, cudaStream_t s) {
   kv_attn_plan(g, p, p.weight != nullptr, static_cast<uint8_t*>(ws));
   const dim3 grid(p.row_tiles * p.splits, g.hkv, g.B);
-  if (g.d == 128) kv_attn_rows_kernel<128><<<grid, WARPS * 32, 0, s>>>(g, p);
-  else kv_attn_rows_kernel<64><<<grid, WARPS * 32, 0, s>>>(g, p);
-  cudaError_t e = cudaGetLastError();
+  cudaError_t e = g.d == 128 ? launch_rows<128>(g, p, grid, s) : launch_rows<64>(g, p, grid, s);
   if (e != cudaSuccess) return e;
   const dim3 jg((p.n_q * p.group + 3) / 4, g.hkv, g.B);
   if (g.d == 128) kv_join_kernel<128><<<jg, 128, 0, s>>>(g, p);

@@ -81,6 +81,9 @@ __device__ __forceinline__ bool kv_seen(int p, int t, int causal, int window, in
   return window <= 0 || p < sinks || (long long)p > (long long)t - window;
 }
 
+// A pool as a 2D map of bytes [rows, d], box [box_rows, d], swizzled over d bytes (64 or 128).
+CUresult encode_tensor_map_2d_u8(CUtensorMap* map, const void* base, uint64_t d, uint64_t rows, uint32_t box_rows);
+
 cudaError_t launch_kv_append(const KvGeom& g, const KvRows& k, const KvRows& v, int n, const int32_t* n_new,
                              cudaStream_t s);
 cudaError_t launch_kv_advance(const KvGeom& g, int n, const int32_t* n_new, cudaStream_t s);

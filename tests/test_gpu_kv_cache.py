@@ -313,6 +313,16 @@ def test_queries_that_see_nothing(n):
     assert (o == 0).all() and (lse == -float("inf")).all()
 
 
+@pytest.mark.parametrize("n", [1, 20, 200])
+def test_window_behind_the_last_tile_leaves_the_first_tokens(n):
+    """Positions far ahead of all tiles: only the first tokens are seen, and
+    the last tile, which is not full, is none of theirs."""
+    for held in (130, 64 * 6 + 1, 40):
+        c = random_cache(45, 1, 2, 64, 64, 8, [held])
+        c.next_pos.fill_(1 << 20)
+        check_attention(c, bf16(46, 1, n, 4, 64), pending=False, window=50, sinks=100)
+
+
 @pytest.mark.parametrize("n", [1, 3, 40, 300])
 def test_long_cache_is_split(n):
     c = random_cache(50, 1, 1, 128, 128, 81, [10000 + n], spread=3.0)
