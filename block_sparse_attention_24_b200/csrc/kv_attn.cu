@@ -12,7 +12,7 @@
 // pair converts to in one instruction) holds it. OFF keeps what lies 2^-31
 // below the reference out of fp16's zero: even a million such keys add less
 // than a part in a thousand. Sums, references and O are fp32.
-#include "kv_internal.cuh"
+#include "kv_attn.cuh"
 
 namespace veda {
 namespace {
@@ -20,8 +20,8 @@ namespace {
 constexpr int ROWS = 16;    // query rows per CTA (the M of one mma)
 constexpr int PIECE = 32;   // keys a warp takes at a time
 constexpr int WARPS = 4;
-constexpr float OFF = 7.f, MARGIN = 8.f;
-constexpr float LN2 = 0.69314718055994531f;
+constexpr int TILE_KERNEL_ROWS = 32;  // more query rows per K/V head than this: the tile kernel
+constexpr float MARGIN = 8.f;
 
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
@@ -31,50 +31,11 @@ __device__ __forceinline__ void ldsm4_t(uint32_t (&r)[4], uint32_t addr) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
 }
-// two f16 pairs from four e4m3 codes
-__device__ __forceinline__ void codes_f16(uint32_t c, uint32_t& lo, uint32_t& hi) {
-  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
-      : "=r"(lo), "=r"(hi) : "r"(c));
-}
-__device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* map, uint64_t* bar, int c0, int c1) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(
-          smem_u32(dst)), "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1)
-      : "memory");
-}
 __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-
-// The power of two that takes a row whose largest |value| has the bits `top`
-// into [2^13, 2^14) (1 for infinities and NaN), and its inverse.
-__device__ __forceinline__ void q_scale(uint32_t top, float& mul, float& inv) {
-  int ex = top >= 0x7f800000u ? 127 : 127 + 13 - ((int)(top >> 23) - 127);
-  if (ex > 253) ex = 253;
-  mul = __uint_as_float((uint32_t)ex << 23);
-  inv = __uint_as_float((uint32_t)(254 - ex) << 23);
-}
-
-// 16-byte chunk `ch` of row r of a piece in shared memory: chunks are permuted
-// inside each 128 bytes so that eight rows' chunks fall into different banks
-// (TMA's 128- and 64-byte swizzles).
-template <int D>
-__device__ __forceinline__ int swz(int r, int ch) {
-  return D == 128 ? r * 128 + ((ch ^ (r & 7)) << 4) : r * 64 + ((ch ^ ((r >> 1) & 3)) << 4);
-}
-
-// The two code pools as [n_slots * tile, d] bytes, boxes of one piece.
-struct KvMaps {
-  CUtensorMap k, v;
-};
-
 // A CTA has 16 query rows of one K/V head and a range of its tiles, in pieces
 // of 32 keys; warp w takes every fourth piece and keeps its own reference, sum
 // and O, so that no warp waits for another before the end. Pieces reach the
@@ -118,37 +79,12 @@ __global__ void __launch_bounds__(WARPS * 32, RowsCfg<D>::CTAS)
   fence_mbar_init();
   __syncthreads();
 
-  // the tiles this CTA's queries see: [0, n_first) and [from, upto) of the table
   const int nb = (total + g.tile - 1) / g.tile;
-  int n_first = 0, from = 0, upto = nb;
-  if (p.window > 0 || (p.causal && t_hi < t0 + n_b - 1)) {
-    int a = 0, f = 0, u = 0;
-    for (int i = tid; i < nb; i += WARPS * 32) {
-      const int ps = g.pos[trow + i];
-      const bool ahead = p.causal && ps > t_hi;
-      u += !ahead;
-      if (p.window > 0 && !ahead) {
-        a += ps < p.sinks;
-        f += (long long)ps + g.tile - 1 <= (long long)t_lo - p.window;
-      }
-    }
-    a = __reduce_add_sync(0xffffffffu, a);
-    f = __reduce_add_sync(0xffffffffu, f);
-    u = __reduce_add_sync(0xffffffffu, u);
-    if (lane == 0) {
-      atomicAdd(&sm_cnt[0], a);
-      atomicAdd(&sm_cnt[1], f);
-      atomicAdd(&sm_cnt[2], u);
-    }
-    __syncthreads();
-    upto = sm_cnt[2];
-    from = sm_cnt[1];
-    n_first = min(sm_cnt[0], from);
-  }
+  const KvRange rg = kv_range(g, p, trow, nb, t_lo, t_hi, t0 + n_b - 1, sm_cnt, tid, WARPS * 32);
   const int ppt = g.tile / PIECE;
   // pieces behind the last token, where its tile is among them
-  const int tail = upto == nb && (from < nb || n_first == nb) ? (nb * g.tile - total) / PIECE : 0;
-  const int pieces = max(0, (n_first + upto - from) * ppt - tail);
+  const int tail = rg.upto == nb && (rg.from < nb || rg.n_first == nb) ? (nb * g.tile - total) / PIECE : 0;
+  const int pieces = max(0, rg.count() * ppt - tail);
   const int per = (pieces + p.splits - 1) / p.splits;
   const int p_lo = sp * per, p_hi = min(pieces, p_lo + per);
   const int mine = p_hi - p_lo > warp ? (p_hi - p_lo - warp + WARPS - 1) / WARPS : 0;  // this warp's pieces
@@ -156,7 +92,7 @@ __global__ void __launch_bounds__(WARPS * 32, RowsCfg<D>::CTAS)
   auto place = [&](int k, int& sub) {
     const int pc = p_lo + warp + k * WARPS, vt = pc / ppt;
     sub = pc - vt * ppt;
-    return vt < n_first ? vt : vt - n_first + from;
+    return rg.tile(vt);
   };
   uint8_t* ring = smem + warp * ST * 2 * Cfg::PB;
   int row_of = 0;  // lane j: pool row of the piece issued (32-blockwise) j-th, -1 for none
@@ -205,13 +141,12 @@ __global__ void __launch_bounds__(WARPS * 32, RowsCfg<D>::CTAS)
       if (r < rows)
         w[ks] = *reinterpret_cast<const uint2*>(p.q.p + b * p.q.sb + (long long)(r / p.group) * p.q.sn +
                                                 (long long)(h * p.group + r % p.group) * p.q.sh + ks * 16 + c4 * 4);
-      top = max(max(top, max((w[ks].x << 16) & 0x7fffffffu, w[ks].x & 0x7fff0000u)),
-                max((w[ks].y << 16) & 0x7fffffffu, w[ks].y & 0x7fff0000u));
+      top = max(top, max(bf16x2_top(w[ks].x), bf16x2_top(w[ks].y)));
     }
     top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
     top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
     float mul;
-    q_scale(top, mul, qs[e]);
+    q_scale<13>(top, mul, qs[e]);
     qs[e] *= p.scale_log2;
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks) {
@@ -248,7 +183,7 @@ __global__ void __launch_bounds__(WARPS * 32, RowsCfg<D>::CTAS)
     const float sk = __shfl_sync(0xffffffffu, sk_of, k & 31), sv = __shfl_sync(0xffffffffu, sv_of, k & 31);
     if (!(there >> st & 1u)) {
       if (p.lw && lane < ROWS && mt * ROWS + lane < rows)
-        p.lw[((long long)bh * p.n_q * p.group + mt * ROWS + lane) * p.pieces_cap + i * ppt + sub] = -INFINITY;
+        p.lw[((long long)bh * p.pieces_cap + i * ppt + sub) * p.rows_cap + mt * ROWS + lane] = -INFINITY;
     } else {
     if (!__all_sync(0xffffffffu, mbar_wait(&bars[warp][st], phase >> st & 1u, &sm_abort, g.dev_status))) {
       ok = false;
@@ -260,7 +195,7 @@ __global__ void __launch_bounds__(WARPS * 32, RowsCfg<D>::CTAS)
     if (left < PIECE) {
       // V rows behind the last token become zeroes: their codes may be anything
       for (int x = left * D / 16 + lane; x < Cfg::PB / 16; x += 32)
-        *reinterpret_cast<uint4*>(ring + st * 2 * Cfg::PB + Cfg::PB + swz<D>(x / (D / 16), x % (D / 16))) =
+        *reinterpret_cast<uint4*>(ring + st * 2 * Cfg::PB + Cfg::PB + code_at<D>(x / (D / 16), x % (D / 16))) =
             make_uint4(0, 0, 0, 0);
       fence_proxy_async_smem();
       __syncwarp();
@@ -273,7 +208,7 @@ __global__ void __launch_bounds__(WARPS * 32, RowsCfg<D>::CTAS)
 #pragma unroll
       for (int q4 = 0; q4 < KS / 4; ++q4) {
         uint32_t f[4];
-        ldsm4(f, ka + swz<D>(nt * 8 + (lane & 7), q4 * 4 + (lane >> 3)));
+        ldsm4(f, ka + code_at<D>(nt * 8 + (lane & 7), q4 * 4 + (lane >> 3)));
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
           uint32_t b0, b1;
@@ -338,14 +273,14 @@ __global__ void __launch_bounds__(WARPS * 32, RowsCfg<D>::CTAS)
         t += __shfl_xor_sync(0xffffffffu, t, 2);
         const int r = e ? r1 : r0;
         if (c4 == 0 && r < rows)
-          p.lw[((long long)bh * p.n_q * p.group + r) * p.pieces_cap + i * ppt + sub] =
+          p.lw[((long long)bh * p.pieces_cap + i * ppt + sub) * p.rows_cap + r] =
               t == 0.f ? -INFINITY : log2f(t) + (m[e] - OFF - ev);
       }
     }
 #pragma unroll
     for (int ch = 0; ch < KS; ++ch) {
       uint32_t f[4], ev_f[4], od_f[4];
-      ldsm4_t(f, va + swz<D>(lane, ch));
+      ldsm4_t(f, va + code_at<D>(lane, ch));
 #pragma unroll
       for (int x = 0; x < 4; ++x) codes_f16(__byte_perm(f[x], 0, 0x3120), ev_f[x], od_f[x]);
       mma(o[ch][0], pa[0], ev_f[0], ev_f[1]);
@@ -386,7 +321,7 @@ __global__ void __launch_bounds__(WARPS * 32, RowsCfg<D>::CTAS)
           o[ch][0][2 * e] * f, o[ch][1][2 * e] * f, o[ch][0][2 * e + 1] * f, o[ch][1][2 * e + 1] * f);
   }
   __syncthreads();
-  const long long prow = (((long long)bh * p.splits + sp) * p.row_tiles + mt) * ROWS;
+  const long long prow = ((long long)bh * p.splits + sp) * p.rows_pad + mt * ROWS;
   for (int x = tid; x < ROWS * D / 4; x += WARPS * 32) {
     const int r = x / (D / 4), c = x % (D / 4) * 4;
     if (mt * ROWS + r >= rows) break;
@@ -420,7 +355,7 @@ __global__ void __launch_bounds__(128) kv_join_kernel(const KvGeom g, const KvAt
   if (!kv_counts(g, b, h, p.n_q, p.n_new, p.pending, n_b, held, total)) return;
   if (r >= n_b * p.group) return;
   const int bh = b * g.hkv + h;
-  const long long rows = (long long)p.row_tiles * ROWS;
+  const long long rows = p.rows_pad;
   const float2* ml = p.part_ml + (long long)bh * p.splits * rows + r;
   float m = -INFINITY;
   for (int s = 0; s < p.splits; ++s) m = fmaxf(m, ml[s * rows].x);
@@ -445,42 +380,51 @@ __global__ void __launch_bounds__(128) kv_join_kernel(const KvGeom g, const KvAt
 #pragma unroll
   for (int e = 0; e < D / 64; ++e) reinterpret_cast<uint32_t*>(dst)[e] = w[e];
   if (lane == 0) {
-    const float l2 = none ? -INFINITY : log2f(l) + (m - OFF);
+    const float l2 = none ? -INFINITY : log2f(l) + (m == -INFINITY ? 0.f : m) - OFF;
     if (p.lse) p.lse[((long long)b * p.heads + qh) * p.n_q + i] = l2 * LN2;
-    if (p.lse2) p.lse2[(long long)bh * p.n_q * p.group + r] = l2;
+    if (p.lse2) p.lse2[(long long)bh * p.rows_cap + r] = l2;
   }
 }
 
 // weight[tile] = decay * weight[tile] + sum over rows and the tile's pieces of
-// 2^(lw - lse2): a warp per tile, the rows in a fixed order over its lanes.
-__global__ void __launch_bounds__(128) kv_weight_kernel(const KvGeom g, const KvAttnParams p, const int piece,
-                                                        const int rows_per_tile) {
-  const int lane = threadIdx.x % 32, h = blockIdx.y, b = blockIdx.z;
-  const int i = blockIdx.x * 4 + threadIdx.x / 32;
+// 2^(lw - lse2): a block per tile, its sums joined in a fixed order.
+constexpr int WEIGHT_THREADS = 128;
+__global__ void __launch_bounds__(WEIGHT_THREADS) kv_weight_kernel(const KvGeom g, const KvAttnParams p) {
+  __shared__ float part[WEIGHT_THREADS / 32];
+  const int i = blockIdx.x, h = blockIdx.y, b = blockIdx.z, tid = threadIdx.x;
   int n_b, held, total;
   if (!kv_counts(g, b, h, p.n_q, p.n_new, p.pending, n_b, held, total)) return;
   const int nb = (total + g.tile - 1) / g.tile;
   if (i >= nb || n_b == 0) return;
-  const int bh = b * g.hkv + h, ppt = g.tile / piece;
+  const int bh = b * g.hkv + h, ppt = g.tile / p.piece;
   const long long entry = (long long)bh * g.nb_cap + i;
   const int rows = n_b * p.group, t0 = g.next_pos[b], ps = g.pos[entry];
+  const float* lse2 = p.lse2 + (long long)bh * p.rows_cap;
+  const float* lw = p.lw + ((long long)bh * p.pieces_cap + (long long)i * ppt) * p.rows_cap;
   float w = 0.f;
-  for (int r = lane; r < rows; r += 32) {
+  for (int r = tid; r < rows; r += WEIGHT_THREADS) {
     // only tiles that the row's whole CTA could see were visited
-    const int m0 = r / rows_per_tile * rows_per_tile, m1 = min(rows, m0 + rows_per_tile) - 1;
-    const bool seen = kv_tile_seen(ps, g.tile, t0 + m0 / p.group, t0 + m1 / p.group, p.causal, p.window, p.sinks);
-    const float z = p.lse2[(long long)bh * p.n_q * p.group + r];
-    if (!seen || z == -INFINITY) continue;
-    const float* x = p.lw + ((long long)bh * p.n_q * p.group + r) * p.pieces_cap + (long long)i * ppt;
-    for (int k = 0; k < ppt && i * g.tile + k * piece < total; ++k) w += fast_exp2(x[k] - z);
+    const int m0 = r / p.tile_rows * p.tile_rows, m1 = min(rows, m0 + p.tile_rows) - 1;
+    if (!kv_tile_seen(ps, g.tile, t0 + m0 / p.group, t0 + m1 / p.group, p.causal, p.window, p.sinks)) continue;
+    const float z = lse2[r];
+    if (z == -INFINITY) continue;
+    for (int k = 0; k < ppt && i * g.tile + k * p.piece < total; ++k) {
+      const float x = lw[(long long)k * p.rows_cap + r];
+      if (x != -INFINITY) w += fast_exp2(x - z);  // none of it seen: nothing, even of a row that is NaN
+    }
   }
 #pragma unroll
   for (int d = 16; d; d >>= 1) w += __shfl_xor_sync(0xffffffffu, w, d);
-  if (lane == 0) p.weight[entry] = p.decay == 0.f ? w : p.decay * p.weight[entry] + w;
+  if (tid % 32 == 0) part[tid / 32] = w;
+  __syncthreads();
+  if (tid == 0) {
+    for (int k = 1; k < WEIGHT_THREADS / 32; ++k) w += part[k];
+    p.weight[entry] = p.decay == 0.f ? w : p.decay * p.weight[entry] + w;
+  }
 }
 
 template <int D>
-cudaError_t launch_rows(const KvGeom& g, const KvAttnParams& p, dim3 grid, cudaStream_t s) {
+cudaError_t launch_rows(const KvGeom& g, const KvAttnParams& p, cudaStream_t s) {
   KvMaps maps;
   const uint64_t rows = (uint64_t)g.n_slots * g.tile;
   if (encode_tensor_map_2d_u8(&maps.k, g.k8, D, rows, PIECE) != CUDA_SUCCESS ||
@@ -489,7 +433,7 @@ cudaError_t launch_rows(const KvGeom& g, const KvAttnParams& p, dim3 grid, cudaS
   const cudaError_t e =
       cudaFuncSetAttribute(kv_attn_rows_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, RowsCfg<D>::SMEM);
   if (e != cudaSuccess) return e;
-  kv_attn_rows_kernel<D><<<grid, WARPS * 32, RowsCfg<D>::SMEM, s>>>(g, p, maps);
+  kv_attn_rows_kernel<D><<<dim3(p.row_tiles * p.splits, g.hkv, g.B), WARPS * 32, RowsCfg<D>::SMEM, s>>>(g, p, maps);
   return cudaGetLastError();
 }
 
@@ -497,23 +441,27 @@ cudaError_t launch_rows(const KvGeom& g, const KvAttnParams& p, dim3 grid, cudaS
 
 size_t kv_attn_plan(const KvGeom& g, KvAttnParams& p, bool weights, uint8_t* ws) {
   const long long rows = (long long)p.n_q * p.group;
-  p.row_tiles = (int)((rows + ROWS - 1) / ROWS);
-  const long long ctas = (long long)g.B * g.hkv * p.row_tiles;
-  const long long tgt = 148 * 6;
-  const long long want = (tgt + ctas - 1) / ctas;
-  const long long most = ((long long)g.nb_cap * g.tile / PIECE + WARPS - 1) / WARPS;
+  p.tiles = rows > TILE_KERNEL_ROWS;
+  p.tile_rows = p.tiles ? 256 : ROWS;
+  p.row_tiles = (int)((rows + p.tile_rows - 1) / p.tile_rows);
+  p.rows_cap = (int)rows;
+  p.rows_pad = p.row_tiles * p.tile_rows;
+  p.piece = p.tiles ? g.tile : PIECE;
+  p.pieces_cap = g.nb_cap * (g.tile / p.piece);
+  const long long ctas = (long long)g.B * g.hkv * p.row_tiles, keys = (long long)g.nb_cap * g.tile;
+  const long long want = ((p.tiles ? 148 * 2 : 148 * 6) + ctas - 1) / ctas;
+  const long long most = p.tiles ? (keys + 511) / 512 : (keys + PIECE * WARPS - 1) / (PIECE * WARPS);
   p.splits = (int)(want < most ? want : most);
   if (p.splits < 1) p.splits = 1;
-  p.pieces_cap = g.nb_cap * (g.tile / PIECE);
   size_t off = 0;
   auto take = [&](size_t bytes) {
     uint8_t* at = ws ? ws + off : nullptr;
     off += (bytes + 255) / 256 * 256;
     return at;
   };
-  const size_t prows = (size_t)g.B * g.hkv * p.splits * p.row_tiles * ROWS;
-  p.part_o = reinterpret_cast<float*>(take(prows * g.d * 4));
+  const size_t prows = (size_t)g.B * g.hkv * p.splits * p.rows_pad;
   p.part_ml = reinterpret_cast<float2*>(take(prows * 8));
+  p.part_o = p.tiles && p.splits == 1 ? nullptr : reinterpret_cast<float*>(take(prows * g.d * 4));
   p.lse2 = nullptr;
   p.lw = nullptr;
   if (weights) {
@@ -533,15 +481,16 @@ size_t kv_attn_ws_bytes(const KvGeom& g, int heads, int n_q, bool weights) {
 
 cudaError_t launch_kv_attn(const KvGeom& g, KvAttnParams p, void* ws, cudaStream_t s) {
   kv_attn_plan(g, p, p.weight != nullptr, static_cast<uint8_t*>(ws));
-  const dim3 grid(p.row_tiles * p.splits, g.hkv, g.B);
-  cudaError_t e = g.d == 128 ? launch_rows<128>(g, p, grid, s) : launch_rows<64>(g, p, grid, s);
+  cudaError_t e = p.tiles ? launch_kv_attn_tiles(g, p, s) : g.d == 128 ? launch_rows<128>(g, p, s) : launch_rows<64>(g, p, s);
   if (e != cudaSuccess) return e;
-  const dim3 jg((p.n_q * p.group + 3) / 4, g.hkv, g.B);
-  if (g.d == 128) kv_join_kernel<128><<<jg, 128, 0, s>>>(g, p);
-  else kv_join_kernel<64><<<jg, 128, 0, s>>>(g, p);
-  e = cudaGetLastError();
+  if (!p.tiles || p.splits > 1) {
+    const dim3 jg((p.rows_cap + 3) / 4, g.hkv, g.B);
+    if (g.d == 128) kv_join_kernel<128><<<jg, 128, 0, s>>>(g, p);
+    else kv_join_kernel<64><<<jg, 128, 0, s>>>(g, p);
+    e = cudaGetLastError();
+  }
   if (e != cudaSuccess || !p.weight) return e;
-  kv_weight_kernel<<<dim3((g.nb_cap + 3) / 4, g.hkv, g.B), 128, 0, s>>>(g, p, PIECE, ROWS);
+  kv_weight_kernel<<<dim3(g.nb_cap, g.hkv, g.B), WEIGHT_THREADS, 0, s>>>(g, p);
   return cudaGetLastError();
 }
 

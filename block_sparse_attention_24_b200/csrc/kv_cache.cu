@@ -6,7 +6,7 @@
 // dividing by it, changing it later and folding it into an exponent are exact;
 // a floating-point code loses no precision by that, only range, of which 448
 // to 2^-9 leaves plenty.
-#include "kv_internal.cuh"
+#include "kv_attn.cuh"
 
 namespace veda {
 namespace {
@@ -24,13 +24,6 @@ __device__ __forceinline__ float scale_of(float a) {
   if (e < -40) e = -40;
   if (u >= 0x7f800000u || e > 80) return __uint_as_float(0x7fffffffu);
   return __uint_as_float((uint32_t)(e + 127) << 23);
-}
-
-__device__ __forceinline__ uint32_t pack_e4m3x4(float a, float b, float c, float d) {
-  uint16_t lo, hi;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(b), "f"(a));
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(d), "f"(c));
-  return (uint32_t)lo | ((uint32_t)hi << 16);
 }
 
 __device__ __forceinline__ float2 unpack_e4m3x2(uint16_t c) {

@@ -42,12 +42,14 @@ struct KvAttnParams {
   float* lse;     // [B, heads, n_q] natural log, or NULL
   float* weight;  // [B, hkv, nb_cap] or NULL
   float decay;
-  // workspace
-  int32_t splits, row_tiles, pieces_cap;
-  float* part_o;   // [B, hkv, splits, row_tiles * rows, d]
-  float2* part_ml; // [B, hkv, splits, row_tiles * rows]: reference (log2) and sum
-  float* lse2;     // [B, hkv, n_q * group] log2
-  float* lw;       // [B, hkv, n_q * group, pieces_cap] log2 of a piece's sum
+  // workspace, and how the rows (n_q * group per K/V head) are cut
+  int32_t tiles;       // 1: the tile kernel (256 rows per CTA), 0: the row kernel
+  int32_t splits, row_tiles, rows_cap, rows_pad, tile_rows;
+  int32_t piece, pieces_cap;  // keys per entry of lw, entries per head
+  float* part_o;   // [B, hkv, splits, rows_pad, d]
+  float2* part_ml; // [B, hkv, splits, rows_pad]: reference (log2) and sum
+  float* lse2;     // [B, hkv, rows_cap] log2
+  float* lw;       // [B, hkv, pieces_cap, rows_cap] log2 of a piece's sum
 };
 
 // New tokens of sequence b (n_new == NULL: all n), and the tokens its head h

@@ -1,0 +1,567 @@
+// Attention over the 8-bit K/V tile cache, for many query rows (whole chunks
+// and prompts): tcgen05 MMAs with accumulators in TMEM.
+//
+// A CTA owns two row tiles A and B of 128 query rows of one K/V head (row =
+// token * group + head of the group) and walks the tiles that they see, 128
+// keys a step.
+//   S = Q K^T   kind::f8f6f4 on the codes as they lie in the cache: each Q row,
+//               times a power of two, is the sum of two e4m3 parts (8 bits, as
+//               bf16 has; values below 2^-10 of the row's largest lose what is
+//               below 2^-18 of it), so K needs no conversion and two passes at
+//               the 8-bit rate cost what one at 16 bits does.
+//   O += P V    kind::f16: P as fp16 in TMEM (see kv_attn.cu for the exponent
+//               that carries the V scale), V converted from e4m3 by two
+//               warps of their own; a second e4m3 part of P would cost the softmax
+//               warps, which bound the kernel, more than this costs those.
+// The softmax reference is the first maximum and moves only where a step's sum
+// passes 2^15 (then P may no longer fit fp16).
+//
+// Roles (384 threads; more would leave the softmax too few registers for a row of S):
+//   warps 0-3 / 4-7  softmax of A / B: a thread owns a row (TMEM lane). S_A in
+//                    TMEM columns [0,128), S_B [128,256); P over the second
+//                    half of its S; O_A at [256,256+D), O_B at [384,384+D).
+//   warp 8           producer: table, scales, TMA copies of the K and V codes
+//   warp 9           MMA issuer (one thread)
+//   warps 10, 11     V: e4m3 tile -> fp16 tile
+// Every wait is bounded, as in the other pipelines.
+#include <type_traits>
+
+#include "kv_attn.cuh"
+
+namespace veda {
+namespace {
+
+constexpr int BM = 128, BN = 128;
+constexpr int HALF = 64;               // keys per TMA box; a step is two halves
+constexpr int KST = 3, VST = 2, WST = 2;  // stages: K codes, V codes, V fp16
+constexpr int MST = KST + 2;           // step descriptions
+constexpr int SDR = 4;                 // step-done barriers
+constexpr float OVERFLOW_SUM = 32768.f;
+constexpr int THREADS = 384, CONVERT_WARPS = 2;
+// 2*128*208 + 128*88 = 64,512 = the 384*168 of the launch
+constexpr int REGS_SOFTMAX = 208, REGS_ROLES = 88;
+
+struct StepMeta {
+  float ks[2], ev[2], rv[2];  // K scale, log2 of the V scale, its inverse
+  int pos[2], left[2];        // first position, keys that exist
+  int entry[2];               // table entry, -1 for none
+};
+
+template <int D>
+struct TileLayout {
+  static constexpr int QB = BM * D;      // bytes of one part of a row tile
+  static constexpr int CB = BN * D;      // bytes of a step's K or V codes
+  static constexpr int WB = BN * D * 2;  // bytes of a step's V in fp16
+  static constexpr int OFF_Q = 0;        // A hi, A lo, B hi, B lo
+  static constexpr int OFF_K = 4 * QB;
+  static constexpr int OFF_V = OFF_K + KST * CB;
+  static constexpr int OFF_W = OFF_V + VST * CB;
+  static constexpr int OFF_META = OFF_W + WST * WB;
+  static constexpr int OFF_BAR = OFF_META + MST * (int)sizeof(StepMeta);
+  static constexpr int NUM_BARS = 1 + KST + 2 * VST + WST + MST + SDR + 2 + 2 + 2 + 1;
+  static constexpr int OFF_MISC = OFF_BAR + NUM_BARS * 8;
+  static constexpr int ALLOC = OFF_MISC + 32 + 1024;
+};
+static_assert(sizeof(StepMeta) % 8 == 0, "barriers follow");
+
+// Visible keys of one half for one row: k < hi && (k >= lo || k < first).
+struct Span {
+  int lo, hi, first;
+  __device__ bool has(int k) const { return k < hi && (k >= lo || k < first); }
+};
+
+template <bool FULL>
+__device__ __forceinline__ float half_max(const uint32_t (&u)[64], const Span& sp) {
+  float pm[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) pm[i] = -INFINITY;
+#pragma unroll
+  for (int c = 0; c < 64; c += 16)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float v0 = (FULL || sp.has(c + i)) ? __uint_as_float(u[c + i]) : -INFINITY;
+      const float v1 = (FULL || sp.has(c + 8 + i)) ? __uint_as_float(u[c + 8 + i]) : -INFINITY;
+      pm[i] = fmax3(pm[i], v0, v1);
+    }
+  return fmax3(fmax3(pm[0], pm[1], pm[2]), fmax3(pm[3], pm[4], pm[5]), fmaxf(pm[6], pm[7]));
+}
+
+// P = 2^(s*c + nm) of one half as fp16 pairs; returns the sum of the fp32 values.
+template <bool FULL>
+__device__ __forceinline__ float half_p(const uint32_t (&u)[64], const Span& sp, float c, float nm, uint32_t (&pk)[32]) {
+  const uint64_t C2 = f2(c, c), NM = f2(nm, nm);
+  uint64_t acc[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) acc[e] = f2(0.f, 0.f);
+#pragma unroll
+  for (int w = 0; w < 32; ++w) {
+    const uint64_t x = f2_fma(f2(__uint_as_float(u[2 * w]), __uint_as_float(u[2 * w + 1])), C2, NM);
+    float x0, x1;
+    f2_split(x, x0, x1);
+    float p0 = fast_exp2(x0), p1 = fast_exp2(x1);
+    if (!FULL) {
+      p0 = sp.has(2 * w) ? p0 : 0.f;
+      p1 = sp.has(2 * w + 1) ? p1 : 0.f;
+    }
+    acc[w & 3] = f2_add(acc[w & 3], f2(p0, p1));
+    pk[w] = pack_f16x2(p0, p1);
+  }
+  float lo, hi;
+  f2_split(f2_add(f2_add(acc[0], acc[1]), f2_add(acc[2], acc[3])), lo, hi);
+  return lo + hi;
+}
+
+// D[tmem] (+)= A * B: e4m3 from shared memory, or fp16 with A in tensor memory.
+__device__ __forceinline__ void umma_f8_ss(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem), "l"(a), "l"(b), "r"(idesc),
+      "r"(acc) : "memory");
+}
+// Instruction descriptor for M x N with fp32 D and A, B of format 0 (e4m3, or fp16 in kind::f16).
+__host__ __device__ constexpr uint32_t idesc_fmt0(int M, int N, bool b_mn_major) {
+  return (1u << 4) | ((b_mn_major ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+// K-major operand of D-byte rows, swizzled over them (128 or 64 bytes).
+template <int D>
+__device__ __forceinline__ uint64_t sdesc_codes(uint32_t saddr) {
+  uint64_t d = sdesc_sw128(saddr, 16, 8 * D);
+  if (D == 64) d = (d & ~((uint64_t)7 << 61)) | ((uint64_t)4 << 61);  // SWIZZLE_64B
+  return d;
+}
+
+template <int D>
+__global__ void __launch_bounds__(THREADS, 1)
+    kv_attn_tiles_kernel(const KvGeom g, const KvAttnParams p, const __grid_constant__ KvMaps maps) {
+  using Lay = TileLayout<D>;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ int sm_cnt[3];
+  uint8_t* smem = smem_raw + (((smem_u32(smem_raw) + 1023u) & ~1023u) - smem_u32(smem_raw));
+  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+  // under a causal mask the last row tiles have the most keys: they start first
+  const int mt = p.row_tiles - 1 - (int)(blockIdx.x / p.splits), sp = blockIdx.x % p.splits, h = blockIdx.y,
+            b = blockIdx.z;
+  int n_b, held, total;
+  if (!kv_counts(g, b, h, p.n_q, p.n_new, p.pending, n_b, held, total)) return;
+  const int rows = n_b * p.group;
+  const int base = mt * 2 * BM;
+  if (base >= rows) return;
+  const bool has_b = base + BM < rows;
+  const int bh = b * g.hkv + h;
+  const long long trow = (long long)bh * g.nb_cap;
+  const int t0 = g.next_pos[b];
+  const int t_lo = t0 + base / p.group, t_hi = t0 + (min(rows, base + 2 * BM) - 1) / p.group;
+
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Lay::OFF_BAR);
+  uint64_t* q_full = bars;
+  uint64_t* k_full = bars + 1;
+  uint64_t* v_full = k_full + KST;
+  uint64_t* v_free = v_full + VST;   // an arrival per converting warp: it has read the codes
+  uint64_t* w_full = v_free + VST;   // an arrival per converting warp
+  uint64_t* meta_full = w_full + WST;
+  uint64_t* step_done = meta_full + MST;  // S of step e and P V of e-1 have completed
+  uint64_t* s_full = step_done + SDR;     // [2]
+  uint64_t* p_full = s_full + 2;          // [2], 128 arrivals
+  uint64_t* pv_done = p_full + 2;         // [2]
+  uint64_t* drain = pv_done + 2;
+  StepMeta* meta = reinterpret_cast<StepMeta*>(smem + Lay::OFF_META);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Lay::OFF_MISC);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Lay::OFF_MISC + 4);
+  if (tid == 0) {
+    for (int i = 0; i < Lay::NUM_BARS; ++i) {
+      uint64_t* bar = bars + i;
+      int count = 1;
+      if (bar == q_full) count = has_b ? 256 : 128;
+      if (bar >= v_free && bar < w_full + WST) count = CONVERT_WARPS;
+      if (bar == p_full || bar == p_full + 1) count = 128;
+      mbar_init(bar, count);
+    }
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (tid < 3) sm_cnt[tid] = 0;
+  if (warp == 9) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  const int nb = (total + g.tile - 1) / g.tile;
+  const KvRange rg = kv_range(g, p, trow, nb, t_lo, t_hi, t0 + n_b - 1, sm_cnt, tid, THREADS);
+  const int per_step = BN / g.tile;  // tiles per step
+  const int n_tiles = rg.count();
+  const int steps_all = (n_tiles + per_step - 1) / per_step;
+  const int per = (steps_all + p.splits - 1) / p.splits;
+  const int s_lo = min(steps_all, sp * per), n_steps = min(steps_all, s_lo + per) - s_lo;
+
+  if (warp >= 8) {
+    regs_lower<REGS_ROLES>();
+    if (warp == 8) {
+      // --------------------------------------------------------- producer
+      // lane j holds what the step's halves need, 16 steps at a time
+      int pool = -1, entry = -1, pos = 0, left = 0;
+      float ks = 0.f, vs = 1.f;
+      int e = 0;
+      bool ok = true;
+      for (; e < n_steps; ++e) {
+        if ((e & 15) == 0) {
+          const int half = 2 * (s_lo + e) + lane;  // 64-key halves of the tiles seen
+          const int vt = per_step == 1 ? half >> 1 : half, sub = per_step == 1 ? half & 1 : 0;
+          pool = entry = -1;
+          left = 0;
+          ks = 0.f;
+          vs = 1.f;
+          if (vt < n_tiles && e + (lane >> 1) < n_steps) {
+            const int i = rg.tile(vt);
+            const int slot = g.table[trow + i];
+            entry = i;
+            pos = g.pos[trow + i] + sub * HALF;
+            if (slot >= 0 && slot < g.n_slots) {
+              left = max(0, min(HALF, total - (i * g.tile + sub * HALF)));
+              pool = left > 0 ? slot * g.tile + sub * HALF : -1;
+              ks = g.k_scale[trow + i];
+              vs = g.v_scale[trow + i];
+            } else {
+              report(g.dev_status, VEDA_ERR_BAD_INDEX);
+            }
+          }
+        }
+        const int l0 = 2 * (e & 15);
+        const int st = e % KST, vt = e % VST, ms = e % MST;
+        // the description's slot is free: step_done(e - KST) follows the softmax of step e - KST - 1
+        if (e >= KST) ok = mbar_wait(step_done + (e - KST) % SDR, ((e - KST) / SDR) & 1, abort_flag, g.dev_status);
+        if (ok && e >= VST) ok = mbar_wait(v_free + vt, (e / VST - 1) & 1, abort_flag, g.dev_status);
+        if (!__all_sync(0xffffffffu, ok)) break;
+        if (lane == l0 || lane == l0 + 1) {
+          const int x = lane & 1;
+          StepMeta& m = meta[ms];
+          m.ks[x] = ks;
+          m.ev[x] = log2f(vs);
+          m.rv[x] = 1.0f / vs;
+          m.pos[x] = pos;
+          m.left[x] = left;
+          m.entry[x] = entry;
+        }
+        const int row0 = __shfl_sync(0xffffffffu, pool, l0), row1 = __shfl_sync(0xffffffffu, pool, l0 + 1);
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(meta_full + ms);
+          const uint32_t bytes = (row0 >= 0 ? Lay::CB / 2 : 0) + (row1 >= 0 ? Lay::CB / 2 : 0);
+          uint8_t* kd = smem + Lay::OFF_K + st * Lay::CB;
+          uint8_t* vd = smem + Lay::OFF_V + vt * Lay::CB;
+          mbar_expect_tx(k_full + st, bytes);
+          if (row0 >= 0) tma_load_2d(kd, &maps.k, k_full + st, 0, row0);
+          if (row1 >= 0) tma_load_2d(kd + Lay::CB / 2, &maps.k, k_full + st, 0, row1);
+          mbar_expect_tx(v_full + vt, bytes);
+          if (row0 >= 0) tma_load_2d(vd, &maps.v, v_full + vt, 0, row0);
+          if (row1 >= 0) tma_load_2d(vd + Lay::CB / 2, &maps.v, v_full + vt, 0, row1);
+        }
+        __syncwarp();
+      }
+      if (*abort_flag && lane == 0) {  // let every copy that was started land
+        for (int x = max(0, e - KST); x < e; ++x) mbar_wait_drain(k_full + x % KST, (x / KST) & 1, VEDA_WAIT_LIMIT_NS);
+        for (int x = max(0, e - VST); x < e; ++x) mbar_wait_drain(v_full + x % VST, (x / VST) & 1, VEDA_WAIT_LIMIT_NS);
+      }
+    } else if (warp == 9) {
+      if (lane == 0) {
+      // ------------------------------------------------------- MMA issuer
+      constexpr uint32_t idesc_s = idesc_fmt0(BM, BN, false);
+      constexpr uint32_t idesc_o = idesc_fmt0(BM, D, true);
+      const uint64_t dQ = sdesc_codes<D>(smem_u32(smem + Lay::OFF_Q));
+      const uint64_t dK = sdesc_codes<D>(smem_u32(smem + Lay::OFF_K));
+      const uint64_t dW = sdesc_sw128(smem_u32(smem + Lay::OFF_W), BN * 128, 1024);
+      bool ok = n_steps == 0 || mbar_wait(q_full, 0, abort_flag, g.dev_status);
+      if (ok) tc_fence_after();
+      const int tiles = has_b ? 2 : 1;
+      auto issue_pv = [&](int r, int e) -> bool {  // P V of step e
+        const int ws = e % WST;
+        if (!mbar_wait(p_full + r, e & 1, abort_flag, g.dev_status)) return false;
+        if (!mbar_wait(w_full + ws, (e / WST) & 1, abort_flag, g.dev_status)) return false;
+        tc_fence_after();
+        const uint32_t o_addr = tmem + 2 * BN + r * BN, p_addr = tmem + r * BN + 64;
+        const uint64_t d = dW + (uint64_t)(ws * (Lay::WB >> 4));
+#pragma unroll
+        for (int kk = 0; kk < BN / 16; ++kk)
+          umma_bf16_ts(o_addr, p_addr + kk * 8, d + (uint64_t)(kk * (2048 >> 4)), idesc_o, (e > 0 || kk > 0) ? 1u : 0u);
+        if (e == n_steps - 1) umma_commit(pv_done + r);
+        return true;
+      };
+      for (int e = 0; ok && e < n_steps; ++e) {
+        const int st = e % KST;
+        if (!mbar_wait(k_full + st, (e / KST) & 1, abort_flag, g.dev_status)) break;
+        tc_fence_after();
+        for (int r = 0; r < tiles; ++r) {
+          if (e > 0 && !(ok = issue_pv(r, e - 1))) break;
+          const uint64_t q = dQ + (uint64_t)(r * (2 * Lay::QB >> 4)), k = dK + (uint64_t)(st * (Lay::CB >> 4));
+#pragma unroll
+          for (int part = 0; part < 2; ++part)
+#pragma unroll
+            for (int kk = 0; kk < D / 32; ++kk)
+              umma_f8_ss(tmem + r * BN, q + (uint64_t)((part * Lay::QB + kk * 32) >> 4), k + (uint64_t)(kk * 32 >> 4),
+                         idesc_s, (part || kk) ? 1u : 0u);
+          umma_commit(s_full + r);
+        }
+        if (!ok) break;
+        umma_commit(step_done + e % SDR);
+      }
+      for (int r = 0; r < tiles && ok && n_steps > 0 && !*abort_flag; ++r) ok = issue_pv(r, n_steps - 1);
+      umma_commit(drain);
+      mbar_wait_drain(drain, 0, VEDA_WAIT_LIMIT_NS);
+      }
+    } else {
+    // ---------------------------------------------------------- V to fp16
+    // a thread's 16 codes of one key become two 16-byte chunks of that key's
+    // row in a 64-column box; eight threads next to one another take four
+    // chunks of two keys, whose writes fall into different banks
+    const int ct = tid - 320;
+    constexpr int CH = D / 16, CT = CONVERT_WARPS * 32, VECS = BN * CH / CT;
+    for (int e = 0; e < n_steps; ++e) {
+      const int vt = e % VST, ws = e % WST;
+      bool ok = mbar_wait(meta_full + e % MST, (e / MST) & 1, abort_flag, g.dev_status);
+      ok = ok && mbar_wait(v_full + vt, (e / VST) & 1, abort_flag, g.dev_status);
+      // fp16 slot: P V of step e - WST has completed
+      if (ok && e >= WST) {
+        const int sd = e - WST + 1;
+        ok = mbar_wait(step_done + sd % SDR, (sd / SDR) & 1, abort_flag, g.dev_status);
+      }
+      if (!__all_sync(0xffffffffu, ok)) break;
+      const int left0 = meta[e % MST].left[0], left1 = meta[e % MST].left[1];
+      const uint8_t* src = smem + Lay::OFF_V + vt * Lay::CB;
+      uint8_t* dst = smem + Lay::OFF_W + ws * Lay::WB;
+#pragma unroll
+      for (int j = 0; j < VECS; ++j) {
+        const int x = j * CT + ct;
+        const int quad = x >> 3, r = (quad / (CH / 4)) * 2 + ((x >> 2) & 1), ch = (quad % (CH / 4)) * 4 + (x & 3);
+        uint4 c = *reinterpret_cast<const uint4*>(src + code_at<D>(r, ch));
+        const int kk = r & (HALF - 1);
+        if (kk >= (r < HALF ? left0 : left1)) c = make_uint4(0, 0, 0, 0);  // codes behind the last token may be anything
+        uint4 lo, hi;
+        codes_f16(c.x, lo.x, lo.y);
+        codes_f16(c.y, lo.z, lo.w);
+        codes_f16(c.z, hi.x, hi.y);
+        codes_f16(c.w, hi.z, hi.w);
+        uint8_t* box = dst + (ch >> 2) * (BN * 128) + r * 128;
+        const int c2 = (ch & 3) * 2;
+        *reinterpret_cast<uint4*>(box + ((c2 ^ (r & 7)) << 4)) = lo;
+        *reinterpret_cast<uint4*>(box + (((c2 + 1) ^ (r & 7)) << 4)) = hi;
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(v_free + vt);
+        mbar_arrive(w_full + ws);
+      }
+    }
+    }
+  } else {
+    regs_raise<REGS_SOFTMAX>();
+    // ------------------------------------------------------------ softmax
+    const int rt = warp / 4;
+    const int row = base + tid;  // tid is 0..255 here
+    const bool row_valid = row < rows;
+    const int t = t0 + row / p.group;
+    const int w_lo = t0 + (base + warp * 32) / p.group;
+    const int w_hi = t0 + (min(rows, base + warp * 32 + 32) - 1) / p.group;  // the warp's positions
+    const uint32_t lane_addr = tmem + ((uint32_t)((warp % 4) * 32) << 16);
+    const uint32_t s_col = rt * BN, o_col = 2 * BN + rt * BN;
+    const bool mine = rt == 0 || has_b;
+    float qs = 0.f;
+    if (mine && n_steps > 0) {
+      // the row of Q in its two e4m3 parts
+      const __nv_bfloat16* src = p.q.p + b * p.q.sb + (long long)(row / p.group) * p.q.sn +
+                                 (long long)(h * p.group + row % p.group) * p.q.sh;
+      uint4 w[D / 8];
+      uint32_t top = 0;
+#pragma unroll
+      for (int c = 0; c < D / 8; ++c) {
+        w[c] = row_valid ? *reinterpret_cast<const uint4*>(src + c * 8) : make_uint4(0, 0, 0, 0);
+        top = max(top, max(bf16x2_top(w[c].x), max(bf16x2_top(w[c].y), max(bf16x2_top(w[c].z), bf16x2_top(w[c].w)))));
+      }
+      float mul;
+      q_scale<7>(top, mul, qs);
+      qs *= fabsf(p.scale_log2);
+      mul = copysignf(mul, p.scale_log2);
+      uint8_t* qh = smem + Lay::OFF_Q + rt * 2 * Lay::QB;
+      const int r = tid & (BM - 1);
+#pragma unroll
+      for (int c = 0; c < D / 16; ++c) {
+        const uint32_t x[8] = {w[2 * c].x, w[2 * c].y, w[2 * c].z, w[2 * c].w,
+                               w[2 * c + 1].x, w[2 * c + 1].y, w[2 * c + 1].z, w[2 * c + 1].w};
+        uint32_t hi[4], lo[4];
+#pragma unroll
+        for (int y = 0; y < 4; ++y) split_e4m3x4(x[2 * y], x[2 * y + 1], mul, hi[y], lo[y]);
+        *reinterpret_cast<uint4*>(qh + code_at<D>(r, c)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        *reinterpret_cast<uint4*>(qh + Lay::QB + code_at<D>(r, c)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+      }
+      fence_proxy_async_smem();
+      mbar_arrive(q_full);
+    }
+    float m = -INFINITY, l = 0.f;
+    bool ok = true;
+    for (int e = 0; mine && e < n_steps; ++e) {
+      bool go = mbar_wait(meta_full + e % MST, (e / MST) & 1, abort_flag, g.dev_status);
+      go = go && mbar_wait(s_full + rt, e & 1, abort_flag, g.dev_status);
+      if (!__all_sync(0xffffffffu, go)) { ok = false; break; }
+      tc_fence_after();
+      const StepMeta& sm = meta[e % MST];
+      const float c0 = qs * sm.ks[0], c1 = qs * sm.ks[1], ev0 = sm.ev[0], ev1 = sm.ev[1];
+      Span sp0, sp1;
+      bool full = true;
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const int ps = sm.pos[x], left = sm.left[x];
+        full = full && left == HALF && (!p.causal || ps + HALF - 1 <= w_lo) &&
+               (p.window <= 0 || ps + HALF <= p.sinks || (long long)ps > (long long)w_hi - p.window);
+        Span& s = x ? sp1 : sp0;
+        const long long d = (long long)t - ps;
+        s.hi = p.causal ? (int)max(0ll, min((long long)left, d + 1)) : left;
+        s.lo = p.window > 0 ? (int)max(0ll, min((long long)HALF, d - p.window + 1)) : 0;
+        s.first = p.window > 0 ? (int)max(0ll, min((long long)HALF, (long long)p.sinks - ps)) : 0;
+      }
+      uint32_t u[BN];
+      tmem_ld128(lane_addr + s_col, u);
+      const uint32_t (&u0)[64] = *reinterpret_cast<const uint32_t(*)[64]>(&u[0]);
+      const uint32_t (&u1)[64] = *reinterpret_cast<const uint32_t(*)[64]>(&u[64]);
+      auto row_max = [&]() {  // of x = s*c + log2(V scale); c is not negative
+        return full ? fmaxf(half_max<true>(u0, sp0) * c0 + ev0, half_max<true>(u1, sp1) * c1 + ev1)
+                    : fmaxf(half_max<false>(u0, sp0) * c0 + ev0, half_max<false>(u1, sp1) * c1 + ev1);
+      };
+      if (__any_sync(0xffffffffu, m == -INFINITY)) {
+        const float mx = row_max();
+        if (m == -INFINITY) m = fmaxf(m, mx);  // no key before: O and l are 0
+      }
+      uint32_t pk0[32], pk1[32];
+      float sum0, sum1;
+      auto row_p = [&]() {
+        const float bias = OFF - (m == -INFINITY ? 0.f : m);
+        if (full) {
+          sum0 = half_p<true>(u0, sp0, c0, ev0 + bias, pk0);
+          sum1 = half_p<true>(u1, sp1, c1, ev1 + bias, pk1);
+        } else {
+          sum0 = half_p<false>(u0, sp0, c0, ev0 + bias, pk0);
+          sum1 = half_p<false>(u1, sp1, c1, ev1 + bias, pk1);
+        }
+      };
+      row_p();
+      const bool redo = !(sum0 + sum1 <= OVERFLOW_SUM);
+      if (__any_sync(0xffffffffu, redo)) {
+        tmem_ld128(lane_addr + s_col, u);
+        const float mx = row_max();
+        const float m_new = redo ? fmaxf(m, mx) : m;
+        const float alpha = m_new == m ? 1.f : fast_exp2(m - m_new);
+        if (e > 0) {
+          // O holds P V of all earlier steps: S of this one was issued behind them
+#pragma unroll
+          for (int c = 0; c < D / 32; ++c) {
+            uint32_t o[32];
+            tmem_ld32(lane_addr + o_col + c * 32, o);
+#pragma unroll
+            for (int y = 0; y < 32; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * alpha);
+            tmem_st32(lane_addr + o_col + c * 32, o);
+          }
+        }
+        l *= alpha;
+        m = m_new;
+        row_p();
+      }
+      tmem_st32_async(lane_addr + s_col + 64, pk0);
+      tmem_st32_async(lane_addr + s_col + 96, pk1);
+      tmem_wait_st_keep(pk0, pk1);
+      tc_fence_before();
+      mbar_arrive(p_full + rt);
+      l += (sum0 == 0.f ? 0.f : sum0 * sm.rv[0]) + (sum1 == 0.f ? 0.f : sum1 * sm.rv[1]);
+      if (p.lw && row_valid) {
+        const float off = (m == -INFINITY ? 0.f : m) - OFF;
+        float* dst = p.lw + (long long)bh * p.pieces_cap * p.rows_cap + row;
+        if (per_step == 1) {
+          if (sm.entry[0] >= 0) dst[(long long)sm.entry[0] * p.rows_cap] =
+              sum0 + sum1 == 0.f ? -INFINITY : log2f(sum0 + sum1) + (off - ev0);
+        } else {
+          if (sm.entry[0] >= 0) dst[(long long)sm.entry[0] * p.rows_cap] = sum0 == 0.f ? -INFINITY : log2f(sum0) + (off - ev0);
+          if (sm.entry[1] >= 0) dst[(long long)sm.entry[1] * p.rows_cap] = sum1 == 0.f ? -INFINITY : log2f(sum1) + (off - ev1);
+        }
+      }
+    }
+    // O / l, or this split's part of them
+    const long long prow = ((long long)bh * p.splits + sp) * p.rows_pad + row;
+    bool have = false;
+    if (ok && mine && n_steps > 0) {
+      have = __all_sync(0xffffffffu, mbar_wait(pv_done + rt, 0, abort_flag, g.dev_status));
+      tc_fence_after();
+    }
+    if (mine) {
+      const float inv = l == 0.f ? 0.f : 1.0f / l;
+      const int qh = h * p.group + row % p.group, i = row / p.group;
+      __nv_bfloat16* dst = p.o + b * p.o_sb + (long long)i * p.o_sn + (long long)qh * p.o_sh;
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c) {
+        uint32_t u[32];
+        if (have) {
+          tmem_ld32(lane_addr + o_col + c * 32, u);
+        } else {
+#pragma unroll
+          for (int y = 0; y < 32; ++y) u[y] = 0u;
+        }
+        if (row_valid && p.splits > 1) {
+          float4* d4 = reinterpret_cast<float4*>(p.part_o + prow * D + c * 32);
+#pragma unroll
+          for (int y = 0; y < 8; ++y)
+            d4[y] = make_float4(__uint_as_float(u[4 * y]), __uint_as_float(u[4 * y + 1]), __uint_as_float(u[4 * y + 2]),
+                                __uint_as_float(u[4 * y + 3]));
+        } else if (row_valid) {
+          uint4* d4 = reinterpret_cast<uint4*>(dst + c * 32);
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            uint32_t x[4];
+#pragma unroll
+            for (int z = 0; z < 4; ++z)
+              x[z] = pack_bf16x2_rn(l == 0.f ? 0.f : __uint_as_float(u[8 * y + 2 * z]) * inv,
+                                    l == 0.f ? 0.f : __uint_as_float(u[8 * y + 2 * z + 1]) * inv);
+            d4[y] = make_uint4(x[0], x[1], x[2], x[3]);
+          }
+        }
+        __syncwarp();
+      }
+      if (row_valid) {
+        if (p.splits > 1) {
+          p.part_ml[prow] = make_float2(m, l);
+        } else {
+          const float l2 = l == 0.f ? -INFINITY : log2f(l) + (m == -INFINITY ? 0.f : m) - OFF;
+          if (p.lse) p.lse[((long long)b * p.heads + qh) * p.n_q + i] = l2 * LN2;
+          if (p.lse2) p.lse2[(long long)bh * p.rows_cap + row] = l2;
+        }
+      }
+    }
+    tc_fence_before();
+  }
+  __syncthreads();
+  if (warp == 9) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+template <int D>
+cudaError_t launch(const KvGeom& g, const KvAttnParams& p, cudaStream_t s) {
+  KvMaps maps;
+  const uint64_t rows = (uint64_t)g.n_slots * g.tile;
+  if (encode_tensor_map_2d_u8(&maps.k, g.k8, D, rows, HALF) != CUDA_SUCCESS ||
+      encode_tensor_map_2d_u8(&maps.v, g.v8, D, rows, HALF) != CUDA_SUCCESS)
+    return cudaErrorInvalidValue;
+  const cudaError_t e =
+      cudaFuncSetAttribute(kv_attn_tiles_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, TileLayout<D>::ALLOC);
+  if (e != cudaSuccess) return e;
+  kv_attn_tiles_kernel<D><<<dim3(p.row_tiles * p.splits, g.hkv, g.B), THREADS, TileLayout<D>::ALLOC, s>>>(g, p, maps);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_kv_attn_tiles(const KvGeom& g, const KvAttnParams& p, cudaStream_t s) {
+  return g.d == 128 ? launch<128>(g, p, s) : launch<64>(g, p, s);
+}
+
+}  // namespace veda

@@ -110,11 +110,13 @@ class Cache:
         A = sum p |v| and S = scale * sum |q| |k| (largest over its keys):
         o [B, n, heads, d], lse [B, heads, n], weight [B, hkv, nb_cap] (NaN
         where not written), A like o, S like lse, and R like lse: the largest
-        p_j times its tile's V scale."""
+        p_j times its tile's V scale; Q likewise, scale * max |q| * sum |k|
+        (largest over its keys)."""
         B, n, heads, d = q.shape
         g = heads // self.hkv
         o, A = np.full(q.shape, np.nan), np.full(q.shape, np.nan)
         lse, S, R = np.full((B, heads, n), np.nan), np.zeros((B, heads, n)), np.zeros((B, heads, n))
+        Q = np.zeros((B, heads, n))
         weight = np.full(self.table.shape, np.nan)
         written = np.zeros(self.table.shape, bool)
         for b in range(B):
@@ -150,13 +152,15 @@ class Cache:
                         sick = (see & bad[None, :]).any(1)
                         o[b, :m, j][sick] = np.nan
                         S[b, j, :m] = np.max(np.where(see, np.abs(q[b, :m, j]) @ np.abs(K).T, 0.0), axis=1, initial=0.0) * abs(scale)
+                        top = np.abs(q[b, :m, j]).max(-1) * abs(scale)
+                        Q[b, j, :m] = top * np.max(np.where(see, np.abs(K).sum(-1)[None, :], 0.0), axis=1, initial=0.0)
                         # a V tile without a scale also spoils the row's sum
                         lse[b, j, :m][sick] = np.nan
                         p = np.where(sick[:, None], np.nan, p)
                         acc[:total] += np.where(see, p, 0.0).sum(0)
                 weight[b, h, :nb] = acc.reshape(nb, self.tile).sum(1)
                 written[b, h, :nb] = True
-        return o, lse, weight, written, A, S, R
+        return o, lse, weight, written, A, S, R, Q
 
     def evict(self, keep, sink, recent):
         for b in range(self.B):

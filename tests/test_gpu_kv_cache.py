@@ -8,7 +8,11 @@ Tolerances of attention, per element. K and V are exact (codes times scales).
           (the tensor core may truncate each partial sum, hence 2^-23), and
           the exponent's argument, at most 2 S in magnitude next to its
           reference, and ex2 another 2^-22 * (1 + 4 S): D = 2^-16 * (1 + S)
-          covers both for d <= 128.
+          covers both for d <= 128. With more query rows per K/V head than
+          FEW, q is taken in two e4m3 parts, each row scaled so that its
+          largest value is at 2^7 or above: what is left is half a step of
+          e4m3's subnormals, 2^-10, at most: 2^-17 of max |q|, and D grows
+          by 2^-17 * Q, Q = scale * max |q| * sum |k|.
   P       fp16, relative to the largest p_j sv_j =: R of the row, which is at
           2^7 or above: 2^-11 of each weight, and 2^-25 where it is subnormal,
           that is 2^-32 R per key, times a code of up to 448 in any channel
@@ -27,6 +31,7 @@ from oracle.kv_oracle import Cache
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda:0"
+FEW = 32          # query rows per K/V head up to which q is taken whole, in fp16
 
 
 def host(t):
@@ -101,14 +106,14 @@ def check_attention(c, q, news=None, causal=True, window=0, sinks=0, pending=Tru
     before = o.clone()
     lse = torch.full((B, heads, n), 7.0, device=DEV)
     w0 = host(c.weight)
-    want_o, want_l, want_w, wrote, A, S, R = oracle_of(c).attend(host(q), [n] * B if news is None else news, scale,
+    want_o, want_l, want_w, wrote, A, S, R, Q = oracle_of(c).attend(host(q), [n] * B if news is None else news, scale,
                                                                  causal, window, sinks, pending)
     nn = None if news is None else torch.tensor(news, dtype=torch.int32, device=DEV)
     V.veda_kv_attn(c, q, o, scale, workspace(c, heads, n, weight), causal=causal, window=window, sinks=sinks, n_new=nn,
                    pending=pending, lse=lse, weight=c.weight if weight else None, decay=decay)
     V.veda_kv_check_status(c)
     keys = c.nb_cap * c.tile
-    D = 2.0 ** -16 * (1 + S)                                             # [B, heads, n]
+    D = 2.0 ** -16 * (1 + S) + (2.0 ** -17 * Q if n * heads // c.heads_kv > FEW else 0.0)      # [B, heads, n]
     for b in range(B):
         m = n if news is None else news[b]
         # rows behind the sequence's own are left as they were
