@@ -34,7 +34,10 @@ namespace {
 constexpr int BM = 128, BN = 128;
 constexpr int HALF = 64;               // keys per TMA box; a step is two halves
 constexpr int KST = 3, VST = 2, WST = 2;  // stages: K codes, V codes, V fp16
-constexpr int MST = KST + 2;           // step descriptions
+// Step descriptions: written before the step's copies are announced, so whoever
+// has seen those copies (or an MMA on them) complete can read them; a slot is
+// written again only after the softmax of the step before step_done's.
+constexpr int MST = KST + 2;
 constexpr int SDR = 4;                 // step-done barriers
 constexpr float OVERFLOW_SUM = 32768.f;
 constexpr int THREADS = 384, CONVERT_WARPS = 2;
@@ -45,6 +48,8 @@ struct StepMeta {
   float ks[2], ev[2], rv[2];  // K scale, log2 of the V scale, its inverse
   int pos[2], left[2];        // first position, keys that exist
   int entry[2];               // table entry, -1 for none
+  int full;                   // every query of the CTA sees all 128 keys
+  int pad;
 };
 
 template <int D>
@@ -58,37 +63,44 @@ struct TileLayout {
   static constexpr int OFF_W = OFF_V + VST * CB;
   static constexpr int OFF_META = OFF_W + WST * WB;
   static constexpr int OFF_BAR = OFF_META + MST * (int)sizeof(StepMeta);
-  static constexpr int NUM_BARS = 1 + KST + 2 * VST + WST + MST + SDR + 2 + 2 + 2 + 1;
+  static constexpr int NUM_BARS = 1 + KST + 2 * VST + WST + SDR + 2 + 2 + 2 + 1;
   static constexpr int OFF_MISC = OFF_BAR + NUM_BARS * 8;
   static constexpr int ALLOC = OFF_MISC + 32 + 1024;
 };
 static_assert(sizeof(StepMeta) % 8 == 0, "barriers follow");
 
-// Visible keys of one half for one row: k < hi && (k >= lo || k < first).
-struct Span {
-  int lo, hi, first;
-  __device__ bool has(int k) const { return k < hi && (k >= lo || k < first); }
-};
+// The keys of one half that the query at position t sees, as bits.
+__device__ __forceinline__ uint64_t half_seen(const KvAttnParams& p, int t, int pos, int left) {
+  auto below = [](long long n) { return n >= HALF ? ~0ull : n <= 0 ? 0ull : (1ull << n) - 1ull; };
+  const long long d = (long long)t - pos;
+  uint64_t seen = below(left);
+  if (p.causal) seen &= below(d + 1);
+  if (p.window > 0) seen &= ~below(d - p.window + 1) | below((long long)p.sinks - pos);
+  return seen;
+}
 
-template <bool FULL>
-__device__ __forceinline__ float half_max(const uint32_t (&u)[64], const Span& sp) {
+__device__ __forceinline__ void half_mask(uint32_t (&u)[64], uint64_t seen) {
+  const uint32_t lo = (uint32_t)seen, hi = (uint32_t)(seen >> 32);
+#pragma unroll
+  for (int k = 0; k < 32; ++k) {
+    if (!(lo >> k & 1u)) u[k] = 0xff800000u;
+    if (!(hi >> k & 1u)) u[32 + k] = 0xff800000u;
+  }
+}
+
+__device__ __forceinline__ float half_max(const uint32_t (&u)[64]) {
   float pm[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) pm[i] = -INFINITY;
+  for (int i = 0; i < 8; ++i) pm[i] = fmaxf(__uint_as_float(u[i]), __uint_as_float(u[8 + i]));
 #pragma unroll
-  for (int c = 0; c < 64; c += 16)
+  for (int c = 16; c < 64; c += 16)
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float v0 = (FULL || sp.has(c + i)) ? __uint_as_float(u[c + i]) : -INFINITY;
-      const float v1 = (FULL || sp.has(c + 8 + i)) ? __uint_as_float(u[c + 8 + i]) : -INFINITY;
-      pm[i] = fmax3(pm[i], v0, v1);
-    }
+    for (int i = 0; i < 8; ++i) pm[i] = fmax3(pm[i], __uint_as_float(u[c + i]), __uint_as_float(u[c + 8 + i]));
   return fmax3(fmax3(pm[0], pm[1], pm[2]), fmax3(pm[3], pm[4], pm[5]), fmaxf(pm[6], pm[7]));
 }
 
 // P = 2^(s*c + nm) of one half as fp16 pairs; returns the sum of the fp32 values.
-template <bool FULL>
-__device__ __forceinline__ float half_p(const uint32_t (&u)[64], const Span& sp, float c, float nm, uint32_t (&pk)[32]) {
+__device__ __forceinline__ float half_p(const uint32_t (&u)[64], float c, float nm, uint32_t (&pk)[32]) {
   const uint64_t C2 = f2(c, c), NM = f2(nm, nm);
   uint64_t acc[4];
 #pragma unroll
@@ -98,11 +110,7 @@ __device__ __forceinline__ float half_p(const uint32_t (&u)[64], const Span& sp,
     const uint64_t x = f2_fma(f2(__uint_as_float(u[2 * w]), __uint_as_float(u[2 * w + 1])), C2, NM);
     float x0, x1;
     f2_split(x, x0, x1);
-    float p0 = fast_exp2(x0), p1 = fast_exp2(x1);
-    if (!FULL) {
-      p0 = sp.has(2 * w) ? p0 : 0.f;
-      p1 = sp.has(2 * w + 1) ? p1 : 0.f;
-    }
+    const float p0 = fast_exp2(x0), p1 = fast_exp2(x1);
     acc[w & 3] = f2_add(acc[w & 3], f2(p0, p1));
     pk[w] = pack_f16x2(p0, p1);
   }
@@ -158,8 +166,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   uint64_t* v_full = k_full + KST;
   uint64_t* v_free = v_full + VST;   // an arrival per converting warp: it has read the codes
   uint64_t* w_full = v_free + VST;   // an arrival per converting warp
-  uint64_t* meta_full = w_full + WST;
-  uint64_t* step_done = meta_full + MST;  // S of step e and P V of e-1 have completed
+  uint64_t* step_done = w_full + WST;  // S of step e and P V of e-1 have completed
   uint64_t* s_full = step_done + SDR;     // [2]
   uint64_t* p_full = s_full + 2;          // [2], 128 arrivals
   uint64_t* pv_done = p_full + 2;         // [2]
@@ -235,6 +242,9 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (e >= KST) ok = mbar_wait(step_done + (e - KST) % SDR, ((e - KST) / SDR) & 1, abort_flag, g.dev_status);
         if (ok && e >= VST) ok = mbar_wait(v_free + vt, (e / VST - 1) & 1, abort_flag, g.dev_status);
         if (!__all_sync(0xffffffffu, ok)) break;
+        const bool seen = left == HALF && (!p.causal || pos + HALF - 1 <= t_lo) &&
+                          (p.window <= 0 || pos + HALF <= p.sinks || (long long)pos > (long long)t_hi - p.window);
+        const int both = (__ballot_sync(0xffffffffu, seen) >> l0 & 3u) == 3u;
         if (lane == l0 || lane == l0 + 1) {
           const int x = lane & 1;
           StepMeta& m = meta[ms];
@@ -244,11 +254,11 @@ __global__ void __launch_bounds__(THREADS, 1)
           m.pos[x] = pos;
           m.left[x] = left;
           m.entry[x] = entry;
+          m.full = both;
         }
         const int row0 = __shfl_sync(0xffffffffu, pool, l0), row1 = __shfl_sync(0xffffffffu, pool, l0 + 1);
         __syncwarp();
         if (lane == 0) {
-          mbar_arrive(meta_full + ms);
           const uint32_t bytes = (row0 >= 0 ? Lay::CB / 2 : 0) + (row1 >= 0 ? Lay::CB / 2 : 0);
           uint8_t* kd = smem + Lay::OFF_K + st * Lay::CB;
           uint8_t* vd = smem + Lay::OFF_V + vt * Lay::CB;
@@ -320,8 +330,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     constexpr int CH = D / 16, CT = CONVERT_WARPS * 32, VECS = BN * CH / CT;
     for (int e = 0; e < n_steps; ++e) {
       const int vt = e % VST, ws = e % WST;
-      bool ok = mbar_wait(meta_full + e % MST, (e / MST) & 1, abort_flag, g.dev_status);
-      ok = ok && mbar_wait(v_full + vt, (e / VST) & 1, abort_flag, g.dev_status);
+      bool ok = mbar_wait(v_full + vt, (e / VST) & 1, abort_flag, g.dev_status);
       // fp16 slot: P V of step e - WST has completed
       if (ok && e >= WST) {
         const int sd = e - WST + 1;
@@ -331,22 +340,32 @@ __global__ void __launch_bounds__(THREADS, 1)
       const int left0 = meta[e % MST].left[0], left1 = meta[e % MST].left[1];
       const uint8_t* src = smem + Lay::OFF_V + vt * Lay::CB;
       uint8_t* dst = smem + Lay::OFF_W + ws * Lay::WB;
+      constexpr int BATCH = 8;  // loads in flight
 #pragma unroll
-      for (int j = 0; j < VECS; ++j) {
-        const int x = j * CT + ct;
-        const int quad = x >> 3, r = (quad / (CH / 4)) * 2 + ((x >> 2) & 1), ch = (quad % (CH / 4)) * 4 + (x & 3);
-        uint4 c = *reinterpret_cast<const uint4*>(src + code_at<D>(r, ch));
-        const int kk = r & (HALF - 1);
-        if (kk >= (r < HALF ? left0 : left1)) c = make_uint4(0, 0, 0, 0);  // codes behind the last token may be anything
-        uint4 lo, hi;
-        codes_f16(c.x, lo.x, lo.y);
-        codes_f16(c.y, lo.z, lo.w);
-        codes_f16(c.z, hi.x, hi.y);
-        codes_f16(c.w, hi.z, hi.w);
-        uint8_t* box = dst + (ch >> 2) * (BN * 128) + r * 128;
-        const int c2 = (ch & 3) * 2;
-        *reinterpret_cast<uint4*>(box + ((c2 ^ (r & 7)) << 4)) = lo;
-        *reinterpret_cast<uint4*>(box + (((c2 + 1) ^ (r & 7)) << 4)) = hi;
+      for (int j0 = 0; j0 < VECS; j0 += BATCH) {
+        uint4 c[BATCH];
+#pragma unroll
+        for (int j = 0; j < BATCH; ++j) {
+          const int x = (j0 + j) * CT + ct, quad = x >> 3;
+          const int r = (quad / (CH / 4)) * 2 + ((x >> 2) & 1), ch = (quad % (CH / 4)) * 4 + (x & 3);
+          c[j] = *reinterpret_cast<const uint4*>(src + code_at<D>(r, ch));
+          // codes behind the last token may be anything
+          if ((r & (HALF - 1)) >= (r < HALF ? left0 : left1)) c[j] = make_uint4(0, 0, 0, 0);
+        }
+#pragma unroll
+        for (int j = 0; j < BATCH; ++j) {
+          const int x = (j0 + j) * CT + ct, quad = x >> 3;
+          const int r = (quad / (CH / 4)) * 2 + ((x >> 2) & 1), ch = (quad % (CH / 4)) * 4 + (x & 3);
+          uint4 lo, hi;
+          codes_f16(c[j].x, lo.x, lo.y);
+          codes_f16(c[j].y, lo.z, lo.w);
+          codes_f16(c[j].z, hi.x, hi.y);
+          codes_f16(c[j].w, hi.z, hi.w);
+          uint8_t* box = dst + (ch >> 2) * (BN * 128) + r * 128;
+          const int c2 = (ch & 3) * 2;
+          *reinterpret_cast<uint4*>(box + ((c2 ^ (r & 7)) << 4)) = lo;
+          *reinterpret_cast<uint4*>(box + (((c2 + 1) ^ (r & 7)) << 4)) = hi;
+        }
       }
       fence_proxy_async_smem();
       __syncwarp();
@@ -402,71 +421,58 @@ __global__ void __launch_bounds__(THREADS, 1)
     float m = -INFINITY, l = 0.f;
     bool ok = true;
     for (int e = 0; mine && e < n_steps; ++e) {
-      bool go = mbar_wait(meta_full + e % MST, (e / MST) & 1, abort_flag, g.dev_status);
-      go = go && mbar_wait(s_full + rt, e & 1, abort_flag, g.dev_status);
-      if (!__all_sync(0xffffffffu, go)) { ok = false; break; }
+      if (!__all_sync(0xffffffffu, mbar_wait(s_full + rt, e & 1, abort_flag, g.dev_status))) { ok = false; break; }
       tc_fence_after();
       const StepMeta& sm = meta[e % MST];
-      const float c0 = qs * sm.ks[0], c1 = qs * sm.ks[1], ev0 = sm.ev[0], ev1 = sm.ev[1];
-      Span sp0, sp1;
-      bool full = true;
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        const int ps = sm.pos[x], left = sm.left[x];
-        full = full && left == HALF && (!p.causal || ps + HALF - 1 <= w_lo) &&
-               (p.window <= 0 || ps + HALF <= p.sinks || (long long)ps > (long long)w_hi - p.window);
-        Span& s = x ? sp1 : sp0;
-        const long long d = (long long)t - ps;
-        s.hi = p.causal ? (int)max(0ll, min((long long)left, d + 1)) : left;
-        s.lo = p.window > 0 ? (int)max(0ll, min((long long)HALF, d - p.window + 1)) : 0;
-        s.first = p.window > 0 ? (int)max(0ll, min((long long)HALF, (long long)p.sinks - ps)) : 0;
+      float c0 = qs * sm.ks[0], c1 = qs * sm.ks[1], ev0 = sm.ev[0], ev1 = sm.ev[1];
+      const bool full = sm.full;
+      uint64_t seen0 = 0, seen1 = 0;
+      if (!full) {
+        // a hidden key's logit is -inf, which the coefficient must leave so: it
+        // is not 0, and a NaN one only counts where the row sees the half
+        seen0 = half_seen(p, t, sm.pos[0], sm.left[0]);
+        seen1 = half_seen(p, t, sm.pos[1], sm.left[1]);
+        if (!seen0 || c0 == 0.f) c0 = 1e-37f;
+        if (!seen1 || c1 == 0.f) c1 = 1e-37f;
+        if (!seen0) ev0 = 0.f;
+        if (!seen1) ev1 = 0.f;
       }
-      uint32_t u[BN];
-      tmem_ld128(lane_addr + s_col, u);
-      const uint32_t (&u0)[64] = *reinterpret_cast<const uint32_t(*)[64]>(&u[0]);
-      const uint32_t (&u1)[64] = *reinterpret_cast<const uint32_t(*)[64]>(&u[64]);
-      auto row_max = [&]() {  // of x = s*c + log2(V scale); c is not negative
-        return full ? fmaxf(half_max<true>(u0, sp0) * c0 + ev0, half_max<true>(u1, sp1) * c1 + ev1)
-                    : fmaxf(half_max<false>(u0, sp0) * c0 + ev0, half_max<false>(u1, sp1) * c1 + ev1);
-      };
-      if (__any_sync(0xffffffffu, m == -INFINITY)) {
-        const float mx = row_max();
-        if (m == -INFINITY) m = fmaxf(m, mx);  // no key before: O and l are 0
-      }
-      uint32_t pk0[32], pk1[32];
+      uint32_t u[BN], pk0[32], pk1[32];
+      uint32_t (&u0)[64] = *reinterpret_cast<uint32_t(*)[64]>(&u[0]);
+      uint32_t (&u1)[64] = *reinterpret_cast<uint32_t(*)[64]>(&u[64]);
       float sum0, sum1;
-      auto row_p = [&]() {
+      float alpha = 1.f;
+      bool move = m == -INFINITY;  // the reference has to be found; in a second pass: found again
+      for (int pass = 0;; ++pass) {
+        tmem_ld128(lane_addr + s_col, u);  // P is not stored yet, so S is intact in a second pass
+        if (!full) {
+          half_mask(u0, seen0);
+          half_mask(u1, seen1);
+        }
+        if (__any_sync(0xffffffffu, move)) {
+          const float mx = fmaxf(half_max(u0) * c0 + ev0, half_max(u1) * c1 + ev1);
+          const float m_new = move ? fmaxf(m, mx) : m;
+          alpha = m_new == m ? 1.f : fast_exp2(m - m_new);
+          m = m_new;
+        }
         const float bias = OFF - (m == -INFINITY ? 0.f : m);
-        if (full) {
-          sum0 = half_p<true>(u0, sp0, c0, ev0 + bias, pk0);
-          sum1 = half_p<true>(u1, sp1, c1, ev1 + bias, pk1);
-        } else {
-          sum0 = half_p<false>(u0, sp0, c0, ev0 + bias, pk0);
-          sum1 = half_p<false>(u1, sp1, c1, ev1 + bias, pk1);
-        }
-      };
-      row_p();
-      const bool redo = !(sum0 + sum1 <= OVERFLOW_SUM);
-      if (__any_sync(0xffffffffu, redo)) {
-        tmem_ld128(lane_addr + s_col, u);
-        const float mx = row_max();
-        const float m_new = redo ? fmaxf(m, mx) : m;
-        const float alpha = m_new == m ? 1.f : fast_exp2(m - m_new);
-        if (e > 0) {
-          // O holds P V of all earlier steps: S of this one was issued behind them
-#pragma unroll
-          for (int c = 0; c < D / 32; ++c) {
-            uint32_t o[32];
-            tmem_ld32(lane_addr + o_col + c * 32, o);
-#pragma unroll
-            for (int y = 0; y < 32; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * alpha);
-            tmem_st32(lane_addr + o_col + c * 32, o);
-          }
-        }
-        l *= alpha;
-        m = m_new;
-        row_p();
+        sum0 = half_p(u0, c0, ev0 + bias, pk0);
+        sum1 = half_p(u1, c1, ev1 + bias, pk1);
+        move = !(sum0 + sum1 <= OVERFLOW_SUM);
+        if (pass == 1 || !__any_sync(0xffffffffu, move)) break;
       }
+      if (__any_sync(0xffffffffu, alpha != 1.f && l != 0.f)) {
+        // O holds P V of all earlier steps: S of this one was issued behind them
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t o[32];
+          tmem_ld32(lane_addr + o_col + c * 32, o);
+#pragma unroll
+          for (int y = 0; y < 32; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * alpha);
+          tmem_st32(lane_addr + o_col + c * 32, o);
+        }
+      }
+      l *= alpha;
       tmem_st32_async(lane_addr + s_col + 64, pk0);
       tmem_st32_async(lane_addr + s_col + 96, pk1);
       tmem_wait_st_keep(pk0, pk1);
@@ -478,10 +484,10 @@ __global__ void __launch_bounds__(THREADS, 1)
         float* dst = p.lw + (long long)bh * p.pieces_cap * p.rows_cap + row;
         if (per_step == 1) {
           if (sm.entry[0] >= 0) dst[(long long)sm.entry[0] * p.rows_cap] =
-              sum0 + sum1 == 0.f ? -INFINITY : log2f(sum0 + sum1) + (off - ev0);
+              sum0 + sum1 == 0.f ? -INFINITY : log2f(sum0 + sum1) + (off - sm.ev[0]);
         } else {
-          if (sm.entry[0] >= 0) dst[(long long)sm.entry[0] * p.rows_cap] = sum0 == 0.f ? -INFINITY : log2f(sum0) + (off - ev0);
-          if (sm.entry[1] >= 0) dst[(long long)sm.entry[1] * p.rows_cap] = sum1 == 0.f ? -INFINITY : log2f(sum1) + (off - ev1);
+          if (sm.entry[0] >= 0) dst[(long long)sm.entry[0] * p.rows_cap] = sum0 == 0.f ? -INFINITY : log2f(sum0) + (off - sm.ev[0]);
+          if (sm.entry[1] >= 0) dst[(long long)sm.entry[1] * p.rows_cap] = sum1 == 0.f ? -INFINITY : log2f(sum1) + (off - sm.ev[1]);
         }
       }
     }
