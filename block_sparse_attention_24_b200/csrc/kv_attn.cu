@@ -12,6 +12,8 @@
 // pair converts to in one instruction) holds it. OFF keeps what lies 2^-31
 // below the reference out of fp16's zero: even a million such keys add less
 // than a part in a thousand. Sums, references and O are fp32.
+#include <cmath>
+
 #include "kv_attn.cuh"
 
 namespace veda {
@@ -367,8 +369,17 @@ __global__ void __launch_bounds__(128) kv_join_kernel(const KvGeom g, const KvAt
     const float f = x.x == -INFINITY ? (x.y == x.y ? 0.f : 1.f) : fast_exp2(x.x - m);
     l += x.y * f;
     const float* src = p.part_o + (((long long)bh * p.splits + s) * rows + r) * D + lane * (D / 32);
-#pragma unroll
-    for (int e = 0; e < D / 32; ++e) o[e] += src[e] * f;
+    if constexpr (D == 128) {
+      const float4 v = *reinterpret_cast<const float4*>(src);
+      o[0] += v.x * f;
+      o[1] += v.y * f;
+      o[2] += v.z * f;
+      o[3] += v.w * f;
+    } else {
+      const float2 v = *reinterpret_cast<const float2*>(src);
+      o[0] += v.x * f;
+      o[1] += v.y * f;
+    }
   }
   const bool none = l == 0.f;
   const float inv = none ? 0.f : 1.0f / l;
@@ -388,7 +399,7 @@ __global__ void __launch_bounds__(128) kv_join_kernel(const KvGeom g, const KvAt
 
 // weight[tile] = decay * weight[tile] + sum over rows and the tile's pieces of
 // 2^(lw - lse2): a block per tile, its sums joined in a fixed order.
-constexpr int WEIGHT_THREADS = 128;
+constexpr int WEIGHT_THREADS = 256;  // a row tile's rows at most
 __global__ void __launch_bounds__(WEIGHT_THREADS) kv_weight_kernel(const KvGeom g, const KvAttnParams p) {
   __shared__ float part[WEIGHT_THREADS / 32];
   const int i = blockIdx.x, h = blockIdx.y, b = blockIdx.z, tid = threadIdx.x;
@@ -402,10 +413,11 @@ __global__ void __launch_bounds__(WEIGHT_THREADS) kv_weight_kernel(const KvGeom 
   const float* lse2 = p.lse2 + (long long)bh * p.rows_cap;
   const float* lw = p.lw + ((long long)bh * p.pieces_cap + (long long)i * ppt) * p.rows_cap;
   float w = 0.f;
-  for (int r = tid; r < rows; r += WEIGHT_THREADS) {
-    // only tiles that the row's whole CTA could see were visited
-    const int m0 = r / p.tile_rows * p.tile_rows, m1 = min(rows, m0 + p.tile_rows) - 1;
-    if (!kv_tile_seen(ps, g.tile, t0 + m0 / p.group, t0 + m1 / p.group, p.causal, p.window, p.sinks)) continue;
+  // row tile by row tile: only tiles that a row tile's CTA could see were visited
+#pragma unroll 4
+  for (int m0 = 0; m0 < rows; m0 += p.tile_rows) {
+    const int m1 = min(rows, m0 + p.tile_rows) - 1, r = m0 + tid;
+    if (r > m1 || !kv_tile_seen(ps, g.tile, t0 + m0 / p.group, t0 + m1 / p.group, p.causal, p.window, p.sinks)) continue;
     const float z = lse2[r];
     if (z == -INFINITY) continue;
     for (int k = 0; k < ppt && i * g.tile + k * p.piece < total; ++k) {
@@ -439,6 +451,9 @@ cudaError_t launch_rows(const KvGeom& g, const KvAttnParams& p, cudaStream_t s) 
 
 }  // namespace
 
+// Tokens that the rows of a row tile span.
+static int n_tok(int rows, int group) { return (rows + group - 1) / group + 1; }
+
 size_t kv_attn_plan(const KvGeom& g, KvAttnParams& p, bool weights, uint8_t* ws) {
   const long long rows = (long long)p.n_q * p.group;
   p.tiles = rows > TILE_KERNEL_ROWS;
@@ -449,10 +464,28 @@ size_t kv_attn_plan(const KvGeom& g, KvAttnParams& p, bool weights, uint8_t* ws)
   p.piece = p.tiles ? g.tile : PIECE;
   p.pieces_cap = g.nb_cap * (g.tile / p.piece);
   const long long ctas = (long long)g.B * g.hkv * p.row_tiles, keys = (long long)g.nb_cap * g.tile;
-  const long long want = ((p.tiles ? 148 * 2 : 148 * 6) + ctas - 1) / ctas;
-  const long long most = p.tiles ? (keys + 511) / 512 : (keys + PIECE * WARPS - 1) / (PIECE * WARPS);
-  p.splits = (int)(want < most ? want : most);
-  if (p.splits < 1) p.splits = 1;
+  p.splits = 1;
+  if (p.tiles) {
+    // One CTA per SM: waves of CTAs, each as long as its steps and what begins
+    // and ends it; what is split is written and read once more and joined.
+    // Measured at d = 128: 2.1 us a step, 5 us a CTA, 8 us for the join.
+    const long long see = p.window > 0 ? (long long)p.window + p.sinks + n_tok(p.tile_rows, p.group) + 2 * g.tile : keys;
+    const double steps = (double)((see < keys ? see : keys) + 127) / 128, t = 2.1 * g.d / 128;
+    double best = 0;
+    for (int s = 1; s <= 32 && (s == 1 || steps >= 3 * s); ++s) {
+      const double waves = (double)((ctas * s + 147) / 148);
+      const double us = waves * (ceil(steps / s) * t + 5) +
+                        (s > 1 ? 8 + (double)ctas * s * p.tile_rows * g.d * 8 / 4e6 : 0);
+      if (s == 1 || us < best) {
+        best = us;
+        p.splits = s;
+      }
+    }
+  } else {
+    const long long want = (148 * 6 + ctas - 1) / ctas, most = (keys + PIECE * WARPS - 1) / (PIECE * WARPS);
+    p.splits = (int)(want < most ? want : most);
+    if (p.splits < 1) p.splits = 1;
+  }
   size_t off = 0;
   auto take = [&](size_t bytes) {
     uint8_t* at = ws ? ws + off : nullptr;

@@ -187,6 +187,10 @@ __global__ void __launch_bounds__(THREADS, 1)
     fence_mbar_init();
   }
   if (tid < 3) sm_cnt[tid] = 0;
+  if (tid == 256) {
+    tma_prefetch_desc(&maps.k);
+    tma_prefetch_desc(&maps.v);
+  }
   if (warp == 9) {
     tmem_alloc(tmem_slot, 512);
     tmem_relinquish();
@@ -387,34 +391,41 @@ __global__ void __launch_bounds__(THREADS, 1)
     const uint32_t lane_addr = tmem + ((uint32_t)((warp % 4) * 32) << 16);
     const uint32_t s_col = rt * BN, o_col = 2 * BN + rt * BN;
     const bool mine = rt == 0 || has_b;
+    uint8_t* own = smem + Lay::OFF_Q + rt * 2 * Lay::QB;  // the row tile's Q, and its O at the end
     float qs = 0.f;
     if (mine && n_steps > 0) {
-      // the row of Q in its two e4m3 parts
-      const __nv_bfloat16* src = p.q.p + b * p.q.sb + (long long)(row / p.group) * p.q.sn +
-                                 (long long)(h * p.group + row % p.group) * p.q.sh;
-      uint4 w[D / 8];
-      uint32_t top = 0;
+      // Q in its two e4m3 parts: D/8 lanes read a row, so that a warp reads
+      // whole rows at once
+      constexpr int LPR = D / 8, RPI = 32 / LPR, ITERS = 32 / RPI;
+      const int wr = (warp % 4) * 32, sub = lane / LPR, c8 = lane % LPR;  // the warp's rows in the tile
+      uint4 w[ITERS];
 #pragma unroll
-      for (int c = 0; c < D / 8; ++c) {
-        w[c] = row_valid ? *reinterpret_cast<const uint4*>(src + c * 8) : make_uint4(0, 0, 0, 0);
-        top = max(top, max(bf16x2_top(w[c].x), max(bf16x2_top(w[c].y), max(bf16x2_top(w[c].z), bf16x2_top(w[c].w)))));
+      for (int j = 0; j < ITERS; ++j) {
+        const int gr = base + rt * BM + wr + j * RPI + sub;
+        w[j] = make_uint4(0, 0, 0, 0);
+        if (gr < rows)
+          w[j] = *reinterpret_cast<const uint4*>(p.q.p + b * p.q.sb + (long long)(gr / p.group) * p.q.sn +
+                                                 (long long)(h * p.group + gr % p.group) * p.q.sh + c8 * 8);
       }
-      float mul;
-      q_scale<7>(top, mul, qs);
+#pragma unroll
+      for (int j = 0; j < ITERS; ++j) {
+        uint32_t top = max(max(bf16x2_top(w[j].x), bf16x2_top(w[j].y)), max(bf16x2_top(w[j].z), bf16x2_top(w[j].w)));
+#pragma unroll
+        for (int d = 1; d < LPR; d <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
+        float mul, inv;
+        q_scale<7>(top, mul, inv);
+        mul = copysignf(mul, p.scale_log2);
+        uint32_t hi[2], lo[2];
+        split_e4m3x4(w[j].x, w[j].y, mul, hi[0], lo[0]);
+        split_e4m3x4(w[j].z, w[j].w, mul, hi[1], lo[1]);
+        const int r = wr + j * RPI + sub, at = code_at<D>(r, c8 >> 1) + (c8 & 1) * 8;
+        *reinterpret_cast<uint2*>(own + at) = make_uint2(hi[0], hi[1]);
+        *reinterpret_cast<uint2*>(own + Lay::QB + at) = make_uint2(lo[0], lo[1]);
+        // the lane that owns the row keeps its factor
+        const float got = __shfl_sync(0xffffffffu, inv, (lane % RPI) * LPR);
+        if (lane / RPI == j) qs = got;
+      }
       qs *= fabsf(p.scale_log2);
-      mul = copysignf(mul, p.scale_log2);
-      uint8_t* qh = smem + Lay::OFF_Q + rt * 2 * Lay::QB;
-      const int r = tid & (BM - 1);
-#pragma unroll
-      for (int c = 0; c < D / 16; ++c) {
-        const uint32_t x[8] = {w[2 * c].x, w[2 * c].y, w[2 * c].z, w[2 * c].w,
-                               w[2 * c + 1].x, w[2 * c + 1].y, w[2 * c + 1].z, w[2 * c + 1].w};
-        uint32_t hi[4], lo[4];
-#pragma unroll
-        for (int y = 0; y < 4; ++y) split_e4m3x4(x[2 * y], x[2 * y + 1], mul, hi[y], lo[y]);
-        *reinterpret_cast<uint4*>(qh + code_at<D>(r, c)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-        *reinterpret_cast<uint4*>(qh + Lay::QB + code_at<D>(r, c)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-      }
       fence_proxy_async_smem();
       mbar_arrive(q_full);
     }
@@ -501,32 +512,51 @@ __global__ void __launch_bounds__(THREADS, 1)
     if (mine) {
       const float inv = l == 0.f ? 0.f : 1.0f / l;
       const int qh = h * p.group + row % p.group, i = row / p.group;
-      __nv_bfloat16* dst = p.o + b * p.o_sb + (long long)i * p.o_sn + (long long)qh * p.o_sh;
+      // rows go through the row tile's own shared memory, 2 D bytes of each at
+      // a time, so that a warp writes whole rows: its bf16 row, or half of its
+      // fp32 one
+      constexpr int UNITS = D / 8;  // 16-byte units per row and pass
+      uint8_t* mem = own + (warp % 4) * 32 * 2 * D;
+      auto slot = [&](int r, int u) { return mem + r * 2 * D + ((u ^ (r & (UNITS - 1))) << 4); };
+      const int passes = p.splits > 1 ? 2 : 1;
+      for (int ps = 0; ps < passes; ++ps) {
+        const int cols = D / passes;
+        for (int c = 0; c < cols; c += 32) {
+          uint32_t u[32];
+          if (have) {
+            tmem_ld32(lane_addr + o_col + ps * cols + c, u);
+          } else {
 #pragma unroll
-      for (int c = 0; c < D / 32; ++c) {
-        uint32_t u[32];
-        if (have) {
-          tmem_ld32(lane_addr + o_col + c * 32, u);
-        } else {
+            for (int y = 0; y < 32; ++y) u[y] = 0u;
+          }
+          if (passes == 2) {
 #pragma unroll
-          for (int y = 0; y < 32; ++y) u[y] = 0u;
+            for (int y = 0; y < 8; ++y)
+              *reinterpret_cast<uint4*>(slot(lane, c / 4 + y)) = make_uint4(u[4 * y], u[4 * y + 1], u[4 * y + 2], u[4 * y + 3]);
+          } else {
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+              uint32_t x[4];
+#pragma unroll
+              for (int z = 0; z < 4; ++z)
+                x[z] = pack_bf16x2_rn(l == 0.f ? 0.f : __uint_as_float(u[8 * y + 2 * z]) * inv,
+                                      l == 0.f ? 0.f : __uint_as_float(u[8 * y + 2 * z + 1]) * inv);
+              *reinterpret_cast<uint4*>(slot(lane, c / 8 + y)) = make_uint4(x[0], x[1], x[2], x[3]);
+            }
+          }
         }
-        if (row_valid && p.splits > 1) {
-          float4* d4 = reinterpret_cast<float4*>(p.part_o + prow * D + c * 32);
+        __syncwarp();
 #pragma unroll
-          for (int y = 0; y < 8; ++y)
-            d4[y] = make_float4(__uint_as_float(u[4 * y]), __uint_as_float(u[4 * y + 1]), __uint_as_float(u[4 * y + 2]),
-                                __uint_as_float(u[4 * y + 3]));
-        } else if (row_valid) {
-          uint4* d4 = reinterpret_cast<uint4*>(dst + c * 32);
-#pragma unroll
-          for (int y = 0; y < 4; ++y) {
-            uint32_t x[4];
-#pragma unroll
-            for (int z = 0; z < 4; ++z)
-              x[z] = pack_bf16x2_rn(l == 0.f ? 0.f : __uint_as_float(u[8 * y + 2 * z]) * inv,
-                                    l == 0.f ? 0.f : __uint_as_float(u[8 * y + 2 * z + 1]) * inv);
-            d4[y] = make_uint4(x[0], x[1], x[2], x[3]);
+        for (int j = 0; j < 32; j += 32 / UNITS) {
+          const int r = j + lane / UNITS, u = lane % UNITS, gr = base + (warp / 4) * BM + (warp % 4) * 32 + r;
+          const uint4 v = *reinterpret_cast<const uint4*>(slot(r, u));
+          if (gr >= rows) continue;
+          if (passes == 2) {
+            const long long pr = ((long long)bh * p.splits + sp) * p.rows_pad + gr;
+            *reinterpret_cast<uint4*>(p.part_o + pr * D + ps * (D / 2) + u * 4) = v;
+          } else {
+            *reinterpret_cast<uint4*>(p.o + b * p.o_sb + (long long)(gr / p.group) * p.o_sn +
+                                      (long long)(h * p.group + gr % p.group) * p.o_sh + u * 8) = v;
           }
         }
         __syncwarp();
