@@ -61,7 +61,7 @@ class _Layer(ctypes.Structure):
 class _KvCache(ctypes.Structure):
     _fields_ = ([(n, ctypes.c_int32) for n in ("B", "heads_kv", "d", "tile", "n_slots", "nb_cap")] +
                 [(n, ctypes.c_void_p) for n in ("k8", "v8", "table", "pos", "k_scale", "v_scale", "weight", "len",
-                                                "next_pos", "dev_status")])
+                                                "next_pos", "arrive", "dev_status")])
 
 
 _P = ctypes.c_void_p
@@ -386,9 +386,11 @@ class KVCache:
         self.device = device
         self.n_slots = n_slots
         self.status = torch.zeros(4, dtype=torch.int32, device=device)
+        self._arrive = torch.zeros((B, heads_kv), dtype=torch.int32, device=device)
         self._c = _KvCache(B, heads_kv, d, tile, n_slots, nb_cap,
                            *[getattr(self, n).data_ptr() for n in ("k8", "v8", "table", "pos", "k_scale", "v_scale",
-                                                                   "weight", "len", "next_pos", "status")])
+                                                                   "weight", "len", "next_pos", "_arrive",
+                                                                   "status")])
 
     @property
     def ref(self):

@@ -117,6 +117,7 @@ int build_kv(const veda_kv_cache* C, veda::KvGeom* g, const char* what) {
   VEDA_TRY(check_ptr(C->v_scale, "v_scale"));
   VEDA_TRY(check_ptr(C->len, "len"));
   VEDA_TRY(check_ptr(C->next_pos, "next_pos"));
+  VEDA_TRY(check_ptr(C->arrive, "arrive"));
   if (C->weight) VEDA_TRY(check_ptr(C->weight, "weight"));
   g->B = C->B;
   g->hkv = C->heads_kv;
@@ -133,6 +134,7 @@ int build_kv(const veda_kv_cache* C, veda::KvGeom* g, const char* what) {
   g->weight = C->weight;
   g->len = C->len;
   g->next_pos = C->next_pos;
+  g->arrive = C->arrive;
   g->dev_status = C->dev_status;
   return VEDA_OK;
 }
@@ -721,6 +723,7 @@ int veda_kv_attn(const veda_kv_cache* C, const void* q, const int64_t* q_strides
   p.lse = lse;
   p.weight = weight;
   p.decay = decay;
+  p.arrive = g.arrive;
   return after_launch(veda::launch_kv_attn(g, p, ws, stream), "veda_kv_attn");
 }
 

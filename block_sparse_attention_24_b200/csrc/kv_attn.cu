@@ -1,4 +1,6 @@
-// Attention over the 8-bit K/V tile cache, for few query rows.
+// Attention over the 8-bit K/V tile cache: the plan of a call, the kernel for
+// few query rows per K/V head (single tokens and their groups), and what joins
+// the parts of the other one (kv_tiles.cu).
 //
 // Row r of a K/V head is query token r / group, query head h*group + r % group.
 // With c the codes, s the tile scales and x_ij = scale*log2(e) * (q_i . ck_j)
@@ -7,11 +9,8 @@
 // The V scale is part of the exponent, so P V runs on the bare codes and tiles
 // of any scale add up in one accumulator; dividing P by sv again for the sum is
 // exact for powers of two. M is a reference, not the maximum: it moves only
-// when some x passes it by MARGIN, so that P stays within 2^(MARGIN + OFF) and
-// fp16 (which has 11 bits of significand against bf16's 8, and is what an e4m3
-// pair converts to in one instruction) holds it. OFF keeps what lies 2^-31
-// below the reference out of fp16's zero: even a million such keys add less
-// than a part in a thousand. Sums, references and O are fp32.
+// when some x passes it by a margin, so that P stays within its type (fp16 in
+// the tile kernel, e4m3 parts here). Sums, references and O are fp32.
 #include <cmath>
 
 #include "kv_attn.cuh"
@@ -19,332 +18,450 @@
 namespace veda {
 namespace {
 
-constexpr int ROWS = 16;    // query rows per CTA (the M of one mma)
-constexpr int PIECE = 32;   // keys a warp takes at a time
-constexpr int WARPS = 4;
-constexpr int TILE_KERNEL_ROWS = 32;  // more query rows per K/V head than this: the tile kernel
-constexpr float MARGIN = 8.f;
+// Few rows: HBM is the bound (1 byte per K and V value, each used by up to 16
+// rows), so the codes go from TMA straight into tcgen05 MMAs on e4m3 and no
+// thread touches them; converting them first (mma.sync on fp16) took 840
+// instructions per 32 keys and ran at 4.1 TB/s.
+//   S^T = K Q^T   A = the K tile (128 keys x d), B = Q: each row, times a power
+//                 of two, in four e4m3 parts of which each holds 16 times what
+//                 the one before left, N = 4 RP columns; a row's logit is the
+//                 sum of its four columns with weights 16^-k.
+//   O^T = V^T P   A = the V tile taken along its rows (d x 128 keys; for d = 64
+//                 the upper half of M repeats the lower), B = P^T, in four
+//                 parts too: 16 bits, down to 2^-29 of the row's largest.
+// A thread owns a key (TMEM lane) of S^T and a channel of O^T; the rows are
+// columns, so the work per key goes with the rows there are. A step (128 keys)
+// is S, softmax, P V in turn; about a thousand clocks, which two CTAs per SM
+// hide behind the 2,800 that a step's bytes take for each of them.
+//   warps 0-3  softmax; thread 0 issues the MMAs
+//   warp 4     producer: table, scales, TMA
+// The CTAs that share a head's keys count themselves in `arrive`; the last one
+// joins their parts, and sums the tile weights.
+constexpr int FEW_ROWS = 16;
+constexpr int THREADS = 160;
+constexpr float MARGIN = 1.5f;  // P <= 2^(OFF + MARGIN) = 362 < 448
 
-__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
-}
-__device__ __forceinline__ void ldsm4_t(uint32_t (&r)[4], uint32_t addr) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
-}
-__device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-               : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-               : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-// A CTA has 16 query rows of one K/V head and a range of its tiles, in pieces
-// of 32 keys; warp w takes every fourth piece and keeps its own reference, sum
-// and O, so that no warp waits for another before the end. Pieces reach the
-// warp through its own ring of STAGES TMA copies on mbarriers: the bound is HBM
-// (1 byte per K and V value, each used by up to 16 rows), so what matters is
-// that enough copies are in flight, not which warp asks for them. Table
-// entries, positions and scales of the warp's next 32 pieces sit in its lanes.
-template <int D>
+template <int D, int RP>
 struct RowsCfg {
-  static constexpr int STAGES = D == 128 ? 2 : 3;
-  static constexpr int PB = PIECE * D;                                   // bytes of a piece of K or V
-  static constexpr int SMEM = WARPS * STAGES * 2 * PB + 1024;            // and alignment
-  static constexpr int CTAS = D == 128 ? 3 : 4;                          // per SM, by registers
+  static constexpr int N = 4 * RP;
+  static constexpr int CB = STEP * D;                           // bytes of a step's K or V codes
+  static constexpr int ST = D == 64 ? 6 : (RP == 16 ? 2 : 3);   // ring stages: two CTAs per SM
+  static constexpr int OFF_Q = ST * 2 * CB;
+  static constexpr int OFF_P = OFF_Q + N * D;
+  static constexpr int OFF_META = OFF_P + N * STEP;
+  static constexpr int OFF_BAR = OFF_META + ST * (int)sizeof(StepMeta);
+  static constexpr int NUM_BARS = 3 * ST + 1;                   // K, V, free per stage; S
+  static constexpr int OFF_RED = OFF_BAR + NUM_BARS * 8;        // float [4][RP], then [RP] factors, int [RP] positions
+  static constexpr int OFF_MISC = OFF_RED + 6 * RP * 4;
+  static constexpr int ALLOC = OFF_MISC + 32 + 1024;
+  static constexpr int TMEM = 2 * N < 32 ? 32 : 2 * N;          // S^T, O^T
 };
 
-template <int D>
-__global__ void __launch_bounds__(WARPS * 32, RowsCfg<D>::CTAS)
+__device__ __forceinline__ void softmax_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+__device__ __forceinline__ bool softmax_any(bool x) {
+  int r;
+  asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %1, 0;\n\tbar.red.or.pred q, 1, 128, p;\n\tselp.b32 %0, 1, 0, q;\n\t}"
+               : "=r"(r) : "r"((int)x) : "memory");
+  return r != 0;
+}
+
+template <int N>
+__device__ __forceinline__ void tmem_load(uint32_t addr, uint32_t (&u)[N]) {
+  if constexpr (N == 16) tmem_ld16(addr, u);
+  else if constexpr (N == 32) tmem_ld32(addr, u);
+  else tmem_ld64(addr, u);
+}
+template <int N>
+__device__ __forceinline__ void tmem_store(uint32_t addr, const uint32_t (&u)[N]) {
+  if constexpr (N == 16) tmem_st16(addr, u);
+  else if constexpr (N == 32) tmem_st32(addr, u);
+  else tmem_st64(addr, u);
+}
+
+// Two values as four e4m3 parts each: part k is the code nearest to 16 times
+// what part k-1 left. The codes of x are in the low bytes, those of y above.
+__device__ __forceinline__ void four_parts(float x, float y, uint16_t (&c)[4]) {
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(c[k]) : "f"(y), "f"(x));
+    if (k < 3) {
+      uint32_t h;
+      asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(c[k]));
+      const float2 f = __half22float2(*reinterpret_cast<__half2*>(&h));
+      x = (x - f.x) * 16.f;
+      y = (y - f.y) * 16.f;
+    }
+  }
+}
+
+template <int D, int RP>
+__global__ void __launch_bounds__(THREADS, 2)
     kv_attn_rows_kernel(const KvGeom g, const KvAttnParams p, const __grid_constant__ KvMaps maps) {
-  using Cfg = RowsCfg<D>;
-  constexpr int KS = D / 16;  // 16-wide steps over the head dimension
-  constexpr int ST = Cfg::STAGES;
+  using Cfg = RowsCfg<D, RP>;
+  constexpr int N = Cfg::N, ST = Cfg::ST;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ float sm_m[WARPS][ROWS], sm_l[WARPS][ROWS];
-  __shared__ int sm_cnt[3];
-  __shared__ int sm_abort;
-  __shared__ __align__(8) uint64_t bars[WARPS][ST];
   uint8_t* smem = smem_raw + (((smem_u32(smem_raw) + 1023u) & ~1023u) - smem_u32(smem_raw));
-  const int mt = blockIdx.x % p.row_tiles, sp = blockIdx.x / p.row_tiles, h = blockIdx.y, b = blockIdx.z;
-  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, gr = lane >> 2, c4 = lane & 3;
+  const int sp = blockIdx.x, h = blockIdx.y, b = blockIdx.z;
+  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
   int n_b, held, total;
   if (!kv_counts(g, b, h, p.n_q, p.n_new, p.pending, n_b, held, total)) return;
   const int rows = n_b * p.group;
-  if (mt * ROWS >= rows) return;
+  if (rows == 0) return;
   const int bh = b * g.hkv + h;
   const long long trow = (long long)bh * g.nb_cap;
-  const int t0 = g.next_pos[b];
-  const int t_lo = t0 + mt * ROWS / p.group, t_hi = t0 + (min(rows, mt * ROWS + ROWS) - 1) / p.group;
-  if (tid < WARPS * ST) mbar_init(&bars[tid / ST][tid % ST], 1);
-  if (tid < 3) sm_cnt[tid] = 0;
-  if (tid == 0) sm_abort = 0;
+  const int t_lo = g.next_pos[b], t_hi = t_lo + n_b - 1;
+
+  uint64_t* k_full = reinterpret_cast<uint64_t*>(smem + Cfg::OFF_BAR);
+  uint64_t* v_full = k_full + ST;
+  uint64_t* free_ = v_full + ST;  // P V of the stage's step has completed
+  uint64_t* s_full = free_ + ST;
+  StepMeta* meta = reinterpret_cast<StepMeta*>(smem + Cfg::OFF_META);
+  float* red = reinterpret_cast<float*>(smem + Cfg::OFF_RED);
+  float* qs = red + 4 * RP;
+  int* t_of = reinterpret_cast<int*>(qs + RP);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Cfg::OFF_MISC);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Cfg::OFF_MISC + 4);
+  int* cnt = reinterpret_cast<int*>(smem + Cfg::OFF_MISC + 8);  // [3], then a flag
+  if (tid < Cfg::NUM_BARS) mbar_init(k_full + tid, 1);
+  if (tid < 4) cnt[tid] = 0;
+  if (tid == 0) *abort_flag = 0;
   fence_mbar_init();
+  if (warp == 4) {
+    if (lane == 0) {
+      tma_prefetch_desc(&maps.k);
+      tma_prefetch_desc(&maps.v);
+    }
+    __syncwarp();
+    tmem_alloc(tmem_slot, Cfg::TMEM);
+    tmem_relinquish();
+  }
+  tc_fence_before();
   __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
 
   const int nb = (total + g.tile - 1) / g.tile;
-  const KvRange rg = kv_range(g, p, trow, nb, t_lo, t_hi, t0 + n_b - 1, sm_cnt, tid, WARPS * 32);
-  const int ppt = g.tile / PIECE;
-  // pieces behind the last token, where its tile is among them
-  const int tail = rg.upto == nb && (rg.from < nb || rg.n_first == nb) ? (nb * g.tile - total) / PIECE : 0;
-  const int pieces = max(0, rg.count() * ppt - tail);
-  const int per = (pieces + p.splits - 1) / p.splits;
-  const int p_lo = sp * per, p_hi = min(pieces, p_lo + per);
-  const int mine = p_hi - p_lo > warp ? (p_hi - p_lo - warp + WARPS - 1) / WARPS : 0;  // this warp's pieces
-  // place of the warp's k-th piece: its tile's entry, and which part of the tile
-  auto place = [&](int k, int& sub) {
-    const int pc = p_lo + warp + k * WARPS, vt = pc / ppt;
-    sub = pc - vt * ppt;
-    return rg.tile(vt);
-  };
-  uint8_t* ring = smem + warp * ST * 2 * Cfg::PB;
-  int row_of = 0;  // lane j: pool row of the piece issued (32-blockwise) j-th, -1 for none
-  auto issue = [&](int k) {
-    if ((k & 31) == 0) {
-      row_of = -1;
-      if (k + lane < mine) {
-        int sub;
-        const int i = place(k + lane, sub);
-        const int slot = g.table[trow + i];
-        if (slot >= 0 && slot < g.n_slots) row_of = slot * g.tile + sub * PIECE;
-        else report(g.dev_status, VEDA_ERR_BAD_INDEX);
+  const KvRange rg = kv_range(g, p, trow, nb, t_lo, t_hi, t_hi, cnt, tid, THREADS);
+  const int per_step = STEP / g.tile;
+  const int steps_all = (rg.count() + per_step - 1) / per_step;
+  const int per = max(1, (steps_all + p.splits - 1) / p.splits);
+  const int parts = max(1, (steps_all + per - 1) / per);  // CTAs that have steps (one, if there are none)
+  const int s_lo = sp * per, n_steps = max(0, min(per, steps_all - s_lo));
+
+  if (sp < parts) {
+  if (warp == 4) {
+    // ------------------------------------------------------------- producer
+    StepFeed feed;
+    int e = 0;
+    for (; e < n_steps; ++e) {
+      if ((e & 15) == 0) feed.load(g, trow, rg, total, s_lo, e, n_steps, lane);
+      const int st = e % ST;
+      if (!__all_sync(0xffffffffu, e < ST || mbar_wait(free_ + st, (e / ST - 1) & 1, abort_flag, g.dev_status))) break;
+      int row0, row1;
+      feed.put(meta[st], g, p, e, t_lo, t_hi, lane, row0, row1);
+      __syncwarp();
+      if (lane == 0) {
+        const uint32_t bytes = (row0 >= 0 ? Cfg::CB / 2 : 0) + (row1 >= 0 ? Cfg::CB / 2 : 0);
+        uint8_t* kd = smem + st * 2 * Cfg::CB;
+        uint8_t* vd = kd + Cfg::CB;
+        mbar_expect_tx(k_full + st, bytes);
+        if (row0 >= 0) tma_load_2d(kd, &maps.k, k_full + st, 0, row0);
+        if (row1 >= 0) tma_load_2d(kd + Cfg::CB / 2, &maps.k, k_full + st, 0, row1);
+        mbar_expect_tx(v_full + st, bytes);
+        if (row0 >= 0) tma_load_2d(vd, &maps.v, v_full + st, 0, row0);
+        if (row1 >= 0) tma_load_2d(vd + Cfg::CB / 2, &maps.v, v_full + st, 0, row1);
       }
-    }
-    const int row = __shfl_sync(0xffffffffu, row_of, k & 31);
-    if (lane == 0 && row >= 0) {
-      uint64_t* bar = &bars[warp][k % ST];
-      uint8_t* dst = ring + (k % ST) * 2 * Cfg::PB;
-      mbar_expect_tx(bar, 2 * Cfg::PB);
-      tma_load_2d(dst, &maps.k, bar, 0, row);
-      tma_load_2d(dst + Cfg::PB, &maps.v, bar, 0, row);
-    }
-    return row >= 0;
-  };
-  uint32_t there = 0;  // bit s: stage s holds a piece (not an absent tile)
-  int issued = 0;
-  for (; issued < ST && issued < mine; ++issued)
-    if (issue(issued)) there |= 1u << issued;
-
-  // Q as fp16 fragments, each row times a power of two that puts its largest
-  // value into [2^13, 2^14): bf16's range fits, and its 8 bits are kept down
-  // to 2^-37 of the row's largest
-  const int r0 = mt * ROWS + gr, r1 = r0 + 8;
-  uint32_t qa[KS][4];
-  float qs[2];
-  int tq[2];
-#pragma unroll
-  for (int e = 0; e < 2; ++e) {
-    const int r = e ? r1 : r0;
-    tq[e] = t0 + r / p.group;
-    uint2 w[KS];
-    uint32_t top = 0;
-#pragma unroll
-    for (int ks = 0; ks < KS; ++ks) {
-      w[ks] = make_uint2(0, 0);
-      if (r < rows)
-        w[ks] = *reinterpret_cast<const uint2*>(p.q.p + b * p.q.sb + (long long)(r / p.group) * p.q.sn +
-                                                (long long)(h * p.group + r % p.group) * p.q.sh + ks * 16 + c4 * 4);
-      top = max(top, max(bf16x2_top(w[ks].x), bf16x2_top(w[ks].y)));
-    }
-    top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-    top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-    float mul;
-    q_scale<13>(top, mul, qs[e]);
-    qs[e] *= p.scale_log2;
-#pragma unroll
-    for (int ks = 0; ks < KS; ++ks) {
-      qa[ks][e] = pack_f16x2(__uint_as_float(w[ks].x << 16) * mul, __uint_as_float(w[ks].x & 0xffff0000u) * mul);
-      qa[ks][2 + e] = pack_f16x2(__uint_as_float(w[ks].y << 16) * mul, __uint_as_float(w[ks].y & 0xffff0000u) * mul);
-    }
-  }
-
-  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-  float o[KS][2][4];
-#pragma unroll
-  for (int c = 0; c < KS; ++c)
-#pragma unroll
-    for (int e = 0; e < 2; ++e)
-#pragma unroll
-      for (int x = 0; x < 4; ++x) o[c][e][x] = 0.f;
-
-  int pos_of = 0;  // lane j: as row_of, for the piece computed j-th
-  float sk_of = 0.f, sv_of = 0.f;
-  bool ok = true;
-  uint32_t phase = 0;  // bit s: parity of stage s
-  for (int k = 0; k < mine; ++k) {
-    const int st = k % ST;
-    int sub;
-    const int i = place(k, sub);
-    if ((k & 31) == 0 && k + lane < mine) {
-      int sb;
-      const long long e = trow + place(k + lane, sb);
-      pos_of = g.pos[e] + sb * PIECE;
-      sk_of = g.k_scale[e];
-      sv_of = g.v_scale[e];
-    }
-    const int pos0 = __shfl_sync(0xffffffffu, pos_of, k & 31);
-    const float sk = __shfl_sync(0xffffffffu, sk_of, k & 31), sv = __shfl_sync(0xffffffffu, sv_of, k & 31);
-    if (!(there >> st & 1u)) {
-      if (p.lw && lane < ROWS && mt * ROWS + lane < rows)
-        p.lw[((long long)bh * p.pieces_cap + i * ppt + sub) * p.rows_cap + mt * ROWS + lane] = -INFINITY;
-    } else {
-    if (!__all_sync(0xffffffffu, mbar_wait(&bars[warp][st], phase >> st & 1u, &sm_abort, g.dev_status))) {
-      ok = false;
-      break;
-    }
-    phase ^= 1u << st;
-    const uint32_t ka = smem_u32(ring + st * 2 * Cfg::PB), va = ka + Cfg::PB;
-    const int left = total - (i * g.tile + sub * PIECE);  // keys of the piece that exist
-    if (left < PIECE) {
-      // V rows behind the last token become zeroes: their codes may be anything
-      for (int x = left * D / 16 + lane; x < Cfg::PB / 16; x += 32)
-        *reinterpret_cast<uint4*>(ring + st * 2 * Cfg::PB + Cfg::PB + code_at<D>(x / (D / 16), x % (D / 16))) =
-            make_uint4(0, 0, 0, 0);
-      fence_proxy_async_smem();
       __syncwarp();
     }
-    float s[4][4];
+    if (*abort_flag && lane == 0)  // let every copy that was started land
+      for (int x = max(0, e - ST); x < e; ++x) {
+        mbar_wait_drain(k_full + x % ST, (x / ST) & 1, VEDA_WAIT_LIMIT_NS);
+        mbar_wait_drain(v_full + x % ST, (x / ST) & 1, VEDA_WAIT_LIMIT_NS);
+      }
+  } else {
+    // ----------------------------------------------------- Q in its parts
+    {
+      constexpr int TPR = 128 / RP, EL = D / TPR;  // threads per row, their values
+      const int r = tid / TPR, d0 = tid % TPR * EL;
+      uint32_t w[EL / 2], top = 0;
+      if (r < rows) {
+        const uint32_t* src = reinterpret_cast<const uint32_t*>(p.q.p + b * p.q.sb + (long long)(r / p.group) * p.q.sn +
+                                                                (long long)(h * p.group + r % p.group) * p.q.sh + d0);
 #pragma unroll
-    for (int nt = 0; nt < 4; ++nt) {
+        for (int x = 0; x < EL / 2; ++x) w[x] = src[x];
+      } else {
 #pragma unroll
-      for (int x = 0; x < 4; ++x) s[nt][x] = 0.f;
+        for (int x = 0; x < EL / 2; ++x) w[x] = 0;
+      }
 #pragma unroll
-      for (int q4 = 0; q4 < KS / 4; ++q4) {
-        uint32_t f[4];
-        ldsm4(f, ka + code_at<D>(nt * 8 + (lane & 7), q4 * 4 + (lane >> 3)));
+      for (int x = 0; x < EL / 2; ++x) top = max(top, bf16x2_top(w[x]));
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          uint32_t b0, b1;
-          codes_f16(f[x], b0, b1);
-          mma(s[nt], qa[q4 * 4 + x], b0, b1);
+      for (int d = 1; d < TPR; d <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
+      float mul, inv;
+      q_scale<7>(top, mul, inv);
+      if (tid % TPR == 0) {
+        qs[r] = inv * p.scale_log2;
+        t_of[r] = t_lo + min(r, rows - 1) / p.group;
+      }
+#pragma unroll
+      for (int x = 0; x < EL / 2; ++x) {
+        uint16_t c[4];
+        four_parts(__uint_as_float(w[x] << 16) * mul, __uint_as_float(w[x] & 0xffff0000u) * mul, c);
+        const int d = d0 + 2 * x;
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          *reinterpret_cast<uint16_t*>(smem + Cfg::OFF_Q + code_at<D>(k * RP + r, d >> 4) + (d & 15)) = c[k];
+      }
+      fence_proxy_async_smem();
+      softmax_sync();
+    }
+    constexpr uint32_t idesc_s = idesc_fmt0(128, N, false, false), idesc_o = idesc_fmt0(128, N, true, false);
+    const uint64_t dK = sdesc_codes<D>(smem_u32(smem)), dV = sdesc_codes<D>(smem_u32(smem + Cfg::CB), 0);
+    const uint64_t dQ = sdesc_codes<D>(smem_u32(smem + Cfg::OFF_Q)), dP = sdesc_codes<128>(smem_u32(smem + Cfg::OFF_P));
+    auto issue_s = [&](int e) {  // one thread
+      const int st = e % ST;
+      if (!mbar_wait(k_full + st, (e / ST) & 1, abort_flag, g.dev_status)) return;
+      tc_fence_after();
+#pragma unroll
+      for (int kk = 0; kk < D / 32; ++kk)
+        umma_f8_ss(tmem, dK + (uint64_t)((st * 2 * Cfg::CB + kk * 32) >> 4), dQ + (uint64_t)(kk * 32 >> 4), idesc_s,
+                   kk > 0);
+      umma_commit(s_full);
+    };
+    if (tid == 0 && n_steps > 0) issue_s(0);
+
+    const uint32_t lane_addr = tmem + ((uint32_t)(warp * 32) << 16);
+    const int half = tid >> 6, kk = tid & 63;  // this thread's key
+    float m[RP], l[RP];
+#pragma unroll
+    for (int r = 0; r < RP; ++r) {
+      m[r] = -INFINITY;
+      l[r] = 0.f;
+    }
+    bool ok = true;
+    for (int e = 0; e < n_steps; ++e) {
+      const int st = e % ST;
+      ok = mbar_wait(s_full, e & 1, abort_flag, g.dev_status);
+      if (softmax_any(!ok)) break;
+      tc_fence_after();
+      const StepMeta& sm = meta[st];
+      uint32_t u[N];
+      tmem_load(lane_addr, u);
+      const float sk = sm.ks[half], ev = sm.ev[half];
+      const int left = sm.left[half], pos = sm.pos[half] + kk;
+      const bool full = sm.full;
+      float x[RP];
+      bool over = false;
+#pragma unroll
+      for (int r = 0; r < RP; ++r) {
+        const float s = fmaf(fmaf(fmaf(__uint_as_float(u[3 * RP + r]), 0.0625f, __uint_as_float(u[2 * RP + r])), 0.0625f,
+                                  __uint_as_float(u[RP + r])), 0.0625f, __uint_as_float(u[r]));
+        x[r] = fmaf(s, qs[r] * sk, ev);
+        if (!full && !(kk < left && kv_seen(pos, t_of[r], p.causal, p.window, p.sinks))) x[r] = -INFINITY;
+        over |= x[r] > m[r] + MARGIN;
+      }
+      if (softmax_any(over)) {
+        // new references: the largest x so far
+#pragma unroll
+        for (int r = 0; r < RP; ++r) {
+          float v = x[r];
+#pragma unroll
+          for (int d = 16; d; d >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, d));
+          if (lane == r) red[warp * RP + r] = v;
+        }
+        softmax_sync();
+        float al[RP];
+#pragma unroll
+        for (int r = 0; r < RP; ++r) {
+          const float mx = fmaxf(fmaxf(red[r], red[RP + r]), fmaxf(red[2 * RP + r], red[3 * RP + r]));
+          const float mn = fmaxf(m[r], mx);
+          al[r] = mn == m[r] ? 1.f : fast_exp2(m[r] - mn);
+          m[r] = mn;
+          l[r] *= al[r];
+        }
+        if (e > 0) {  // O holds P V of all earlier steps: S of this one was issued behind them
+          uint32_t o[N];
+          tmem_load(lane_addr + N, o);
+#pragma unroll
+          for (int k = 0; k < N; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * al[k % RP]);
+          tmem_store(lane_addr + N, o);
+        }
+      }
+      const float rv = sm.rv[half];
+#pragma unroll
+      for (int r = 0; r < RP; r += 2) {
+        const float p0 = fast_exp2(x[r] + (OFF - (m[r] == -INFINITY ? 0.f : m[r])));
+        const float p1 = fast_exp2(x[r + 1] + (OFF - (m[r + 1] == -INFINITY ? 0.f : m[r + 1])));
+        x[r] = p0;
+        x[r + 1] = p1;
+        // NaN scales reach the rows that see the tile through P, and no other
+        l[r] += p0 == 0.f ? 0.f : p0 * rv;
+        l[r + 1] += p1 == 0.f ? 0.f : p1 * rv;
+        uint16_t c[4];
+        four_parts(p0, p1, c);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int n = k * RP + r;
+          uint8_t* dst = smem + Cfg::OFF_P + (tid & 15);
+          dst[n * 128 + (((tid >> 4) ^ (n & 7)) << 4)] = (uint8_t)c[k];
+          dst[(n + 1) * 128 + (((tid >> 4) ^ ((n + 1) & 7)) << 4)] = (uint8_t)(c[k] >> 8);
+        }
+      }
+      if (p.lw && sm.entry[half] >= 0) {
+        const int ppt = g.tile / 32;
+        const long long piece = (long long)bh * p.pieces_cap + sm.entry[half] * ppt + (warp & (ppt - 1));
+        float mine = 0.f, ref = 0.f;
+#pragma unroll
+        for (int r = 0; r < RP; ++r) {
+          float v = x[r];
+#pragma unroll
+          for (int d = 16; d; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+          if (lane == r) {
+            mine = v;
+            ref = m[r];
+          }
+        }
+        if (lane < rows && lane < RP) p.lw[piece * p.rows_cap + lane] = mine == 0.f ? -INFINITY : log2f(mine) + (ref - OFF - ev);
+      }
+      if (!full) {
+        // V rows behind the last token become zeroes: their codes may be anything
+        if (sm.left[0] + sm.left[1] < STEP) {
+          mbar_wait(v_full + st, (e / ST) & 1, abort_flag, g.dev_status);
+          if (kk >= left) {
+            uint4* v = reinterpret_cast<uint4*>(smem + (st * 2 + 1) * Cfg::CB + tid * D);
+#pragma unroll
+            for (int c = 0; c < D / 16; ++c) v[c] = make_uint4(0, 0, 0, 0);
+          }
+        }
+      }
+      fence_proxy_async_smem();
+      tc_fence_before();
+      softmax_sync();
+      if (tid == 0) {
+        tc_fence_after();
+        if (mbar_wait(v_full + st, (e / ST) & 1, abort_flag, g.dev_status)) {
+          tc_fence_after();
+#pragma unroll
+          for (int q = 0; q < STEP / 32; ++q)
+            umma_f8_ss(tmem + N, dV + (uint64_t)((st * 2 * Cfg::CB + q * 32 * D) >> 4), dP + (uint64_t)(q * 32 >> 4),
+                       idesc_o, (e > 0 || q > 0) ? 1u : 0u);
+        }
+        umma_commit(free_ + st);
+        if (e + 1 < n_steps) issue_s(e + 1);
+      }
+    }
+    if (n_steps > 0)  // the last P V (and with it all before), or after an abort whatever was issued
+      ok = mbar_wait(free_ + (n_steps - 1) % ST, ((n_steps - 1) / ST) & 1, abort_flag, g.dev_status) && ok;
+    if (tid == 0 && *abort_flag) {
+      umma_commit(s_full);
+      mbar_wait_drain(s_full, 0, 1000000);
+    }
+    tc_fence_after();
+    // row sums over the keys
+#pragma unroll
+    for (int r = 0; r < RP; ++r) {
+      float v = l[r];
+#pragma unroll
+      for (int d = 16; d; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+      if (lane == r) red[warp * RP + r] = v;
+    }
+    softmax_sync();
+    uint32_t u[N];
+    if (n_steps > 0 && ok) {
+      tmem_load(lane_addr + N, u);
+    } else {
+#pragma unroll
+      for (int k = 0; k < N; ++k) u[k] = 0;
+    }
+    float o[RP];  // this thread's channel of every row
+#pragma unroll
+    for (int r = 0; r < RP; ++r) {
+      l[r] = red[r] + red[RP + r] + red[2 * RP + r] + red[3 * RP + r];
+      o[r] = fmaf(fmaf(fmaf(__uint_as_float(u[3 * RP + r]), 0.0625f, __uint_as_float(u[2 * RP + r])), 0.0625f,
+                       __uint_as_float(u[RP + r])), 0.0625f, __uint_as_float(u[r]));
+    }
+    bool last = true;
+    if (parts > 1) {
+      const long long row0 = ((long long)bh * p.splits + sp) * p.rows_pad;
+#pragma unroll
+      for (int r = 0; r < RP; ++r) {
+        if (r < rows && tid < D) p.part_o[(row0 + r) * D + tid] = o[r];
+        if (r < rows && tid == r) p.part_ml[row0 + r] = make_float2(m[r], l[r]);
+      }
+      __threadfence();
+      softmax_sync();
+      if (tid == 0) {
+        const int before = atomicAdd(p.arrive + bh, 1);
+        cnt[3] = before == parts - 1;
+        if (before == parts - 1) p.arrive[bh] = 0;
+      }
+      softmax_sync();
+      last = cnt[3] != 0;
+      if (last) {
+        __threadfence();
+        const float2* ml = p.part_ml + (long long)bh * p.splits * p.rows_pad;
+        const float* po = p.part_o + (long long)bh * p.splits * p.rows_pad * D;
+#pragma unroll
+        for (int r = 0; r < RP; ++r) {
+          if (r >= rows) break;
+          float mx = -INFINITY, ls = 0.f, os = 0.f;
+#pragma unroll 4
+          for (int s = 0; s < parts; ++s) mx = fmaxf(mx, __ldcg(&ml[(long long)s * p.rows_pad + r].x));
+#pragma unroll 4
+          for (int s = 0; s < parts; ++s) {
+            const float2 v = __ldcg(&ml[(long long)s * p.rows_pad + r]);
+            const float f = v.x == -INFINITY ? (v.y == v.y ? 0.f : 1.f) : fast_exp2(v.x - mx);
+            ls += v.y * f;
+            if (tid < D) os += __ldcg(&po[((long long)s * p.rows_pad + r) * D + tid]) * f;
+          }
+          m[r] = mx;
+          l[r] = ls;
+          o[r] = os;
         }
       }
     }
-    const float ev = log2f(sv), rv = 1.0f / sv;
-    const float co[2] = {qs[0] * sk, qs[1] * sk};
-    const bool whole = left >= PIECE && kv_seen(pos0 + PIECE - 1, t_lo, p.causal, 0, 0) &&
-                       (p.window <= 0 || pos0 + PIECE <= p.sinks || (long long)pos0 > (long long)t_hi - p.window);
-    bool over = false;
+    if (last) {
 #pragma unroll
-    for (int nt = 0; nt < 4; ++nt)
-#pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        const int e = x >> 1, kk = nt * 8 + c4 * 2 + (x & 1);
-        float v = s[nt][x] * co[e] + ev;
-        if (!whole && !(kk < left && kv_seen(pos0 + kk, tq[e], p.causal, p.window, p.sinks))) v = -INFINITY;
-        s[nt][x] = v;
-        over |= v > m[e] + MARGIN;
+      for (int r = 0; r < RP; ++r) {
+        if (r >= rows) break;
+        const bool none = l[r] == 0.f;
+        const int i = r / p.group, qh = h * p.group + r % p.group;
+        if (tid < D)
+          p.o[b * p.o_sb + (long long)i * p.o_sn + (long long)qh * p.o_sh + tid] =
+              __float2bfloat16(none ? 0.f : o[r] / l[r]);
+        if (tid == r) {
+          const float l2 = none ? -INFINITY : log2f(l[r]) + (m[r] == -INFINITY ? 0.f : m[r]) - OFF;
+          if (p.lse) p.lse[((long long)b * p.heads + qh) * p.n_q + i] = l2 * LN2;
+          qs[r] = l2;
+        }
       }
-    if (__any_sync(0xffffffffu, over)) {
+      if (p.weight) {
+        softmax_sync();
+        const int ppt = g.tile / 32;
+        for (int i = tid; i < nb; i += 128) {
+          float w = 0.f;
+          if (kv_tile_seen(g.pos[trow + i], g.tile, t_lo, t_hi, p.causal, p.window, p.sinks)) {
+            const float* lw = p.lw + ((long long)bh * p.pieces_cap + (long long)i * ppt) * p.rows_cap;
+            for (int k = 0; k < ppt && i * g.tile + k * 32 < total; ++k)
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        float mx = m[e];
-#pragma unroll
-        for (int nt = 0; nt < 4; ++nt) mx = fmaxf(mx, fmaxf(s[nt][2 * e], s[nt][2 * e + 1]));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-        const float al = mx == m[e] ? 1.f : fast_exp2(m[e] - mx);
-        m[e] = mx;
-        l[e] *= al;
-#pragma unroll
-        for (int c = 0; c < KS; ++c)
-#pragma unroll
-          for (int y = 0; y < 2; ++y) {
-            o[c][y][2 * e] *= al;
-            o[c][y][2 * e + 1] *= al;
+              for (int r = 0; r < RP; ++r) {
+                if (r >= rows) break;
+                const float v = __ldcg(&lw[(long long)k * p.rows_cap + r]), z = qs[r];
+                // none of it seen: nothing, even of a row that is NaN
+                if (v != -INFINITY && z != -INFINITY) w += fast_exp2(v - z);
+              }
           }
+          p.weight[trow + i] = p.decay == 0.f ? w : p.decay * p.weight[trow + i] + w;
+        }
       }
     }
-    float ls[2] = {0.f, 0.f};
-    uint32_t pa[2][4];
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const float base = OFF - (m[e] == -INFINITY ? 0.f : m[e]);
-#pragma unroll
-      for (int nt = 0; nt < 4; ++nt) {
-        const float x0 = fast_exp2(s[nt][2 * e] + base), x1 = fast_exp2(s[nt][2 * e + 1] + base);
-        ls[e] += x0 + x1;
-        pa[nt >> 1][(nt & 1) * 2 + e] = pack_f16x2(x0, x1);
-      }
-      // the sum without sv; NaN scales reach the rows that see the tile through P, and no other
-      l[e] += ls[e] == 0.f ? 0.f : ls[e] * rv;
-    }
-    if (p.lw) {
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        float t = ls[e] + __shfl_xor_sync(0xffffffffu, ls[e], 1);
-        t += __shfl_xor_sync(0xffffffffu, t, 2);
-        const int r = e ? r1 : r0;
-        if (c4 == 0 && r < rows)
-          p.lw[((long long)bh * p.pieces_cap + i * ppt + sub) * p.rows_cap + r] =
-              t == 0.f ? -INFINITY : log2f(t) + (m[e] - OFF - ev);
-      }
-    }
-#pragma unroll
-    for (int ch = 0; ch < KS; ++ch) {
-      uint32_t f[4], ev_f[4], od_f[4];
-      ldsm4_t(f, va + code_at<D>(lane, ch));
-#pragma unroll
-      for (int x = 0; x < 4; ++x) codes_f16(__byte_perm(f[x], 0, 0x3120), ev_f[x], od_f[x]);
-      mma(o[ch][0], pa[0], ev_f[0], ev_f[1]);
-      mma(o[ch][1], pa[0], od_f[0], od_f[1]);
-      mma(o[ch][0], pa[1], ev_f[2], ev_f[3]);
-      mma(o[ch][1], pa[1], od_f[2], od_f[3]);
-    }
-    }
-    if (issued < mine) {
-      __syncwarp();  // every lane has read the stage
-      there = issue(issued) ? there | 1u << st : there & ~(1u << st);
-      ++issued;
-    }
+    tc_fence_before();
   }
-  if (!ok)  // let every copy that was started land
-    for (int s = 0; s < ST; ++s)
-      if (there >> s & 1u) mbar_wait_drain(&bars[warp][s], phase >> s & 1u, VEDA_WAIT_LIMIT_NS);
-
-  // join the warps: references, then sums and O in warp order
-#pragma unroll
-  for (int e = 0; e < 2; ++e) {
-    l[e] += __shfl_xor_sync(0xffffffffu, l[e], 1);
-    l[e] += __shfl_xor_sync(0xffffffffu, l[e], 2);
-    if (c4 == 0) sm_m[warp][gr + 8 * e] = m[e];
   }
   __syncthreads();
-  float* acc = reinterpret_cast<float*>(smem);  // [WARPS][ROWS][D], in the ring
-#pragma unroll
-  for (int e = 0; e < 2; ++e) {
-    float mx = sm_m[0][gr + 8 * e];
-#pragma unroll
-    for (int w = 1; w < WARPS; ++w) mx = fmaxf(mx, sm_m[w][gr + 8 * e]);
-    const float f = m[e] == -INFINITY ? (l[e] == l[e] ? 0.f : 1.f) : fast_exp2(m[e] - mx);
-    if (c4 == 0) sm_l[warp][gr + 8 * e] = l[e] * f;
-#pragma unroll
-    for (int ch = 0; ch < KS; ++ch)
-      *reinterpret_cast<float4*>(acc + (warp * ROWS + gr + 8 * e) * D + ch * 16 + c4 * 4) = make_float4(
-          o[ch][0][2 * e] * f, o[ch][1][2 * e] * f, o[ch][0][2 * e + 1] * f, o[ch][1][2 * e + 1] * f);
-  }
-  __syncthreads();
-  const long long prow = ((long long)bh * p.splits + sp) * p.rows_pad + mt * ROWS;
-  for (int x = tid; x < ROWS * D / 4; x += WARPS * 32) {
-    const int r = x / (D / 4), c = x % (D / 4) * 4;
-    if (mt * ROWS + r >= rows) break;
-    float4 v = *reinterpret_cast<float4*>(acc + r * D + c);
-#pragma unroll
-    for (int w = 1; w < WARPS; ++w) {
-      const float4 u = *reinterpret_cast<float4*>(acc + (w * ROWS + r) * D + c);
-      v.x += u.x;
-      v.y += u.y;
-      v.z += u.z;
-      v.w += u.w;
-    }
-    *reinterpret_cast<float4*>(p.part_o + (prow + r) * D + c) = v;
-  }
-  if (tid < ROWS) {
-    float lsum = 0.f, mm = sm_m[0][tid];
-    for (int w = 0; w < WARPS; ++w) {
-      lsum += sm_l[w][tid];
-      mm = fmaxf(mm, sm_m[w][tid]);
-    }
-    p.part_ml[prow + tid] = make_float2(mm, lsum);
+  if (warp == 4) {
+    tc_fence_after();
+    tmem_dealloc(tmem, Cfg::TMEM);
   }
 }
 
@@ -435,18 +552,25 @@ __global__ void __launch_bounds__(WEIGHT_THREADS) kv_weight_kernel(const KvGeom 
   }
 }
 
-template <int D>
-cudaError_t launch_rows(const KvGeom& g, const KvAttnParams& p, cudaStream_t s) {
+template <int D, int RP>
+cudaError_t launch_rows_t(const KvGeom& g, const KvAttnParams& p, cudaStream_t s) {
+  using Cfg = RowsCfg<D, RP>;
   KvMaps maps;
   const uint64_t rows = (uint64_t)g.n_slots * g.tile;
-  if (encode_tensor_map_2d_u8(&maps.k, g.k8, D, rows, PIECE) != CUDA_SUCCESS ||
-      encode_tensor_map_2d_u8(&maps.v, g.v8, D, rows, PIECE) != CUDA_SUCCESS)
+  if (encode_tensor_map_2d_u8(&maps.k, g.k8, D, rows, HALF) != CUDA_SUCCESS ||
+      encode_tensor_map_2d_u8(&maps.v, g.v8, D, rows, HALF) != CUDA_SUCCESS)
     return cudaErrorInvalidValue;
   const cudaError_t e =
-      cudaFuncSetAttribute(kv_attn_rows_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, RowsCfg<D>::SMEM);
+      cudaFuncSetAttribute(kv_attn_rows_kernel<D, RP>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::ALLOC);
   if (e != cudaSuccess) return e;
-  kv_attn_rows_kernel<D><<<dim3(p.row_tiles * p.splits, g.hkv, g.B), WARPS * 32, RowsCfg<D>::SMEM, s>>>(g, p, maps);
+  kv_attn_rows_kernel<D, RP><<<dim3(p.splits, g.hkv, g.B), THREADS, Cfg::ALLOC, s>>>(g, p, maps);
   return cudaGetLastError();
+}
+
+template <int D>
+cudaError_t launch_rows(const KvGeom& g, const KvAttnParams& p, cudaStream_t s) {
+  return p.rows_cap <= 4 ? launch_rows_t<D, 4>(g, p, s)
+                         : p.rows_cap <= 8 ? launch_rows_t<D, 8>(g, p, s) : launch_rows_t<D, 16>(g, p, s);
 }
 
 }  // namespace
@@ -456,12 +580,12 @@ static int n_tok(int rows, int group) { return (rows + group - 1) / group + 1; }
 
 size_t kv_attn_plan(const KvGeom& g, KvAttnParams& p, bool weights, uint8_t* ws) {
   const long long rows = (long long)p.n_q * p.group;
-  p.tiles = rows > TILE_KERNEL_ROWS;
-  p.tile_rows = p.tiles ? 256 : ROWS;
+  p.tiles = rows > FEW_ROWS;
+  p.tile_rows = p.tiles ? 256 : FEW_ROWS;
   p.row_tiles = (int)((rows + p.tile_rows - 1) / p.tile_rows);
   p.rows_cap = (int)rows;
   p.rows_pad = p.row_tiles * p.tile_rows;
-  p.piece = p.tiles ? g.tile : PIECE;
+  p.piece = p.tiles ? g.tile : 32;
   p.pieces_cap = g.nb_cap * (g.tile / p.piece);
   const long long ctas = (long long)g.B * g.hkv * p.row_tiles, keys = (long long)g.nb_cap * g.tile;
   p.splits = 1;
@@ -482,7 +606,8 @@ size_t kv_attn_plan(const KvGeom& g, KvAttnParams& p, bool weights, uint8_t* ws)
       }
     }
   } else {
-    const long long want = (148 * 6 + ctas - 1) / ctas, most = (keys + PIECE * WARPS - 1) / (PIECE * WARPS);
+    // two CTAs per SM, each with a step at least
+    const long long want = 296 / ctas, most = (keys + STEP - 1) / STEP;
     p.splits = (int)(want < most ? want : most);
     if (p.splits < 1) p.splits = 1;
   }
@@ -494,11 +619,11 @@ size_t kv_attn_plan(const KvGeom& g, KvAttnParams& p, bool weights, uint8_t* ws)
   };
   const size_t prows = (size_t)g.B * g.hkv * p.splits * p.rows_pad;
   p.part_ml = reinterpret_cast<float2*>(take(prows * 8));
-  p.part_o = p.tiles && p.splits == 1 ? nullptr : reinterpret_cast<float*>(take(prows * g.d * 4));
+  p.part_o = p.splits == 1 ? nullptr : reinterpret_cast<float*>(take(prows * g.d * 4));
   p.lse2 = nullptr;
   p.lw = nullptr;
   if (weights) {
-    p.lse2 = reinterpret_cast<float*>(take((size_t)g.B * g.hkv * rows * 4));
+    if (p.tiles) p.lse2 = reinterpret_cast<float*>(take((size_t)g.B * g.hkv * rows * 4));
     p.lw = reinterpret_cast<float*>(take((size_t)g.B * g.hkv * rows * p.pieces_cap * 4));
   }
   return off;
@@ -514,9 +639,10 @@ size_t kv_attn_ws_bytes(const KvGeom& g, int heads, int n_q, bool weights) {
 
 cudaError_t launch_kv_attn(const KvGeom& g, KvAttnParams p, void* ws, cudaStream_t s) {
   kv_attn_plan(g, p, p.weight != nullptr, static_cast<uint8_t*>(ws));
-  cudaError_t e = p.tiles ? launch_kv_attn_tiles(g, p, s) : g.d == 128 ? launch_rows<128>(g, p, s) : launch_rows<64>(g, p, s);
+  if (!p.tiles) return g.d == 128 ? launch_rows<128>(g, p, s) : launch_rows<64>(g, p, s);
+  cudaError_t e = launch_kv_attn_tiles(g, p, s);
   if (e != cudaSuccess) return e;
-  if (!p.tiles || p.splits > 1) {
+  if (p.splits > 1) {
     const dim3 jg((p.rows_cap + 3) / 4, g.hkv, g.B);
     if (g.d == 128) kv_join_kernel<128><<<jg, 128, 0, s>>>(g, p);
     else kv_join_kernel<64><<<jg, 128, 0, s>>>(g, p);

@@ -111,6 +111,98 @@ __device__ __forceinline__ KvRange kv_range(const KvGeom& g, const KvAttnParams&
   return r;
 }
 
+// ------------------------------------------------------- steps of 128 keys
+constexpr int STEP = 128, HALF = 64;  // a step is two halves of 64 keys, each a TMA box of its own
+
+// What a step's consumers need to know. Written before the step's copies are
+// announced, so whoever has seen those copies (or an MMA on them) complete can
+// read it.
+struct StepMeta {
+  float ks[2], ev[2], rv[2];  // K scale, log2 of the V scale, its inverse
+  int pos[2], left[2];        // first position, keys that exist
+  int entry[2];               // table entry, -1 for none
+  int full;                   // every query of the CTA sees all 128 keys
+  int pad;
+};
+static_assert(sizeof(StepMeta) % 8 == 0, "barriers follow");
+
+// The producer warp's view of the steps: lane j holds what half j of the next
+// 16 steps needs, so a step's table entry and scales cost no latency.
+struct StepFeed {
+  int pool, entry, pos, left;
+  float ks, vs;
+
+  // halves of steps e .. e+15 of this CTA, whose first step is s_lo of all
+  __device__ void load(const KvGeom& g, long long trow, const KvRange& rg, int total, int s_lo, int e, int n_steps,
+                       int lane) {
+    const int half = 2 * (s_lo + e) + lane, one = g.tile == STEP;  // 64-key halves of the tiles seen
+    const int vt = one ? half >> 1 : half, sub = one ? half & 1 : 0;
+    pool = entry = -1;
+    pos = left = 0;
+    ks = 0.f;
+    vs = 1.f;
+    if (vt < rg.count() && e + (lane >> 1) < n_steps) {
+      const int i = rg.tile(vt);
+      const int slot = g.table[trow + i];
+      entry = i;
+      pos = g.pos[trow + i] + sub * HALF;
+      const float k = g.k_scale[trow + i], v = g.v_scale[trow + i];
+      if (slot >= 0 && slot < g.n_slots) {
+        left = max(0, min(HALF, total - (i * g.tile + sub * HALF)));
+        pool = left > 0 ? slot * g.tile + sub * HALF : -1;
+        ks = k;
+        vs = v;
+      } else {
+        report(g.dev_status, VEDA_ERR_BAD_INDEX);
+      }
+    }
+  }
+
+  // The description of step e (all lanes call), and the pool rows of its
+  // halves (-1: no copy).
+  __device__ void put(StepMeta& m, const KvGeom& g, const KvAttnParams& p, int e, int t_lo, int t_hi, int lane,
+                      int& row0, int& row1) const {
+    const int l0 = 2 * (e & 15);
+    const bool seen = left == HALF && (!p.causal || pos + HALF - 1 <= t_lo) &&
+                      (p.window <= 0 || pos + HALF <= p.sinks || (long long)pos > (long long)t_hi - p.window);
+    const int both = (__ballot_sync(0xffffffffu, seen) >> l0 & 3u) == 3u;
+    if (lane == l0 || lane == l0 + 1) {
+      const int x = lane & 1;
+      m.ks[x] = ks;
+      m.ev[x] = log2f(vs);
+      m.rv[x] = 1.0f / vs;
+      m.pos[x] = pos;
+      m.left[x] = left;
+      m.entry[x] = entry;
+      m.full = both;
+    }
+    row0 = __shfl_sync(0xffffffffu, pool, l0);
+    row1 = __shfl_sync(0xffffffffu, pool, l0 + 1);
+  }
+};
+
+// D[tmem] (+)= A * B on e4m3 operands in shared memory.
+__device__ __forceinline__ void umma_f8_ss(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem), "l"(a), "l"(b), "r"(idesc),
+      "r"(acc) : "memory");
+}
+// Instruction descriptor for M x N with fp32 D and A, B of format 0 (e4m3, or fp16 in kind::f16).
+__host__ __device__ constexpr uint32_t idesc_fmt0(int M, int N, bool a_mn_major, bool b_mn_major) {
+  return (1u << 4) | ((a_mn_major ? 1u : 0u) << 15) | ((b_mn_major ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) |
+         ((uint32_t)(M >> 4) << 24);
+}
+// Operand of D-byte rows in shared memory, swizzled over them (128 or 64
+// bytes), eight rows to an atom; `lbo`: bytes between column groups where the
+// rows run along K.
+template <int D>
+__device__ __forceinline__ uint64_t sdesc_codes(uint32_t saddr, uint32_t lbo = 16) {
+  uint64_t d = sdesc_sw128(saddr, lbo, 8 * D);
+  if (D == 64) d = (d & ~((uint64_t)7 << 61)) | ((uint64_t)4 << 61);  // SWIZZLE_64B
+  return d;
+}
+
 cudaError_t launch_kv_attn_tiles(const KvGeom& g, const KvAttnParams& p, cudaStream_t s);
 
 }  // namespace veda

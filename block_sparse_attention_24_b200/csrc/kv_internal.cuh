@@ -22,6 +22,7 @@ struct KvGeom {
   float* weight;
   int32_t* len;       // [B, hkv]
   int32_t* next_pos;  // [B]
+  int32_t* arrive;    // [B, hkv], 0 between calls
   int32_t* dev_status;
 };
 
@@ -47,6 +48,7 @@ struct KvAttnParams {
   int32_t splits, row_tiles, rows_cap, rows_pad, tile_rows;
   int32_t piece, pieces_cap;  // keys per entry of lw, entries per head
   float* part_o;   // [B, hkv, splits, rows_pad, d]
+  int32_t* arrive;
   float2* part_ml; // [B, hkv, splits, rows_pad]: reference (log2) and sum
   float* lse2;     // [B, hkv, rows_cap] log2
   float* lw;       // [B, hkv, pieces_cap, rows_cap] log2 of a piece's sum

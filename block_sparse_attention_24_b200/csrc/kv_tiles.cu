@@ -32,25 +32,15 @@ namespace veda {
 namespace {
 
 constexpr int BM = 128, BN = 128;
-constexpr int HALF = 64;               // keys per TMA box; a step is two halves
 constexpr int KST = 3, VST = 2, WST = 2;  // stages: K codes, V codes, V fp16
-// Step descriptions: written before the step's copies are announced, so whoever
-// has seen those copies (or an MMA on them) complete can read them; a slot is
-// written again only after the softmax of the step before step_done's.
+// A description's slot is written again only after the softmax of the step
+// before step_done's.
 constexpr int MST = KST + 2;
 constexpr int SDR = 4;                 // step-done barriers
 constexpr float OVERFLOW_SUM = 32768.f;
 constexpr int THREADS = 384, CONVERT_WARPS = 2;
 // 2*128*208 + 128*88 = 64,512 = the 384*168 of the launch
 constexpr int REGS_SOFTMAX = 208, REGS_ROLES = 88;
-
-struct StepMeta {
-  float ks[2], ev[2], rv[2];  // K scale, log2 of the V scale, its inverse
-  int pos[2], left[2];        // first position, keys that exist
-  int entry[2];               // table entry, -1 for none
-  int full;                   // every query of the CTA sees all 128 keys
-  int pad;
-};
 
 template <int D>
 struct TileLayout {
@@ -117,25 +107,6 @@ __device__ __forceinline__ float half_p(const uint32_t (&u)[64], float c, float 
   float lo, hi;
   f2_split(f2_add(f2_add(acc[0], acc[1]), f2_add(acc[2], acc[3])), lo, hi);
   return lo + hi;
-}
-
-// D[tmem] (+)= A * B: e4m3 from shared memory, or fp16 with A in tensor memory.
-__device__ __forceinline__ void umma_f8_ss(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem), "l"(a), "l"(b), "r"(idesc),
-      "r"(acc) : "memory");
-}
-// Instruction descriptor for M x N with fp32 D and A, B of format 0 (e4m3, or fp16 in kind::f16).
-__host__ __device__ constexpr uint32_t idesc_fmt0(int M, int N, bool b_mn_major) {
-  return (1u << 4) | ((b_mn_major ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
-}
-// K-major operand of D-byte rows, swizzled over them (128 or 64 bytes).
-template <int D>
-__device__ __forceinline__ uint64_t sdesc_codes(uint32_t saddr) {
-  uint64_t d = sdesc_sw128(saddr, 16, 8 * D);
-  if (D == 64) d = (d & ~((uint64_t)7 << 61)) | ((uint64_t)4 << 61);  // SWIZZLE_64B
-  return d;
 }
 
 template <int D>
@@ -212,55 +183,18 @@ __global__ void __launch_bounds__(THREADS, 1)
     regs_lower<REGS_ROLES>();
     if (warp == 8) {
       // --------------------------------------------------------- producer
-      // lane j holds what the step's halves need, 16 steps at a time
-      int pool = -1, entry = -1, pos = 0, left = 0;
-      float ks = 0.f, vs = 1.f;
+      StepFeed feed;
       int e = 0;
       bool ok = true;
       for (; e < n_steps; ++e) {
-        if ((e & 15) == 0) {
-          const int half = 2 * (s_lo + e) + lane;  // 64-key halves of the tiles seen
-          const int vt = per_step == 1 ? half >> 1 : half, sub = per_step == 1 ? half & 1 : 0;
-          pool = entry = -1;
-          left = 0;
-          ks = 0.f;
-          vs = 1.f;
-          if (vt < n_tiles && e + (lane >> 1) < n_steps) {
-            const int i = rg.tile(vt);
-            const int slot = g.table[trow + i];
-            entry = i;
-            pos = g.pos[trow + i] + sub * HALF;
-            if (slot >= 0 && slot < g.n_slots) {
-              left = max(0, min(HALF, total - (i * g.tile + sub * HALF)));
-              pool = left > 0 ? slot * g.tile + sub * HALF : -1;
-              ks = g.k_scale[trow + i];
-              vs = g.v_scale[trow + i];
-            } else {
-              report(g.dev_status, VEDA_ERR_BAD_INDEX);
-            }
-          }
-        }
-        const int l0 = 2 * (e & 15);
+        if ((e & 15) == 0) feed.load(g, trow, rg, total, s_lo, e, n_steps, lane);
         const int st = e % KST, vt = e % VST, ms = e % MST;
         // the description's slot is free: step_done(e - KST) follows the softmax of step e - KST - 1
         if (e >= KST) ok = mbar_wait(step_done + (e - KST) % SDR, ((e - KST) / SDR) & 1, abort_flag, g.dev_status);
         if (ok && e >= VST) ok = mbar_wait(v_free + vt, (e / VST - 1) & 1, abort_flag, g.dev_status);
         if (!__all_sync(0xffffffffu, ok)) break;
-        const bool seen = left == HALF && (!p.causal || pos + HALF - 1 <= t_lo) &&
-                          (p.window <= 0 || pos + HALF <= p.sinks || (long long)pos > (long long)t_hi - p.window);
-        const int both = (__ballot_sync(0xffffffffu, seen) >> l0 & 3u) == 3u;
-        if (lane == l0 || lane == l0 + 1) {
-          const int x = lane & 1;
-          StepMeta& m = meta[ms];
-          m.ks[x] = ks;
-          m.ev[x] = log2f(vs);
-          m.rv[x] = 1.0f / vs;
-          m.pos[x] = pos;
-          m.left[x] = left;
-          m.entry[x] = entry;
-          m.full = both;
-        }
-        const int row0 = __shfl_sync(0xffffffffu, pool, l0), row1 = __shfl_sync(0xffffffffu, pool, l0 + 1);
+        int row0, row1;
+        feed.put(meta[ms], g, p, e, t_lo, t_hi, lane, row0, row1);
         __syncwarp();
         if (lane == 0) {
           const uint32_t bytes = (row0 >= 0 ? Lay::CB / 2 : 0) + (row1 >= 0 ? Lay::CB / 2 : 0);
@@ -282,8 +216,8 @@ __global__ void __launch_bounds__(THREADS, 1)
     } else if (warp == 9) {
       if (lane == 0) {
       // ------------------------------------------------------- MMA issuer
-      constexpr uint32_t idesc_s = idesc_fmt0(BM, BN, false);
-      constexpr uint32_t idesc_o = idesc_fmt0(BM, D, true);
+      constexpr uint32_t idesc_s = idesc_fmt0(BM, BN, false, false);
+      constexpr uint32_t idesc_o = idesc_fmt0(BM, D, false, true);
       const uint64_t dQ = sdesc_codes<D>(smem_u32(smem + Lay::OFF_Q));
       const uint64_t dK = sdesc_codes<D>(smem_u32(smem + Lay::OFF_K));
       const uint64_t dW = sdesc_sw128(smem_u32(smem + Lay::OFF_W), BN * 128, 1024);

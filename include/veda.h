@@ -357,6 +357,7 @@ int veda_output_sq_error(const veda_layer* L, const void* a, const void* b, floa
  *                others follow it. Ascending in i over the tiles in use.
  *   next_pos[b]  position of the sequence's next token (len lags behind it
  *                once tiles have been evicted)
+ *   arrive       counters of veda_kv_attn, which leaves them zero
  *   weight       attention that the tile has received (veda_kv_attn); may be
  *                NULL where it is neither taken nor used
  * All pointers are DEVICE memory, 16-byte aligned, all arrays contiguous;
@@ -388,6 +389,7 @@ typedef struct {
   float *k_scale, *v_scale, *weight;
   int32_t* len;                  /* [B, heads_kv] */
   int32_t* next_pos;             /* [B] */
+  int32_t* arrive;               /* [B, heads_kv], zero before first use */
   int32_t* dev_status;           /* as in veda_layer */
 } veda_kv_cache;
 

@@ -3,23 +3,25 @@ advance and evict alone at the sizes and masks where each can go wrong, then
 together as a stream uses them.
 
 Tolerances of attention, per element. K and V are exact (codes times scales).
-  logits  products of fp16 and e4m3 values are exact in fp32; summing d of
-          them (and two factors) costs at most d * 2^-23 of sum |q||k| =: S
-          (the tensor core may truncate each partial sum, hence 2^-23), and
-          the exponent's argument, at most 2 S in magnitude next to its
-          reference, and ex2 another 2^-22 * (1 + 4 S): D = 2^-16 * (1 + S)
-          covers both for d <= 128. With more query rows per K/V head than
-          FEW, q is taken in two e4m3 parts, each row scaled so that its
-          largest value is at 2^7 or above: what is left is half a step of
-          e4m3's subnormals, 2^-10, at most: 2^-17 of max |q|, and D grows
-          by 2^-17 * Q, Q = scale * max |q| * sum |k|.
-  P       fp16, relative to the largest p_j sv_j =: R of the row, which is at
-          2^7 or above: 2^-11 of each weight, and 2^-25 where it is subnormal,
-          that is 2^-32 R per key, times a code of up to 448 in any channel
-          (that key's, so A, which may be small in that channel, does not
-          bound it).
-  O       with A = sum p |v|: (2^-11 + 4 D) * A + keys * 2^-32 * 448 * R before
-          its own bf16 rounding of 2^-8 |O| (half a step).
+  logits  products of e4m3 values are exact in fp32; summing d of them (and
+          two factors) costs at most d * 2^-23 of sum |q||k| =: S (the tensor
+          core may truncate each partial sum, hence 2^-23), and the exponent's
+          argument, at most 2 S in magnitude next to its reference, and ex2
+          another 2^-22 * (1 + 4 S): D = 2^-16 * (1 + S) covers both for
+          d <= 128.
+  q       each row scaled so that its largest value is at 2^7 or above. In two
+          e4m3 parts (more query rows per K/V head than FEW) what is left is
+          half a step of e4m3's subnormals, 2^-10, at most: 2^-17 of max |q|,
+          and D grows by 2^-17 * Q, Q = scale * max |q| * sum |k|. In four
+          parts, each of 16 times what the last one left, it is 2^-29.
+  P       relative to the largest p_j sv_j =: R of the row, which is at 2^7 or
+          above. As fp16: 2^-11 of each weight, and 2^-25 where it is
+          subnormal, 2^-32 R per key. In four e4m3 parts: 2^-16 of each, and
+          2^-10 / 16^3 = 2^-22 where the last part is subnormal, 2^-29 R per
+          key. Each times a code of up to 448 in any channel (that key's, so A,
+          which may be small in that channel, does not bound it).
+  O       with A = sum p |v|: (2^-11 + 4 D) * A + keys * (2^-32 or 2^-29) * 448
+          * R before its own bf16 rounding of 2^-8 |O| (half a step).
   lse     D + 2^-22 * |lse|.
   weight  (4 D + 2^-20) of itself."""
 import numpy as np
@@ -31,7 +33,7 @@ from oracle.kv_oracle import Cache
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda:0"
-FEW = 32          # query rows per K/V head up to which q is taken whole, in fp16
+FEW = 16          # query rows per K/V head up to which q and P are taken in four parts
 
 
 def host(t):
@@ -113,7 +115,8 @@ def check_attention(c, q, news=None, causal=True, window=0, sinks=0, pending=Tru
                    pending=pending, lse=lse, weight=c.weight if weight else None, decay=decay)
     V.veda_kv_check_status(c)
     keys = c.nb_cap * c.tile
-    D = 2.0 ** -16 * (1 + S) + (2.0 ** -17 * Q if n * heads // c.heads_kv > FEW else 0.0)      # [B, heads, n]
+    few = n * heads // c.heads_kv <= FEW
+    D = 2.0 ** -16 * (1 + S) + 2.0 ** (-29 if few else -17) * Q          # [B, heads, n]
     for b in range(B):
         m = n if news is None else news[b]
         # rows behind the sequence's own are left as they were
@@ -127,7 +130,7 @@ def check_attention(c, q, news=None, causal=True, window=0, sinks=0, pending=Tru
         np.testing.assert_array_equal(gl[~fin], wl[~fin])
         assert np.all(np.abs(gl[fin] - wl[fin]) <= (dd + 2.0 ** -22 * np.abs(wl))[fin])
         tol = ((2.0 ** -11 + 4 * dd.transpose(1, 0)[..., None]) * a + 2.0 ** -8 * np.abs(wo)
-               + keys * 2.0 ** -32 * 448 * R[b, :, :m].transpose(1, 0)[..., None])
+               + keys * 2.0 ** (-29 if few else -32) * 448 * R[b, :, :m].transpose(1, 0)[..., None])
         ok = np.isnan(wo) | (np.abs(go - wo) <= tol)
         assert ok.all(), f"batch {b}: {np.max((np.abs(go - wo) - tol)[~np.isnan(wo)])} over"
     if weight:

@@ -17,7 +17,7 @@ FAKE = 0x1000          # aligned, never dereferenced by a refused call
 def cache(**over):
     f = dict(B=2, heads_kv=3, d=64, tile=64, n_slots=24, nb_cap=4)
     f.update({n: FAKE for n in ("k8", "v8", "table", "pos", "k_scale", "v_scale", "weight", "len", "next_pos",
-                                "dev_status")})
+                                "arrive", "dev_status")})
     f.update(over)
     return V._KvCache(*[f[n] for n, _ in V._KvCache._fields_])
 
@@ -40,7 +40,7 @@ BAD_CACHES = [
     (dict(table=None), V.VEDA_ERR_INVALID_ARG, "table"), (dict(pos=FAKE + 4), V.VEDA_ERR_INVALID_ARG, "pos"),
     (dict(k_scale=None), V.VEDA_ERR_INVALID_ARG, "k_scale"), (dict(v_scale=None), V.VEDA_ERR_INVALID_ARG, "v_scale"),
     (dict(weight=FAKE + 4), V.VEDA_ERR_INVALID_ARG, "weight"), (dict(len=None), V.VEDA_ERR_INVALID_ARG, "len"),
-    (dict(next_pos=None), V.VEDA_ERR_INVALID_ARG, "next_pos"),
+    (dict(next_pos=None), V.VEDA_ERR_INVALID_ARG, "next_pos"), (dict(arrive=None), V.VEDA_ERR_INVALID_ARG, "arrive"),
 ]
 
 
