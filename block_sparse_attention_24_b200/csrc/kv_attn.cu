@@ -399,25 +399,43 @@ __global__ void __launch_bounds__(THREADS, 2)
       last = cnt[3] != 0;
       if (last) {
         __threadfence();
+        // a warp per row: its parts' factors, then each thread its channel
         const float2* ml = p.part_ml + (long long)bh * p.splits * p.rows_pad;
-        const float* po = p.part_o + (long long)bh * p.splits * p.rows_pad * D;
+        const float* po = p.part_o + (long long)bh * p.splits * p.rows_pad * D + tid;
+        float* fac = reinterpret_cast<float*>(smem);  // [parts][RP], in the ring
+        for (int r = warp; r < rows; r += 4) {
+          float mx = -INFINITY, ls = 0.f;
+          for (int s = lane; s < parts; s += 32) mx = fmaxf(mx, __ldcg(&ml[(long long)s * p.rows_pad + r].x));
 #pragma unroll
-        for (int r = 0; r < RP; ++r) {
-          if (r >= rows) break;
-          float mx = -INFINITY, ls = 0.f, os = 0.f;
-#pragma unroll 4
-          for (int s = 0; s < parts; ++s) mx = fmaxf(mx, __ldcg(&ml[(long long)s * p.rows_pad + r].x));
-#pragma unroll 4
-          for (int s = 0; s < parts; ++s) {
+          for (int d = 16; d; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+          for (int s = lane; s < parts; s += 32) {
             const float2 v = __ldcg(&ml[(long long)s * p.rows_pad + r]);
             const float f = v.x == -INFINITY ? (v.y == v.y ? 0.f : 1.f) : fast_exp2(v.x - mx);
+            fac[s * RP + r] = f;
             ls += v.y * f;
-            if (tid < D) os += __ldcg(&po[((long long)s * p.rows_pad + r) * D + tid]) * f;
           }
-          m[r] = mx;
-          l[r] = ls;
-          o[r] = os;
+#pragma unroll
+          for (int d = 16; d; d >>= 1) ls += __shfl_xor_sync(0xffffffffu, ls, d);
+          if (lane == 0) {
+            red[r] = mx;
+            red[RP + r] = ls;
+          }
         }
+        softmax_sync();
+#pragma unroll
+        for (int r = 0; r < RP; ++r) {
+          m[r] = red[r];
+          l[r] = red[RP + r];
+          o[r] = 0.f;
+        }
+        if (tid < D)
+          for (int s = 0; s < parts; ++s) {
+            float v[RP];
+#pragma unroll
+            for (int r = 0; r < RP; ++r) v[r] = r < rows ? __ldcg(po + ((long long)s * p.rows_pad + r) * D) : 0.f;
+#pragma unroll
+            for (int r = 0; r < RP; ++r) o[r] = fmaf(v[r], r < rows ? fac[s * RP + r] : 0.f, o[r]);
+          }
       }
     }
     if (last) {
@@ -437,21 +455,27 @@ __global__ void __launch_bounds__(THREADS, 2)
       }
       if (p.weight) {
         softmax_sync();
-        const int ppt = g.tile / 32;
-        for (int i = tid; i < nb; i += 128) {
+        // a thread per piece, those of a tile side by side
+        const int ppt = g.tile / 32, pieces = nb * ppt;
+        for (int base = 0; base < pieces; base += 128) {
+          const int pc = base + tid, i = pc / ppt;
           float w = 0.f;
-          if (kv_tile_seen(g.pos[trow + i], g.tile, t_lo, t_hi, p.causal, p.window, p.sinks)) {
-            const float* lw = p.lw + ((long long)bh * p.pieces_cap + (long long)i * ppt) * p.rows_cap;
-            for (int k = 0; k < ppt && i * g.tile + k * 32 < total; ++k)
+          if (pc < pieces && pc * 32 < total &&
+              kv_tile_seen(g.pos[trow + i], g.tile, t_lo, t_hi, p.causal, p.window, p.sinks)) {
+            const float* lw = p.lw + ((long long)bh * p.pieces_cap + pc) * p.rows_cap;
+            float v[RP];
 #pragma unroll
-              for (int r = 0; r < RP; ++r) {
-                if (r >= rows) break;
-                const float v = __ldcg(&lw[(long long)k * p.rows_cap + r]), z = qs[r];
-                // none of it seen: nothing, even of a row that is NaN
-                if (v != -INFINITY && z != -INFINITY) w += fast_exp2(v - z);
-              }
+            for (int r = 0; r < RP; ++r) v[r] = r < rows ? __ldcg(lw + r) : -INFINITY;
+#pragma unroll
+            for (int r = 0; r < RP; ++r) {
+              const float z = r < rows ? qs[r] : 0.f;
+              // none of it seen: nothing, even of a row that is NaN
+              if (v[r] != -INFINITY && z != -INFINITY) w += fast_exp2(v[r] - z);
+            }
           }
-          p.weight[trow + i] = p.decay == 0.f ? w : p.decay * p.weight[trow + i] + w;
+          for (int d = 1; d < ppt; d <<= 1) w += __shfl_xor_sync(0xffffffffu, w, d);
+          if (pc < pieces && pc % ppt == 0)
+            p.weight[trow + i] = p.decay == 0.f ? w : p.decay * p.weight[trow + i] + w;
         }
       }
     }
