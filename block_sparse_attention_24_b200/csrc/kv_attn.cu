@@ -11,6 +11,7 @@
 // exact for powers of two. M is a reference, not the maximum: it moves only
 // when some x passes it by a margin, so that P stays within its type (fp16 in
 // the tile kernel, e4m3 parts here). Sums, references and O are fp32.
+#include <climits>
 #include <cmath>
 
 #include "kv_attn.cuh"
@@ -30,31 +31,33 @@ namespace {
 //                 the upper half of M repeats the lower), B = P^T, in four
 //                 parts too: 16 bits, down to 2^-29 of the row's largest.
 // A thread owns a key (TMEM lane) of S^T and a channel of O^T; the rows are
-// columns, so the work per key goes with the rows there are. A step (128 keys)
-// is S, softmax, P V in turn; about a thousand clocks, which two CTAs per SM
-// hide behind the 2,800 that a step's bytes take for each of them.
-//   warps 0-3  softmax; thread 0 issues the MMAs
+// columns, so the work per key goes with the rows there are. S and P are
+// double-buffered: a step's S is issued as soon as its K has arrived, beside
+// the softmax of the step before.
+//   warps 0-3  softmax
 //   warp 4     producer: table, scales, TMA
+//   warp 5     MMA issuer (one thread; issuing blocks it, so it is no softmax thread)
 // The CTAs that share a head's keys count themselves in `arrive`; the last one
 // joins their parts, and sums the tile weights.
 constexpr int FEW_ROWS = 16;
-constexpr int THREADS = 160;
+constexpr int THREADS = 192;
 constexpr float MARGIN = 1.5f;  // P <= 2^(OFF + MARGIN) = 362 < 448
 
 template <int D, int RP>
 struct RowsCfg {
   static constexpr int N = 4 * RP;
   static constexpr int CB = STEP * D;                           // bytes of a step's K or V codes
-  static constexpr int ST = D == 64 ? 6 : (RP == 16 ? 2 : 3);   // ring stages: two CTAs per SM
+  static constexpr int ST = D == 64 ? (RP == 16 ? 5 : 6) : (RP == 16 ? 2 : 3);  // ring stages: two CTAs per SM
   static constexpr int OFF_Q = ST * 2 * CB;
   static constexpr int OFF_P = OFF_Q + N * D;
-  static constexpr int OFF_META = OFF_P + N * STEP;
+  static constexpr int OFF_META = OFF_P + 2 * N * STEP;
   static constexpr int OFF_BAR = OFF_META + ST * (int)sizeof(StepMeta);
-  static constexpr int NUM_BARS = 3 * ST + 1;                   // K, V, free per stage; S
-  static constexpr int OFF_RED = OFF_BAR + NUM_BARS * 8;        // float [4][RP], then [RP] factors, int [RP] positions
-  static constexpr int OFF_MISC = OFF_RED + 6 * RP * 4;
+  static constexpr int NUM_BARS = 3 * ST + 4;                   // K, V, free per stage; S twice; P; drain
+  static constexpr int OFF_RED = OFF_BAR + NUM_BARS * 8;        // float [4][RP], then [RP] factors, int [2][RP] position bounds
+  static constexpr int OFF_MISC = OFF_RED + 7 * RP * 4;
   static constexpr int ALLOC = OFF_MISC + 32 + 1024;
-  static constexpr int TMEM = 2 * N < 32 ? 32 : 2 * N;          // S^T, O^T
+  static constexpr int TMEM = 4 * N;                            // S^T twice, O^T
+  static_assert(2 * (ALLOC + 1024) <= 233472, "two CTAs per SM");
 };
 
 __device__ __forceinline__ void softmax_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
@@ -76,6 +79,26 @@ __device__ __forceinline__ void tmem_store(uint32_t addr, const uint32_t (&u)[N]
   if constexpr (N == 16) tmem_st16(addr, u);
   else if constexpr (N == 32) tmem_st32(addr, u);
   else tmem_st64(addr, u);
+}
+
+// Sums of every row's value over the warp, the rows halved between the lanes
+// at each step: v[0] of the lanes from r * (32 / RP) on is row r's sum, and
+// ref[0] the row's `ref`.
+template <int N, int DIST, int RP>
+__device__ __forceinline__ void warp_rows(float (&v)[RP], float (&ref)[RP], int lane) {
+  if constexpr (N > 1) {
+    const bool up = lane & DIST;
+#pragma unroll
+    for (int r = 0; r < N / 2; ++r) {
+      const float keep = up ? v[N / 2 + r] : v[r], give = up ? v[r] : v[N / 2 + r];
+      v[r] = keep + __shfl_xor_sync(0xffffffffu, give, DIST);
+      ref[r] = up ? ref[N / 2 + r] : ref[r];
+    }
+    warp_rows<N / 2, DIST / 2>(v, ref, lane);
+  } else {
+#pragma unroll
+    for (int d = DIST; d; d /= 2) v[0] += __shfl_xor_sync(0xffffffffu, v[0], d);
+  }
 }
 
 // Two values as four e4m3 parts each: part k is the code nearest to 16 times
@@ -104,25 +127,41 @@ __global__ void __launch_bounds__(THREADS, 2)
   const int sp = blockIdx.x, h = blockIdx.y, b = blockIdx.z;
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
   int n_b, held, total;
+  const int t_lo = g.next_pos[b];
   if (!kv_counts(g, b, h, p.n_q, p.n_new, p.pending, n_b, held, total)) return;
   const int rows = n_b * p.group;
   if (rows == 0) return;
   const int bh = b * g.hkv + h;
   const long long trow = (long long)bh * g.nb_cap;
-  const int t_lo = g.next_pos[b], t_hi = t_lo + n_b - 1;
+  const int t_hi = t_lo + n_b - 1;
+  // Q: 128 / RP threads per row
+  constexpr int TPR = 128 / RP, EL = D / TPR;
+  const int qr = tid / TPR, qd = tid % TPR * EL;
+  uint32_t qw[EL / 2];
+#pragma unroll
+  for (int x = 0; x < EL / 2; ++x) qw[x] = 0;
+  if (qr < rows && warp < 4) {
+    const uint32_t* src = reinterpret_cast<const uint32_t*>(p.q.p + b * p.q.sb + (long long)(qr / p.group) * p.q.sn +
+                                                            (long long)(h * p.group + qr % p.group) * p.q.sh + qd);
+#pragma unroll
+    for (int x = 0; x < EL / 2; ++x) qw[x] = src[x];
+  }
 
   uint64_t* k_full = reinterpret_cast<uint64_t*>(smem + Cfg::OFF_BAR);
   uint64_t* v_full = k_full + ST;
   uint64_t* free_ = v_full + ST;  // P V of the stage's step has completed
-  uint64_t* s_full = free_ + ST;
+  uint64_t* s_full = free_ + ST;  // [2]
+  uint64_t* p_full = s_full + 2;  // 128 arrivals
+  uint64_t* drain = p_full + 1;
   StepMeta* meta = reinterpret_cast<StepMeta*>(smem + Cfg::OFF_META);
   float* red = reinterpret_cast<float*>(smem + Cfg::OFF_RED);
   float* qs = red + 4 * RP;
-  int* t_of = reinterpret_cast<int*>(qs + RP);
+  int* seen_hi = reinterpret_cast<int*>(qs + RP);  // a row sees positions p <= hi && (p > lo || p < sinks)
+  int* seen_lo = seen_hi + RP;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Cfg::OFF_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Cfg::OFF_MISC + 4);
   int* cnt = reinterpret_cast<int*>(smem + Cfg::OFF_MISC + 8);  // [3], then a flag
-  if (tid < Cfg::NUM_BARS) mbar_init(k_full + tid, 1);
+  if (tid < Cfg::NUM_BARS) mbar_init(k_full + tid, k_full + tid == p_full ? 128 : 1);
   if (tid < 4) cnt[tid] = 0;
   if (tid == 0) *abort_flag = 0;
   fence_mbar_init();
@@ -178,58 +217,80 @@ __global__ void __launch_bounds__(THREADS, 2)
         mbar_wait_drain(k_full + x % ST, (x / ST) & 1, VEDA_WAIT_LIMIT_NS);
         mbar_wait_drain(v_full + x % ST, (x / ST) & 1, VEDA_WAIT_LIMIT_NS);
       }
+  } else if (warp == 5) {
+    // ----------------------------------------------------------- MMA issuer
+    if (lane == 0 && n_steps > 0) {
+      constexpr uint32_t idesc_s = idesc_fmt0(128, N, false, false), idesc_o = idesc_fmt0(128, N, true, false);
+      const uint64_t dK = sdesc_codes<D>(smem_u32(smem)), dV = sdesc_codes<D>(smem_u32(smem + Cfg::CB), 0);
+      const uint64_t dQ = sdesc_codes<D>(smem_u32(smem + Cfg::OFF_Q)), dP = sdesc_codes<128>(smem_u32(smem + Cfg::OFF_P));
+      auto issue_s = [&](int e) {  // its K has arrived, and P V of step e-2 has been issued
+        const int st = e % ST;
+        tc_fence_after();
+#pragma unroll
+        for (int kk = 0; kk < D / 32; ++kk)
+          umma_f8_ss(tmem + (e & 1) * N, dK + (uint64_t)((st * 2 * Cfg::CB + kk * 32) >> 4), dQ + (uint64_t)(kk * 32 >> 4),
+                     idesc_s, kk > 0);
+        umma_commit(s_full + (e & 1));
+      };
+      auto k_here = [&](int e) { return mbar_wait(k_full + e % ST, (e / ST) & 1, abort_flag, g.dev_status); };
+      // phase 0 of p_full: Q is in shared memory; phase e + 1: P of step e
+      bool ok = mbar_wait(p_full, 0, abort_flag, g.dev_status) && k_here(0);
+      if (ok) issue_s(0);
+      for (int e = 0; ok && e < n_steps; ++e) {
+        const int st = e % ST;
+        bool ahead = e + 1 == n_steps;  // S of the next step is issued
+        // whichever comes first: the next K, or this P
+        for (int spin = 0; spin < 4096 && !mbar_test(p_full, (e + 1) & 1); ++spin)
+          if (!ahead && mbar_test(k_full + (e + 1) % ST, ((e + 1) / ST) & 1)) {
+            issue_s(e + 1);
+            ahead = true;
+          }
+        ok = mbar_wait(p_full, (e + 1) & 1, abort_flag, g.dev_status) &&
+             mbar_wait(v_full + st, (e / ST) & 1, abort_flag, g.dev_status);
+        if (!ok) break;
+        tc_fence_after();
+#pragma unroll
+        for (int q = 0; q < STEP / 32; ++q)
+          umma_f8_ss(tmem + 2 * N, dV + (uint64_t)((st * 2 * Cfg::CB + q * 32 * D) >> 4),
+                     dP + (uint64_t)(((e & 1) * N * STEP + q * 32) >> 4), idesc_o, (e > 0 || q > 0) ? 1u : 0u);
+        umma_commit(free_ + st);
+        if (!ahead) {
+          ok = k_here(e + 1);
+          if (ok) issue_s(e + 1);
+        }
+      }
+      umma_commit(drain);
+      mbar_wait_drain(drain, 0, VEDA_WAIT_LIMIT_NS);
+    }
   } else {
     // ----------------------------------------------------- Q in its parts
     {
-      constexpr int TPR = 128 / RP, EL = D / TPR;  // threads per row, their values
-      const int r = tid / TPR, d0 = tid % TPR * EL;
-      uint32_t w[EL / 2], top = 0;
-      if (r < rows) {
-        const uint32_t* src = reinterpret_cast<const uint32_t*>(p.q.p + b * p.q.sb + (long long)(r / p.group) * p.q.sn +
-                                                                (long long)(h * p.group + r % p.group) * p.q.sh + d0);
+      uint32_t top = 0;
 #pragma unroll
-        for (int x = 0; x < EL / 2; ++x) w[x] = src[x];
-      } else {
-#pragma unroll
-        for (int x = 0; x < EL / 2; ++x) w[x] = 0;
-      }
-#pragma unroll
-      for (int x = 0; x < EL / 2; ++x) top = max(top, bf16x2_top(w[x]));
+      for (int x = 0; x < EL / 2; ++x) top = max(top, bf16x2_top(qw[x]));
 #pragma unroll
       for (int d = 1; d < TPR; d <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
       float mul, inv;
       q_scale<7>(top, mul, inv);
       if (tid % TPR == 0) {
-        qs[r] = inv * p.scale_log2;
-        t_of[r] = t_lo + min(r, rows - 1) / p.group;
+        qs[qr] = inv * p.scale_log2;
+        const int t = t_lo + min(qr, rows - 1) / p.group;
+        seen_hi[qr] = p.causal ? t : INT_MAX;
+        seen_lo[qr] = p.window > 0 ? (int)max((long long)INT_MIN, (long long)t - p.window) : INT_MIN;
       }
 #pragma unroll
       for (int x = 0; x < EL / 2; ++x) {
         uint16_t c[4];
-        four_parts(__uint_as_float(w[x] << 16) * mul, __uint_as_float(w[x] & 0xffff0000u) * mul, c);
-        const int d = d0 + 2 * x;
+        four_parts(__uint_as_float(qw[x] << 16) * mul, __uint_as_float(qw[x] & 0xffff0000u) * mul, c);
+        const int d = qd + 2 * x;
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-          *reinterpret_cast<uint16_t*>(smem + Cfg::OFF_Q + code_at<D>(k * RP + r, d >> 4) + (d & 15)) = c[k];
+          *reinterpret_cast<uint16_t*>(smem + Cfg::OFF_Q + code_at<D>(k * RP + qr, d >> 4) + (d & 15)) = c[k];
       }
       fence_proxy_async_smem();
+      mbar_arrive(p_full);
       softmax_sync();
     }
-    constexpr uint32_t idesc_s = idesc_fmt0(128, N, false, false), idesc_o = idesc_fmt0(128, N, true, false);
-    const uint64_t dK = sdesc_codes<D>(smem_u32(smem)), dV = sdesc_codes<D>(smem_u32(smem + Cfg::CB), 0);
-    const uint64_t dQ = sdesc_codes<D>(smem_u32(smem + Cfg::OFF_Q)), dP = sdesc_codes<128>(smem_u32(smem + Cfg::OFF_P));
-    auto issue_s = [&](int e) {  // one thread
-      const int st = e % ST;
-      if (!mbar_wait(k_full + st, (e / ST) & 1, abort_flag, g.dev_status)) return;
-      tc_fence_after();
-#pragma unroll
-      for (int kk = 0; kk < D / 32; ++kk)
-        umma_f8_ss(tmem, dK + (uint64_t)((st * 2 * Cfg::CB + kk * 32) >> 4), dQ + (uint64_t)(kk * 32 >> 4), idesc_s,
-                   kk > 0);
-      umma_commit(s_full);
-    };
-    if (tid == 0 && n_steps > 0) issue_s(0);
-
     const uint32_t lane_addr = tmem + ((uint32_t)(warp * 32) << 16);
     const int half = tid >> 6, kk = tid & 63;  // this thread's key
     float m[RP], l[RP];
@@ -241,33 +302,36 @@ __global__ void __launch_bounds__(THREADS, 2)
     bool ok = true;
     for (int e = 0; e < n_steps; ++e) {
       const int st = e % ST;
-      ok = mbar_wait(s_full, e & 1, abort_flag, g.dev_status);
-      if (softmax_any(!ok)) break;
+      // (this S was issued behind P V of step e-2, whose P is overwritten here)
+      ok = mbar_wait(s_full + (e & 1), (e >> 1) & 1, abort_flag, g.dev_status);
       tc_fence_after();
       const StepMeta& sm = meta[st];
       uint32_t u[N];
-      tmem_load(lane_addr, u);
+      tmem_load(lane_addr + (e & 1) * N, u);
       const float sk = sm.ks[half], ev = sm.ev[half];
       const int left = sm.left[half], pos = sm.pos[half] + kk;
-      const bool full = sm.full;
+      const bool full = sm.full, first = pos < p.sinks || p.window <= 0;
       float x[RP];
-      bool over = false;
+      bool over = !ok;
 #pragma unroll
       for (int r = 0; r < RP; ++r) {
         const float s = fmaf(fmaf(fmaf(__uint_as_float(u[3 * RP + r]), 0.0625f, __uint_as_float(u[2 * RP + r])), 0.0625f,
                                   __uint_as_float(u[RP + r])), 0.0625f, __uint_as_float(u[r]));
         x[r] = fmaf(s, qs[r] * sk, ev);
-        if (!full && !(kk < left && kv_seen(pos, t_of[r], p.causal, p.window, p.sinks))) x[r] = -INFINITY;
+        if (!full && !((pos <= seen_hi[r]) & ((pos > seen_lo[r]) | first) & (kk < left))) x[r] = -INFINITY;
         over |= x[r] > m[r] + MARGIN;
       }
       if (softmax_any(over)) {
-        // new references: the largest x so far
+        if (*abort_flag) {
+          ok = false;
+          break;
+        }
+        // new references: the largest x so far, as integers that rank alike
 #pragma unroll
         for (int r = 0; r < RP; ++r) {
-          float v = x[r];
-#pragma unroll
-          for (int d = 16; d; d >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, d));
-          if (lane == r) red[warp * RP + r] = v;
+          const int i = __float_as_int(x[r] == x[r] ? x[r] : -INFINITY);
+          const int v = __reduce_max_sync(0xffffffffu, i ^ ((i >> 31) & 0x7fffffff));
+          if (lane == r) red[warp * RP + r] = __int_as_float(v ^ ((v >> 31) & 0x7fffffff));
         }
         softmax_sync();
         float al[RP];
@@ -279,12 +343,15 @@ __global__ void __launch_bounds__(THREADS, 2)
           m[r] = mn;
           l[r] *= al[r];
         }
-        if (e > 0) {  // O holds P V of all earlier steps: S of this one was issued behind them
+        if (e > 0) {  // O, once P V of the last step has completed
+          mbar_wait(free_ + (e - 1) % ST, ((e - 1) / ST) & 1, abort_flag, g.dev_status);
+          __syncwarp();
+          tc_fence_after();
           uint32_t o[N];
-          tmem_load(lane_addr + N, o);
+          tmem_load(lane_addr + 2 * N, o);
 #pragma unroll
           for (int k = 0; k < N; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * al[k % RP]);
-          tmem_store(lane_addr + N, o);
+          tmem_store(lane_addr + 2 * N, o);
         }
       }
       const float rv = sm.rv[half];
@@ -302,27 +369,12 @@ __global__ void __launch_bounds__(THREADS, 2)
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           const int n = k * RP + r;
-          uint8_t* dst = smem + Cfg::OFF_P + (tid & 15);
+          uint8_t* dst = smem + Cfg::OFF_P + (e & 1) * N * STEP + (tid & 15);
           dst[n * 128 + (((tid >> 4) ^ (n & 7)) << 4)] = (uint8_t)c[k];
           dst[(n + 1) * 128 + (((tid >> 4) ^ ((n + 1) & 7)) << 4)] = (uint8_t)(c[k] >> 8);
         }
       }
-      if (p.lw && sm.entry[half] >= 0) {
-        const int ppt = g.tile / 32;
-        const long long piece = (long long)bh * p.pieces_cap + sm.entry[half] * ppt + (warp & (ppt - 1));
-        float mine = 0.f, ref = 0.f;
-#pragma unroll
-        for (int r = 0; r < RP; ++r) {
-          float v = x[r];
-#pragma unroll
-          for (int d = 16; d; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
-          if (lane == r) {
-            mine = v;
-            ref = m[r];
-          }
-        }
-        if (lane < rows && lane < RP) p.lw[piece * p.rows_cap + lane] = mine == 0.f ? -INFINITY : log2f(mine) + (ref - OFF - ev);
-      }
+      const int entry = sm.entry[half];
       if (!full) {
         // V rows behind the last token become zeroes: their codes may be anything
         if (sm.left[0] + sm.left[1] < STEP) {
@@ -336,26 +388,22 @@ __global__ void __launch_bounds__(THREADS, 2)
       }
       fence_proxy_async_smem();
       tc_fence_before();
-      softmax_sync();
-      if (tid == 0) {
-        tc_fence_after();
-        if (mbar_wait(v_full + st, (e / ST) & 1, abort_flag, g.dev_status)) {
-          tc_fence_after();
+      mbar_arrive(p_full);
+      if (p.lw && entry >= 0) {
+        const int ppt = g.tile / 32;
+        const long long piece = (long long)bh * p.pieces_cap + entry * ppt + (warp & (ppt - 1));
+        float ref[RP];
 #pragma unroll
-          for (int q = 0; q < STEP / 32; ++q)
-            umma_f8_ss(tmem + N, dV + (uint64_t)((st * 2 * Cfg::CB + q * 32 * D) >> 4), dP + (uint64_t)(q * 32 >> 4),
-                       idesc_o, (e > 0 || q > 0) ? 1u : 0u);
-        }
-        umma_commit(free_ + st);
-        if (e + 1 < n_steps) issue_s(e + 1);
+        for (int r = 0; r < RP; ++r) ref[r] = m[r];
+        warp_rows<RP, 16>(x, ref, lane);
+        const int r = lane / (32 / RP);
+        if (lane % (32 / RP) == 0 && r < rows)
+          p.lw[piece * p.rows_cap + r] = x[0] == 0.f ? -INFINITY : __log2f(x[0]) + (ref[0] - OFF - ev);
       }
     }
     if (n_steps > 0)  // the last P V (and with it all before), or after an abort whatever was issued
       ok = mbar_wait(free_ + (n_steps - 1) % ST, ((n_steps - 1) / ST) & 1, abort_flag, g.dev_status) && ok;
-    if (tid == 0 && *abort_flag) {
-      umma_commit(s_full);
-      mbar_wait_drain(s_full, 0, 1000000);
-    }
+    __syncwarp();
     tc_fence_after();
     // row sums over the keys
 #pragma unroll
@@ -368,7 +416,7 @@ __global__ void __launch_bounds__(THREADS, 2)
     softmax_sync();
     uint32_t u[N];
     if (n_steps > 0 && ok) {
-      tmem_load(lane_addr + N, u);
+      tmem_load(lane_addr + 2 * N, u);
     } else {
 #pragma unroll
       for (int k = 0; k < N; ++k) u[k] = 0;
