@@ -391,18 +391,15 @@ class KVCache:
                            *[getattr(self, n).data_ptr() for n in ("k8", "v8", "table", "pos", "k_scale", "v_scale",
                                                                    "weight", "len", "next_pos", "_arrive",
                                                                    "status")])
-
-    @property
-    def ref(self):
-        return ctypes.byref(self._c)
+        self.ref = ctypes.byref(self._c)
 
 
 def _expect(t, name: str, shape, dtype, device, contiguous: bool = True):
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a tensor")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise ValueError(f"{name} must be {dtype}, not {t.dtype}")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
     if device is not None and t.device != device:
         raise ValueError(f"{name} is on {t.device}, not on {device}")
@@ -411,31 +408,44 @@ def _expect(t, name: str, shape, dtype, device, contiguous: bool = True):
 
 
 def _rows(t: torch.Tensor, name: str, shape, cache: KVCache):
-    """Pointer and strides of a [B, n, heads, d] bf16 tensor whose last
-    dimension is contiguous."""
-    _expect(t, name, shape, torch.bfloat16, cache.device, contiguous=False)
-    st = [s if n > 1 else 0 for s, n in zip(t.stride()[:3], t.shape[:3])]
-    if t.numel() and t.stride(3) != 1:
+    """Pointer and strides (None: contiguous) of a [B, n, heads, d] bf16
+    tensor whose last dimension is contiguous."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not torch.bfloat16 or t.shape != shape or t.device != cache.device:
+        _expect(t, name, shape, torch.bfloat16, cache.device, contiguous=False)
+    if t.is_contiguous():
+        return t.data_ptr(), None
+    st = t.stride()
+    if st[3] != 1:
         raise ValueError(f"{name}: the last dimension must be contiguous")
-    return ctypes.c_void_p(t.data_ptr()), (ctypes.c_int64 * 3)(*st)
+    return t.data_ptr(), _Strides(*[s if n > 1 else 0 for s, n in zip(st[:3], shape)])
 
 
-def _kv_call(cache: KVCache, stream, call):
-    """`call(stream pointer)` on the cache's device, on `stream` or that
+_Strides = ctypes.c_int64 * 3
+
+
+def _kv_call(cache: KVCache, stream, fn, *args):
+    """fn(*args, stream pointer) on the cache's device, on `stream` or that
     device's current one."""
+    index = cache.device.index
+    if index is None:
+        raise ValueError("the cache is not on a CUDA device")
     if stream is not None and stream.device != cache.device:
         raise ValueError(f"the stream is on {stream.device}, the cache on {cache.device}")
-    if cache.device.type != "cuda":
-        raise ValueError("the cache is not on a CUDA device")
-    with torch.cuda.device(cache.device):
-        _check(call(_stream(stream)))
+    raw = torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
+    if torch.cuda.current_device() == index:
+        rc = fn(*args, raw)
+    else:
+        with torch.cuda.device(index):
+            rc = fn(*args, raw)
+    if rc != VEDA_OK:
+        _check(rc)
 
 
 def _n_new(cache: KVCache, n_new):
     if n_new is None:
         return None
     _expect(n_new, "n_new", (cache.B,), torch.int32, cache.device)
-    return ctypes.c_void_p(n_new.data_ptr())
+    return n_new.data_ptr()
 
 
 def veda_kv_append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, n_new: Optional[torch.Tensor] = None,
@@ -446,16 +456,15 @@ def veda_kv_append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, n_new: Opti
     if not isinstance(k, torch.Tensor) or k.dim() != 4:
         raise ValueError("k must be a [B, n, heads_kv, d] tensor")
     n = k.shape[1]
-    kp, ks = _rows(k, "k", (cache.B, n, cache.heads_kv, cache.d), cache)
-    vp, vs = _rows(v, "v", (cache.B, n, cache.heads_kv, cache.d), cache)
-    nn = _n_new(cache, n_new)
-    _kv_call(cache, stream, lambda s: _lib.veda_kv_append(cache.ref, kp, ks, vp, vs, n, nn, s))
+    shape = (cache.B, n, cache.heads_kv, cache.d)
+    kp, ks = _rows(k, "k", shape, cache)
+    vp, vs = _rows(v, "v", shape, cache)
+    _kv_call(cache, stream, _lib.veda_kv_append, cache.ref, kp, ks, vp, vs, n, _n_new(cache, n_new))
 
 
 def veda_kv_advance(cache: KVCache, n: int, n_new: Optional[torch.Tensor] = None, stream=None):
     """Take the n (or n_new[b]) pending tokens in."""
-    nn = _n_new(cache, n_new)
-    _kv_call(cache, stream, lambda s: _lib.veda_kv_advance(cache.ref, int(n), nn, s))
+    _kv_call(cache, stream, _lib.veda_kv_advance, cache.ref, int(n), _n_new(cache, n_new))
 
 
 def veda_kv_attn_ws_bytes(cache: KVCache, heads: int, n_q: int, with_weight: bool = False) -> int:
@@ -471,23 +480,24 @@ def veda_kv_attn(cache: KVCache, q: torch.Tensor, o: torch.Tensor, scale: float,
     bytes. weight: [B, heads_kv, nb_cap], e.g. cache.weight."""
     if not isinstance(q, torch.Tensor) or q.dim() != 4:
         raise ValueError("q must be a [B, n_q, heads, d] tensor")
-    n, heads = q.shape[1], q.shape[2]
+    _, n, heads, _ = q.shape
     shape = (cache.B, n, heads, cache.d)
     qp, qs = _rows(q, "q", shape, cache)
     op, os_ = _rows(o, "o", shape, cache)
+    lp = wp = None
     if lse is not None:
         _expect(lse, "lse", (cache.B, heads, n), torch.float32, cache.device)
+        lp = lse.data_ptr()
     if weight is not None:
         _expect(weight, "weight", (cache.B, cache.heads_kv, cache.nb_cap), torch.float32, cache.device)
-    need = veda_kv_attn_ws_bytes(cache, heads, n, weight is not None)
+        wp = weight.data_ptr()
+    need = _lib.veda_kv_attn_ws_bytes(cache.ref, heads, n, wp is not None)
     if not isinstance(ws, torch.Tensor) or ws.device != cache.device or not ws.is_contiguous():
         raise ValueError("ws must be a contiguous tensor on the cache's device")
     if ws.numel() * ws.element_size() < need:
         raise ValueError(f"ws holds {ws.numel() * ws.element_size()} bytes, {need} are needed")
-    nn = _n_new(cache, n_new)
-    _kv_call(cache, stream, lambda s: _lib.veda_kv_attn(
-        cache.ref, qp, qs, heads, n, nn, int(pending), int(causal), int(window), int(sinks), float(scale), op, os_,
-        _ptr(lse), _ptr(weight), float(decay), _ptr(ws), s))
+    _kv_call(cache, stream, _lib.veda_kv_attn, cache.ref, qp, qs, heads, n, _n_new(cache, n_new), bool(pending),
+             bool(causal), int(window), int(sinks), float(scale), op, os_, lp, wp, float(decay), ws.data_ptr())
 
 
 def veda_kv_evict(cache: KVCache, keep: Sequence[int], sink: int, recent: int, out: Optional[KVCache] = None,
@@ -498,12 +508,12 @@ def veda_kv_evict(cache: KVCache, keep: Sequence[int], sink: int, recent: int, o
         raise ValueError(f"keep must have {cache.heads_kv} entries, not {len(keep)}")
     if out is not None and out.device != cache.device:
         raise ValueError(f"out is on {out.device}, the cache on {cache.device}")
-    _kv_call(cache, stream, lambda s: _lib.veda_kv_evict(cache.ref, _host_i32(keep), int(sink), int(recent),
-                                                         None if out is None else out.ref, s))
+    _kv_call(cache, stream, _lib.veda_kv_evict, cache.ref, (ctypes.c_int32 * len(keep))(*keep), int(sink), int(recent),
+             None if out is None else out.ref)
 
 
 def veda_kv_check_status(cache: KVCache, stream=None):
-    _kv_call(cache, stream, lambda s: _lib.veda_kv_check_status(cache.ref, s))
+    _kv_call(cache, stream, _lib.veda_kv_check_status, cache.ref)
 
 
 def library_path() -> str:
