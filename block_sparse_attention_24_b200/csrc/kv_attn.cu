@@ -52,7 +52,7 @@ struct RowsCfg {
   static constexpr int OFF_P = OFF_Q + N * D;
   static constexpr int OFF_META = OFF_P + 2 * N * STEP;
   static constexpr int OFF_BAR = OFF_META + ST * (int)sizeof(StepMeta);
-  static constexpr int NUM_BARS = 3 * ST + 4;                   // K, V, free per stage; S twice; P; drain
+  static constexpr int NUM_BARS = 3 * ST + 5;                   // K, V, free per stage; S, P twice; drain
   static constexpr int OFF_RED = OFF_BAR + NUM_BARS * 8;        // float [4][RP], then [RP] factors, int [2][RP] position bounds
   static constexpr int OFF_MISC = OFF_RED + 7 * RP * 4;
   static constexpr int ALLOC = OFF_MISC + 32 + 1024;
@@ -151,8 +151,10 @@ __global__ void __launch_bounds__(THREADS, 2)
   uint64_t* v_full = k_full + ST;
   uint64_t* free_ = v_full + ST;  // P V of the stage's step has completed
   uint64_t* s_full = free_ + ST;  // [2]
-  uint64_t* p_full = s_full + 2;  // 128 arrivals
-  uint64_t* drain = p_full + 1;
+  // [2], 128 arrivals each: with one, the softmax of the next step, whose S is
+  // there already, could complete the phase after before this one is seen
+  uint64_t* p_full = s_full + 2;
+  uint64_t* drain = p_full + 2;
   StepMeta* meta = reinterpret_cast<StepMeta*>(smem + Cfg::OFF_META);
   float* red = reinterpret_cast<float*>(smem + Cfg::OFF_RED);
   float* qs = red + 4 * RP;
@@ -161,56 +163,87 @@ __global__ void __launch_bounds__(THREADS, 2)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Cfg::OFF_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Cfg::OFF_MISC + 4);
   int* cnt = reinterpret_cast<int*>(smem + Cfg::OFF_MISC + 8);  // [3], then a flag
-  if (tid < Cfg::NUM_BARS) mbar_init(k_full + tid, k_full + tid == p_full ? 128 : 1);
-  if (tid < 4) cnt[tid] = 0;
-  if (tid == 0) *abort_flag = 0;
-  fence_mbar_init();
-  if (warp == 4) {
-    if (lane == 0) {
-      tma_prefetch_desc(&maps.k);
-      tma_prefetch_desc(&maps.v);
-    }
-    __syncwarp();
-    tmem_alloc(tmem_slot, Cfg::TMEM);
-    tmem_relinquish();
+  if (p.window > 0) {
+    if (tid < 3) cnt[tid] = 0;
+    __syncthreads();
   }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
-
   const int nb = (total + g.tile - 1) / g.tile;
   const KvRange rg = kv_range(g, p, trow, nb, t_lo, t_hi, t_hi, cnt, tid, THREADS);
   const int per_step = STEP / g.tile;
   const int steps_all = (rg.count() + per_step - 1) / per_step;
   const int per = max(1, (steps_all + p.splits - 1) / p.splits);
   const int parts = max(1, (steps_all + per - 1) / per);  // CTAs that have steps (one, if there are none)
+  if (sp >= parts) return;
   const int s_lo = sp * per, n_steps = max(0, min(per, steps_all - s_lo));
 
-  if (sp < parts) {
+  // Each warp prepares its part before the one barrier: the first copies are
+  // under way while Q is converted.
+  StepFeed feed;
+  int fed = 0;  // steps whose copies were issued (warp 4)
+  auto produce = [&](int e) {
+    if ((e & 15) == 0) feed.load(g, trow, rg, total, s_lo, e, n_steps, lane);
+    const int st = e % ST;
+    int row0, row1;
+    feed.put(meta[st], g, p, e, t_lo, t_hi, lane, row0, row1);
+    __syncwarp();
+    if (lane == 0) {
+      const uint32_t bytes = (row0 >= 0 ? Cfg::CB / 2 : 0) + (row1 >= 0 ? Cfg::CB / 2 : 0);
+      uint8_t* kd = smem + st * 2 * Cfg::CB;
+      uint8_t* vd = kd + Cfg::CB;
+      mbar_expect_tx(k_full + st, bytes);
+      if (row0 >= 0) tma_load_2d(kd, &maps.k, k_full + st, 0, row0);
+      if (row1 >= 0) tma_load_2d(kd + Cfg::CB / 2, &maps.k, k_full + st, 0, row1);
+      mbar_expect_tx(v_full + st, bytes);
+      if (row0 >= 0) tma_load_2d(vd, &maps.v, v_full + st, 0, row0);
+      if (row1 >= 0) tma_load_2d(vd + Cfg::CB / 2, &maps.v, v_full + st, 0, row1);
+    }
+    __syncwarp();
+  };
+  if (warp == 4) {
+    if (lane < Cfg::NUM_BARS) mbar_init(k_full + lane, k_full + lane == p_full || k_full + lane == p_full + 1 ? 128 : 1);
+    if (lane == 0) *abort_flag = 0;
+    fence_mbar_init();
+    __syncwarp();
+    for (; fed < ST && fed < n_steps; ++fed) produce(fed);
+  } else if (warp == 5) {
+    tmem_alloc(tmem_slot, Cfg::TMEM);
+    tmem_relinquish();
+  } else {
+    uint32_t top = 0;
+#pragma unroll
+    for (int x = 0; x < EL / 2; ++x) top = max(top, bf16x2_top(qw[x]));
+#pragma unroll
+    for (int d = 1; d < TPR; d <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
+    float mul, inv;
+    q_scale<7>(top, mul, inv);
+    if (tid % TPR == 0) {
+      qs[qr] = inv * p.scale_log2;
+      const int t = t_lo + min(qr, rows - 1) / p.group;
+      seen_hi[qr] = p.causal ? t : INT_MAX;
+      seen_lo[qr] = p.window > 0 ? (int)max((long long)INT_MIN, (long long)t - p.window) : INT_MIN;
+    }
+#pragma unroll
+    for (int x = 0; x < EL / 2; ++x) {
+      uint16_t c[4];
+      four_parts(__uint_as_float(qw[x] << 16) * mul, __uint_as_float(qw[x] & 0xffff0000u) * mul, c);
+      const int d = qd + 2 * x;
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        *reinterpret_cast<uint16_t*>(smem + Cfg::OFF_Q + code_at<D>(k * RP + qr, d >> 4) + (d & 15)) = c[k];
+    }
+    fence_proxy_async_smem();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
   if (warp == 4) {
     // ------------------------------------------------------------- producer
-    StepFeed feed;
-    int e = 0;
+    int e = fed;
     for (; e < n_steps; ++e) {
-      if ((e & 15) == 0) feed.load(g, trow, rg, total, s_lo, e, n_steps, lane);
-      const int st = e % ST;
-      if (!__all_sync(0xffffffffu, e < ST || mbar_wait(free_ + st, (e / ST - 1) & 1, abort_flag, g.dev_status))) break;
-      int row0, row1;
-      feed.put(meta[st], g, p, e, t_lo, t_hi, lane, row0, row1);
-      __syncwarp();
-      if (lane == 0) {
-        const uint32_t bytes = (row0 >= 0 ? Cfg::CB / 2 : 0) + (row1 >= 0 ? Cfg::CB / 2 : 0);
-        uint8_t* kd = smem + st * 2 * Cfg::CB;
-        uint8_t* vd = kd + Cfg::CB;
-        mbar_expect_tx(k_full + st, bytes);
-        if (row0 >= 0) tma_load_2d(kd, &maps.k, k_full + st, 0, row0);
-        if (row1 >= 0) tma_load_2d(kd + Cfg::CB / 2, &maps.k, k_full + st, 0, row1);
-        mbar_expect_tx(v_full + st, bytes);
-        if (row0 >= 0) tma_load_2d(vd, &maps.v, v_full + st, 0, row0);
-        if (row1 >= 0) tma_load_2d(vd + Cfg::CB / 2, &maps.v, v_full + st, 0, row1);
-      }
-      __syncwarp();
+      if (!__all_sync(0xffffffffu, mbar_wait(free_ + e % ST, (e / ST - 1) & 1, abort_flag, g.dev_status))) break;
+      produce(e);
     }
     if (*abort_flag && lane == 0)  // let every copy that was started land
       for (int x = max(0, e - ST); x < e; ++x) {
@@ -233,19 +266,18 @@ __global__ void __launch_bounds__(THREADS, 2)
         umma_commit(s_full + (e & 1));
       };
       auto k_here = [&](int e) { return mbar_wait(k_full + e % ST, (e / ST) & 1, abort_flag, g.dev_status); };
-      // phase 0 of p_full: Q is in shared memory; phase e + 1: P of step e
-      bool ok = mbar_wait(p_full, 0, abort_flag, g.dev_status) && k_here(0);
+      bool ok = k_here(0);
       if (ok) issue_s(0);
       for (int e = 0; ok && e < n_steps; ++e) {
         const int st = e % ST;
         bool ahead = e + 1 == n_steps;  // S of the next step is issued
         // whichever comes first: the next K, or this P
-        for (int spin = 0; spin < 4096 && !mbar_test(p_full, (e + 1) & 1); ++spin)
+        for (int spin = 0; spin < 4096 && !mbar_test(p_full + (e & 1), (e >> 1) & 1); ++spin)
           if (!ahead && mbar_test(k_full + (e + 1) % ST, ((e + 1) / ST) & 1)) {
             issue_s(e + 1);
             ahead = true;
           }
-        ok = mbar_wait(p_full, (e + 1) & 1, abort_flag, g.dev_status) &&
+        ok = mbar_wait(p_full + (e & 1), (e >> 1) & 1, abort_flag, g.dev_status) &&
              mbar_wait(v_full + st, (e / ST) & 1, abort_flag, g.dev_status);
         if (!ok) break;
         tc_fence_after();
@@ -263,34 +295,7 @@ __global__ void __launch_bounds__(THREADS, 2)
       mbar_wait_drain(drain, 0, VEDA_WAIT_LIMIT_NS);
     }
   } else {
-    // ----------------------------------------------------- Q in its parts
-    {
-      uint32_t top = 0;
-#pragma unroll
-      for (int x = 0; x < EL / 2; ++x) top = max(top, bf16x2_top(qw[x]));
-#pragma unroll
-      for (int d = 1; d < TPR; d <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
-      float mul, inv;
-      q_scale<7>(top, mul, inv);
-      if (tid % TPR == 0) {
-        qs[qr] = inv * p.scale_log2;
-        const int t = t_lo + min(qr, rows - 1) / p.group;
-        seen_hi[qr] = p.causal ? t : INT_MAX;
-        seen_lo[qr] = p.window > 0 ? (int)max((long long)INT_MIN, (long long)t - p.window) : INT_MIN;
-      }
-#pragma unroll
-      for (int x = 0; x < EL / 2; ++x) {
-        uint16_t c[4];
-        four_parts(__uint_as_float(qw[x] << 16) * mul, __uint_as_float(qw[x] & 0xffff0000u) * mul, c);
-        const int d = qd + 2 * x;
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-          *reinterpret_cast<uint16_t*>(smem + Cfg::OFF_Q + code_at<D>(k * RP + qr, d >> 4) + (d & 15)) = c[k];
-      }
-      fence_proxy_async_smem();
-      mbar_arrive(p_full);
-      softmax_sync();
-    }
+    // ------------------------------------------------------------- softmax
     const uint32_t lane_addr = tmem + ((uint32_t)(warp * 32) << 16);
     const int half = tid >> 6, kk = tid & 63;  // this thread's key
     float m[RP], l[RP];
@@ -388,7 +393,7 @@ __global__ void __launch_bounds__(THREADS, 2)
       }
       fence_proxy_async_smem();
       tc_fence_before();
-      mbar_arrive(p_full);
+      mbar_arrive(p_full + (e & 1));
       if (p.lw && entry >= 0) {
         const int ppt = g.tile / 32;
         const long long piece = (long long)bh * p.pieces_cap + entry * ppt + (warp & (ppt - 1));
@@ -436,17 +441,16 @@ __global__ void __launch_bounds__(THREADS, 2)
         if (r < rows && tid < D) p.part_o[(row0 + r) * D + tid] = o[r];
         if (r < rows && tid == r) p.part_ml[row0 + r] = make_float2(m[r], l[r]);
       }
-      __threadfence();
       softmax_sync();
-      if (tid == 0) {
-        const int before = atomicAdd(p.arrive + bh, 1);
+      if (tid == 0) {  // releases the block's writes, acquires those of the blocks before
+        int before;
+        asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], 1;" : "=r"(before) : "l"(p.arrive + bh) : "memory");
         cnt[3] = before == parts - 1;
         if (before == parts - 1) p.arrive[bh] = 0;
       }
       softmax_sync();
       last = cnt[3] != 0;
       if (last) {
-        __threadfence();
         // a warp per row: its parts' factors, then each thread its channel
         const float2* ml = p.part_ml + (long long)bh * p.splits * p.rows_pad;
         const float* po = p.part_o + (long long)bh * p.splits * p.rows_pad * D + tid;
@@ -529,9 +533,8 @@ __global__ void __launch_bounds__(THREADS, 2)
     }
     tc_fence_before();
   }
-  }
   __syncthreads();
-  if (warp == 4) {
+  if (warp == 5) {
     tc_fence_after();
     tmem_dealloc(tmem, Cfg::TMEM);
   }
