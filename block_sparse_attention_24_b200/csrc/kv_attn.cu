@@ -30,22 +30,25 @@ namespace {
 //   O^T = V^T P   A = the V tile taken along its rows (d x 128 keys; for d = 64
 //                 the upper half of M repeats the lower), B = P^T, in four
 //                 parts too: 16 bits, down to 2^-29 of the row's largest.
-// A thread owns a key (TMEM lane) of S^T and a channel of O^T; the rows are
-// columns, so the work per key goes with the rows there are. S and P are
+// A thread owns a key (TMEM lane) of S^T and a channel of O^T, for four or
+// eight rows; the rows are columns, so the work per key goes with the rows there
+// are, and from five rows on two warpgroups share it. S and P are
 // double-buffered: a step's S is issued as soon as its K has arrived, beside
 // the softmax of the step before.
-//   warps 0-3  softmax
-//   warp 4     producer: table, scales, TMA
-//   warp 5     MMA issuer (one thread; issuing blocks it, so it is no softmax thread)
+//   warps 0-3 (0-7)  softmax
+//   then one warp    producer: table, scales, TMA
+//   and one          MMA issuer (one thread; issuing blocks it, so it is no
+//                    softmax thread)
 // The CTAs that share a head's keys count themselves in `arrive`; the last one
 // joins their parts, and sums the tile weights.
 constexpr int FEW_ROWS = 16;
-constexpr int THREADS = 192;
 constexpr float MARGIN = 1.5f;  // P <= 2^(OFF + MARGIN) = 362 < 448
 
 template <int D, int RP>
 struct RowsCfg {
   static constexpr int N = 4 * RP;
+  static constexpr int G = RP == 4 ? 1 : 2, R = RP / G;         // softmax warpgroups, rows of a thread
+  static constexpr int SM = 128 * G, THREADS = SM + 64;
   static constexpr int CB = STEP * D;                           // bytes of a step's K or V codes
   static constexpr int ST = D == 64 ? (RP == 16 ? 5 : 6) : (RP == 16 ? 2 : 3);  // ring stages: two CTAs per SM
   static constexpr int OFF_Q = ST * 2 * CB;
@@ -60,25 +63,27 @@ struct RowsCfg {
   static_assert(2 * (ALLOC + 1024) <= 233472, "two CTAs per SM");
 };
 
-__device__ __forceinline__ void softmax_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+template <int SM>
+__device__ __forceinline__ void softmax_sync() {
+  asm volatile("bar.sync 1, %0;" ::"n"(SM) : "memory");
+}
+template <int SM>
 __device__ __forceinline__ bool softmax_any(bool x) {
   int r;
-  asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %1, 0;\n\tbar.red.or.pred q, 1, 128, p;\n\tselp.b32 %0, 1, 0, q;\n\t}"
-               : "=r"(r) : "r"((int)x) : "memory");
+  asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %1, 0;\n\tbar.red.or.pred q, 1, %2, p;\n\tselp.b32 %0, 1, 0, q;\n\t}"
+               : "=r"(r) : "r"((int)x), "n"(SM) : "memory");
   return r != 0;
 }
 
 template <int N>
 __device__ __forceinline__ void tmem_load(uint32_t addr, uint32_t (&u)[N]) {
   if constexpr (N == 16) tmem_ld16(addr, u);
-  else if constexpr (N == 32) tmem_ld32(addr, u);
-  else tmem_ld64(addr, u);
+  else tmem_ld32(addr, u);
 }
 template <int N>
 __device__ __forceinline__ void tmem_store(uint32_t addr, const uint32_t (&u)[N]) {
   if constexpr (N == 16) tmem_st16(addr, u);
-  else if constexpr (N == 32) tmem_st32(addr, u);
-  else tmem_st64(addr, u);
+  else tmem_st32(addr, u);
 }
 
 // Sums of every row's value over the warp, the rows halved between the lanes
@@ -118,10 +123,13 @@ __device__ __forceinline__ void four_parts(float x, float y, uint16_t (&c)[4]) {
 }
 
 template <int D, int RP>
-__global__ void __launch_bounds__(THREADS, 2)
+__global__ void __launch_bounds__((RowsCfg<D, RP>::THREADS), 2)
     kv_attn_rows_kernel(const KvGeom g, const KvAttnParams p, const __grid_constant__ KvMaps maps) {
   using Cfg = RowsCfg<D, RP>;
-  constexpr int N = Cfg::N, ST = Cfg::ST;
+  constexpr int N = Cfg::N, ST = Cfg::ST, R = Cfg::R, SM = Cfg::SM, THREADS = Cfg::THREADS;
+  constexpr int PRODUCER = SM / 32, ISSUER = PRODUCER + 1;  // warps
+  // column of part k of a row: a warpgroup's rows are side by side
+  auto column = [](int k, int r) { return r / R * (4 * R) + k * R + r % R; };
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + (((smem_u32(smem_raw) + 1023u) & ~1023u) - smem_u32(smem_raw));
   const int sp = blockIdx.x, h = blockIdx.y, b = blockIdx.z;
@@ -134,13 +142,13 @@ __global__ void __launch_bounds__(THREADS, 2)
   const int bh = b * g.hkv + h;
   const long long trow = (long long)bh * g.nb_cap;
   const int t_hi = t_lo + n_b - 1;
-  // Q: 128 / RP threads per row
-  constexpr int TPR = 128 / RP, EL = D / TPR;
+  // Q: TPR threads per row
+  constexpr int TPR = SM / RP, EL = D / TPR;
   const int qr = tid / TPR, qd = tid % TPR * EL;
   uint32_t qw[EL / 2];
 #pragma unroll
   for (int x = 0; x < EL / 2; ++x) qw[x] = 0;
-  if (qr < rows && warp < 4) {
+  if (qr < rows && warp < PRODUCER) {
     const uint32_t* src = reinterpret_cast<const uint32_t*>(p.q.p + b * p.q.sb + (long long)(qr / p.group) * p.q.sn +
                                                             (long long)(h * p.group + qr % p.group) * p.q.sh + qd);
 #pragma unroll
@@ -151,7 +159,7 @@ __global__ void __launch_bounds__(THREADS, 2)
   uint64_t* v_full = k_full + ST;
   uint64_t* free_ = v_full + ST;  // P V of the stage's step has completed
   uint64_t* s_full = free_ + ST;  // [2]
-  // [2], 128 arrivals each: with one, the softmax of the next step, whose S is
+  // [2], an arrival per softmax thread each: with one, the softmax of the next step, whose S is
   // there already, could complete the phase after before this one is seen
   uint64_t* p_full = s_full + 2;
   uint64_t* drain = p_full + 2;
@@ -179,7 +187,7 @@ __global__ void __launch_bounds__(THREADS, 2)
   // Each warp prepares its part before the one barrier: the first copies are
   // under way while Q is converted.
   StepFeed feed;
-  int fed = 0;  // steps whose copies were issued (warp 4)
+  int fed = 0;  // steps whose copies were issued (the producer's)
   auto produce = [&](int e) {
     if ((e & 15) == 0) feed.load(g, trow, rg, total, s_lo, e, n_steps, lane);
     const int st = e % ST;
@@ -199,13 +207,13 @@ __global__ void __launch_bounds__(THREADS, 2)
     }
     __syncwarp();
   };
-  if (warp == 4) {
-    if (lane < Cfg::NUM_BARS) mbar_init(k_full + lane, k_full + lane == p_full || k_full + lane == p_full + 1 ? 128 : 1);
+  if (warp == PRODUCER) {
+    if (lane < Cfg::NUM_BARS) mbar_init(k_full + lane, k_full + lane == p_full || k_full + lane == p_full + 1 ? SM : 1);
     if (lane == 0) *abort_flag = 0;
     fence_mbar_init();
     __syncwarp();
     for (; fed < ST && fed < n_steps; ++fed) produce(fed);
-  } else if (warp == 5) {
+  } else if (warp == ISSUER) {
     tmem_alloc(tmem_slot, Cfg::TMEM);
     tmem_relinquish();
   } else {
@@ -229,7 +237,7 @@ __global__ void __launch_bounds__(THREADS, 2)
       const int d = qd + 2 * x;
 #pragma unroll
       for (int k = 0; k < 4; ++k)
-        *reinterpret_cast<uint16_t*>(smem + Cfg::OFF_Q + code_at<D>(k * RP + qr, d >> 4) + (d & 15)) = c[k];
+        *reinterpret_cast<uint16_t*>(smem + Cfg::OFF_Q + code_at<D>(column(k, qr), d >> 4) + (d & 15)) = c[k];
     }
     fence_proxy_async_smem();
   }
@@ -238,7 +246,7 @@ __global__ void __launch_bounds__(THREADS, 2)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
-  if (warp == 4) {
+  if (warp == PRODUCER) {
     // ------------------------------------------------------------- producer
     int e = fed;
     for (; e < n_steps; ++e) {
@@ -250,7 +258,7 @@ __global__ void __launch_bounds__(THREADS, 2)
         mbar_wait_drain(k_full + x % ST, (x / ST) & 1, VEDA_WAIT_LIMIT_NS);
         mbar_wait_drain(v_full + x % ST, (x / ST) & 1, VEDA_WAIT_LIMIT_NS);
       }
-  } else if (warp == 5) {
+  } else if (warp == ISSUER) {
     // ----------------------------------------------------------- MMA issuer
     if (lane == 0 && n_steps > 0) {
       constexpr uint32_t idesc_s = idesc_fmt0(128, N, false, false), idesc_o = idesc_fmt0(128, N, true, false);
@@ -296,11 +304,11 @@ __global__ void __launch_bounds__(THREADS, 2)
     }
   } else {
     // ------------------------------------------------------------- softmax
-    const uint32_t lane_addr = tmem + ((uint32_t)(warp * 32) << 16);
-    const int half = tid >> 6, kk = tid & 63;  // this thread's key
-    float m[RP], l[RP];
+    const int wq = warp % 4, r0 = warp / 4 * R, key = tid & 127, half = key >> 6, kk = key & 63;
+    const uint32_t lane_addr = tmem + ((uint32_t)(wq * 32) << 16) + 4 * r0;  // this thread's lane and columns
+    float m[R], l[R];
 #pragma unroll
-    for (int r = 0; r < RP; ++r) {
+    for (int r = 0; r < R; ++r) {
       m[r] = -INFINITY;
       l[r] = 0.f;
     }
@@ -311,38 +319,39 @@ __global__ void __launch_bounds__(THREADS, 2)
       ok = mbar_wait(s_full + (e & 1), (e >> 1) & 1, abort_flag, g.dev_status);
       tc_fence_after();
       const StepMeta& sm = meta[st];
-      uint32_t u[N];
+      uint32_t u[4 * R];
       tmem_load(lane_addr + (e & 1) * N, u);
       const float sk = sm.ks[half], ev = sm.ev[half];
       const int left = sm.left[half], pos = sm.pos[half] + kk;
       const bool full = sm.full, first = pos < p.sinks || p.window <= 0;
-      float x[RP];
+      float x[R];
       bool over = !ok;
 #pragma unroll
-      for (int r = 0; r < RP; ++r) {
-        const float s = fmaf(fmaf(fmaf(__uint_as_float(u[3 * RP + r]), 0.0625f, __uint_as_float(u[2 * RP + r])), 0.0625f,
-                                  __uint_as_float(u[RP + r])), 0.0625f, __uint_as_float(u[r]));
-        x[r] = fmaf(s, qs[r] * sk, ev);
-        if (!full && !((pos <= seen_hi[r]) & ((pos > seen_lo[r]) | first) & (kk < left))) x[r] = -INFINITY;
+      for (int r = 0; r < R; ++r) {
+        const float s = fmaf(fmaf(fmaf(__uint_as_float(u[3 * R + r]), 0.0625f, __uint_as_float(u[2 * R + r])), 0.0625f,
+                                  __uint_as_float(u[R + r])), 0.0625f, __uint_as_float(u[r]));
+        x[r] = fmaf(s, qs[r0 + r] * sk, ev);
+        if (!full && !((pos <= seen_hi[r0 + r]) & ((pos > seen_lo[r0 + r]) | first) & (kk < left))) x[r] = -INFINITY;
         over |= x[r] > m[r] + MARGIN;
       }
-      if (softmax_any(over)) {
+      if (softmax_any<SM>(over)) {
         if (*abort_flag) {
           ok = false;
           break;
         }
         // new references: the largest x so far, as integers that rank alike
 #pragma unroll
-        for (int r = 0; r < RP; ++r) {
+        for (int r = 0; r < R; ++r) {
           const int i = __float_as_int(x[r] == x[r] ? x[r] : -INFINITY);
           const int v = __reduce_max_sync(0xffffffffu, i ^ ((i >> 31) & 0x7fffffff));
-          if (lane == r) red[warp * RP + r] = __int_as_float(v ^ ((v >> 31) & 0x7fffffff));
+          if (lane == r) red[wq * RP + r0 + r] = __int_as_float(v ^ ((v >> 31) & 0x7fffffff));
         }
-        softmax_sync();
-        float al[RP];
+        softmax_sync<SM>();
+        float al[R];
 #pragma unroll
-        for (int r = 0; r < RP; ++r) {
-          const float mx = fmaxf(fmaxf(red[r], red[RP + r]), fmaxf(red[2 * RP + r], red[3 * RP + r]));
+        for (int r = 0; r < R; ++r) {
+          const float* v = red + r0 + r;
+          const float mx = fmaxf(fmaxf(v[0], v[RP]), fmaxf(v[2 * RP], v[3 * RP]));
           const float mn = fmaxf(m[r], mx);
           al[r] = mn == m[r] ? 1.f : fast_exp2(m[r] - mn);
           m[r] = mn;
@@ -352,16 +361,16 @@ __global__ void __launch_bounds__(THREADS, 2)
           mbar_wait(free_ + (e - 1) % ST, ((e - 1) / ST) & 1, abort_flag, g.dev_status);
           __syncwarp();
           tc_fence_after();
-          uint32_t o[N];
+          uint32_t o[4 * R];
           tmem_load(lane_addr + 2 * N, o);
 #pragma unroll
-          for (int k = 0; k < N; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * al[k % RP]);
+          for (int k = 0; k < 4 * R; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * al[k % R]);
           tmem_store(lane_addr + 2 * N, o);
         }
       }
       const float rv = sm.rv[half];
 #pragma unroll
-      for (int r = 0; r < RP; r += 2) {
+      for (int r = 0; r < R; r += 2) {
         const float p0 = fast_exp2(x[r] + (OFF - (m[r] == -INFINITY ? 0.f : m[r])));
         const float p1 = fast_exp2(x[r + 1] + (OFF - (m[r + 1] == -INFINITY ? 0.f : m[r + 1])));
         x[r] = p0;
@@ -373,10 +382,10 @@ __global__ void __launch_bounds__(THREADS, 2)
         four_parts(p0, p1, c);
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          const int n = k * RP + r;
-          uint8_t* dst = smem + Cfg::OFF_P + (e & 1) * N * STEP + (tid & 15);
-          dst[n * 128 + (((tid >> 4) ^ (n & 7)) << 4)] = (uint8_t)c[k];
-          dst[(n + 1) * 128 + (((tid >> 4) ^ ((n + 1) & 7)) << 4)] = (uint8_t)(c[k] >> 8);
+          const int n = 4 * r0 + k * R + r;
+          uint8_t* dst = smem + Cfg::OFF_P + (e & 1) * N * STEP + (key & 15);
+          dst[n * 128 + (((key >> 4) ^ (n & 7)) << 4)] = (uint8_t)c[k];
+          dst[(n + 1) * 128 + (((key >> 4) ^ ((n + 1) & 7)) << 4)] = (uint8_t)(c[k] >> 8);
         }
       }
       const int entry = sm.entry[half];
@@ -384,8 +393,8 @@ __global__ void __launch_bounds__(THREADS, 2)
         // V rows behind the last token become zeroes: their codes may be anything
         if (sm.left[0] + sm.left[1] < STEP) {
           mbar_wait(v_full + st, (e / ST) & 1, abort_flag, g.dev_status);
-          if (kk >= left) {
-            uint4* v = reinterpret_cast<uint4*>(smem + (st * 2 + 1) * Cfg::CB + tid * D);
+          if (kk >= left && r0 == 0) {
+            uint4* v = reinterpret_cast<uint4*>(smem + (st * 2 + 1) * Cfg::CB + key * D);
 #pragma unroll
             for (int c = 0; c < D / 16; ++c) v[c] = make_uint4(0, 0, 0, 0);
           }
@@ -396,13 +405,13 @@ __global__ void __launch_bounds__(THREADS, 2)
       mbar_arrive(p_full + (e & 1));
       if (p.lw && entry >= 0) {
         const int ppt = g.tile / 32;
-        const long long piece = (long long)bh * p.pieces_cap + entry * ppt + (warp & (ppt - 1));
-        float ref[RP];
+        const long long piece = (long long)bh * p.pieces_cap + entry * ppt + (wq & (ppt - 1));
+        float ref[R];
 #pragma unroll
-        for (int r = 0; r < RP; ++r) ref[r] = m[r];
-        warp_rows<RP, 16>(x, ref, lane);
-        const int r = lane / (32 / RP);
-        if (lane % (32 / RP) == 0 && r < rows)
+        for (int r = 0; r < R; ++r) ref[r] = m[r];
+        warp_rows<R, 16>(x, ref, lane);
+        const int r = r0 + lane / (32 / R);
+        if (lane % (32 / R) == 0 && r < rows)
           p.lw[piece * p.rows_cap + r] = x[0] == 0.f ? -INFINITY : __log2f(x[0]) + (ref[0] - OFF - ev);
       }
     }
@@ -412,50 +421,51 @@ __global__ void __launch_bounds__(THREADS, 2)
     tc_fence_after();
     // row sums over the keys
 #pragma unroll
-    for (int r = 0; r < RP; ++r) {
+    for (int r = 0; r < R; ++r) {
       float v = l[r];
 #pragma unroll
       for (int d = 16; d; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
-      if (lane == r) red[warp * RP + r] = v;
+      if (lane == r) red[wq * RP + r0 + r] = v;
     }
-    softmax_sync();
-    uint32_t u[N];
+    softmax_sync<SM>();
+    uint32_t u[4 * R];
     if (n_steps > 0 && ok) {
       tmem_load(lane_addr + 2 * N, u);
     } else {
 #pragma unroll
-      for (int k = 0; k < N; ++k) u[k] = 0;
+      for (int k = 0; k < 4 * R; ++k) u[k] = 0;
     }
-    float o[RP];  // this thread's channel of every row
+    float o[R];  // this thread's channel of its rows
 #pragma unroll
-    for (int r = 0; r < RP; ++r) {
-      l[r] = red[r] + red[RP + r] + red[2 * RP + r] + red[3 * RP + r];
-      o[r] = fmaf(fmaf(fmaf(__uint_as_float(u[3 * RP + r]), 0.0625f, __uint_as_float(u[2 * RP + r])), 0.0625f,
-                       __uint_as_float(u[RP + r])), 0.0625f, __uint_as_float(u[r]));
+    for (int r = 0; r < R; ++r) {
+      const float* v = red + r0 + r;
+      l[r] = v[0] + v[RP] + v[2 * RP] + v[3 * RP];
+      o[r] = fmaf(fmaf(fmaf(__uint_as_float(u[3 * R + r]), 0.0625f, __uint_as_float(u[2 * R + r])), 0.0625f,
+                       __uint_as_float(u[R + r])), 0.0625f, __uint_as_float(u[r]));
     }
     bool last = true;
     if (parts > 1) {
-      const long long row0 = ((long long)bh * p.splits + sp) * p.rows_pad;
+      const long long row0 = ((long long)bh * p.splits + sp) * p.rows_pad + r0;
 #pragma unroll
-      for (int r = 0; r < RP; ++r) {
-        if (r < rows && tid < D) p.part_o[(row0 + r) * D + tid] = o[r];
-        if (r < rows && tid == r) p.part_ml[row0 + r] = make_float2(m[r], l[r]);
+      for (int r = 0; r < R; ++r) {
+        if (r0 + r < rows && key < D) p.part_o[(row0 + r) * D + key] = o[r];
+        if (r0 + r < rows && key == r) p.part_ml[row0 + r] = make_float2(m[r], l[r]);
       }
-      softmax_sync();
+      softmax_sync<SM>();
       if (tid == 0) {  // releases the block's writes, acquires those of the blocks before
         int before;
         asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], 1;" : "=r"(before) : "l"(p.arrive + bh) : "memory");
         cnt[3] = before == parts - 1;
         if (before == parts - 1) p.arrive[bh] = 0;
       }
-      softmax_sync();
+      softmax_sync<SM>();
       last = cnt[3] != 0;
       if (last) {
         // a warp per row: its parts' factors, then each thread its channel
         const float2* ml = p.part_ml + (long long)bh * p.splits * p.rows_pad;
-        const float* po = p.part_o + (long long)bh * p.splits * p.rows_pad * D + tid;
+        const float* po = p.part_o + ((long long)bh * p.splits * p.rows_pad + r0) * D + key;
         float* fac = reinterpret_cast<float*>(smem);  // [parts][RP], in the ring
-        for (int r = warp; r < rows; r += 4) {
+        for (int r = warp; r < rows; r += SM / 32) {
           float mx = -INFINITY, ls = 0.f;
           for (int s = lane; s < parts; s += 32) mx = fmaxf(mx, __ldcg(&ml[(long long)s * p.rows_pad + r].x));
 #pragma unroll
@@ -473,43 +483,44 @@ __global__ void __launch_bounds__(THREADS, 2)
             red[RP + r] = ls;
           }
         }
-        softmax_sync();
+        softmax_sync<SM>();
 #pragma unroll
-        for (int r = 0; r < RP; ++r) {
-          m[r] = red[r];
-          l[r] = red[RP + r];
+        for (int r = 0; r < R; ++r) {
+          m[r] = red[r0 + r];
+          l[r] = red[RP + r0 + r];
           o[r] = 0.f;
         }
-        if (tid < D)
+        if (key < D)
           for (int s = 0; s < parts; ++s) {
-            float v[RP];
+            float v[R];
 #pragma unroll
-            for (int r = 0; r < RP; ++r) v[r] = r < rows ? __ldcg(po + ((long long)s * p.rows_pad + r) * D) : 0.f;
+            for (int r = 0; r < R; ++r) v[r] = r0 + r < rows ? __ldcg(po + ((long long)s * p.rows_pad + r) * D) : 0.f;
 #pragma unroll
-            for (int r = 0; r < RP; ++r) o[r] = fmaf(v[r], r < rows ? fac[s * RP + r] : 0.f, o[r]);
+            for (int r = 0; r < R; ++r) o[r] = fmaf(v[r], r0 + r < rows ? fac[s * RP + r0 + r] : 0.f, o[r]);
           }
       }
     }
     if (last) {
 #pragma unroll
-      for (int r = 0; r < RP; ++r) {
-        if (r >= rows) break;
+      for (int r = 0; r < R; ++r) {
+        const int row = r0 + r;
+        if (row >= rows) break;
         const bool none = l[r] == 0.f;
-        const int i = r / p.group, qh = h * p.group + r % p.group;
-        if (tid < D)
-          p.o[b * p.o_sb + (long long)i * p.o_sn + (long long)qh * p.o_sh + tid] =
+        const int i = row / p.group, qh = h * p.group + row % p.group;
+        if (key < D)
+          p.o[b * p.o_sb + (long long)i * p.o_sn + (long long)qh * p.o_sh + key] =
               __float2bfloat16(none ? 0.f : o[r] / l[r]);
-        if (tid == r) {
+        if (key == r) {
           const float l2 = none ? -INFINITY : log2f(l[r]) + (m[r] == -INFINITY ? 0.f : m[r]) - OFF;
           if (p.lse) p.lse[((long long)b * p.heads + qh) * p.n_q + i] = l2 * LN2;
-          qs[r] = l2;
+          qs[row] = l2;
         }
       }
       if (p.weight) {
-        softmax_sync();
+        softmax_sync<SM>();
         // a thread per piece, those of a tile side by side
         const int ppt = g.tile / 32, pieces = nb * ppt;
-        for (int base = 0; base < pieces; base += 128) {
+        for (int base = 0; base < pieces; base += SM) {
           const int pc = base + tid, i = pc / ppt;
           float w = 0.f;
           if (pc < pieces && pc * 32 < total &&
@@ -534,7 +545,7 @@ __global__ void __launch_bounds__(THREADS, 2)
     tc_fence_before();
   }
   __syncthreads();
-  if (warp == 5) {
+  if (warp == ISSUER) {
     tc_fence_after();
     tmem_dealloc(tmem, Cfg::TMEM);
   }
@@ -638,7 +649,7 @@ cudaError_t launch_rows_t(const KvGeom& g, const KvAttnParams& p, cudaStream_t s
   const cudaError_t e =
       cudaFuncSetAttribute(kv_attn_rows_kernel<D, RP>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::ALLOC);
   if (e != cudaSuccess) return e;
-  kv_attn_rows_kernel<D, RP><<<dim3(p.splits, g.hkv, g.B), THREADS, Cfg::ALLOC, s>>>(g, p, maps);
+  kv_attn_rows_kernel<D, RP><<<dim3(p.splits, g.hkv, g.B), Cfg::THREADS, Cfg::ALLOC, s>>>(g, p, maps);
   return cudaGetLastError();
 }
 
