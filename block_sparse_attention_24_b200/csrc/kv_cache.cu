@@ -12,7 +12,6 @@ namespace veda {
 namespace {
 
 constexpr int APPEND_THREADS = 256;
-constexpr int EVICT_THREADS = 256;
 
 // The least power of two s with 448 s >= a (a >= 0), at least 2^-40; NaN
 // where a is not finite or s would pass 2^80. 448 = 1.75 * 2^8, so the
@@ -35,6 +34,15 @@ __device__ __forceinline__ float2 unpack_e4m3x2(uint16_t c) {
 __device__ __forceinline__ float bf_lo(uint32_t u) { return __uint_as_float(u << 16); }
 __device__ __forceinline__ float bf_hi(uint32_t u) { return __uint_as_float(u & 0xffff0000u); }
 
+// The codes of four bf16 values times f, and of four codes times f.
+__device__ __forceinline__ uint32_t codes_of(uint32_t a, uint32_t b, float f) {
+  return pack_e4m3x4(bf_lo(a) * f, bf_hi(a) * f, bf_lo(b) * f, bf_hi(b) * f);
+}
+__device__ __forceinline__ uint32_t codes_moved(uint32_t c, float f) {
+  const float2 a = unpack_e4m3x2((uint16_t)c), b = unpack_e4m3x2((uint16_t)(c >> 16));
+  return pack_e4m3x4(a.x * f, a.y * f, b.x * f, b.y * f);
+}
+
 // One tile of K or of V of one head: scale' = max(old scale, the new tokens'),
 // old codes moved to it (rounded once more where it grew), new ones quantised,
 // the rows behind the last token zeroed. The tile's bf16 rows are held in
@@ -43,7 +51,7 @@ __device__ __forceinline__ float bf_hi(uint32_t u) { return __uint_as_float(u & 
 template <int D>
 __global__ void __launch_bounds__(APPEND_THREADS)
     kv_append_kernel(const KvGeom g, const KvRows kr, const KvRows vr, const int n, const int32_t* n_new) {
-  constexpr int VPR = D / 8;                           // 8-value vectors per row
+  constexpr int VPR = D / 16;                          // 16-value vectors per row
   constexpr int PT = 128 * VPR / APPEND_THREADS;       // vectors per thread at tile 128
   const int h = blockIdx.y >> 1, is_v = blockIdx.y & 1, b = blockIdx.z;
   int n_b, held, total;
@@ -52,42 +60,44 @@ __global__ void __launch_bounds__(APPEND_THREADS)
   const int row0 = i * g.tile - held;                  // new token in its first row (negative: that row is older)
   if (n_b == 0 || row0 >= n_b) return;
   const long long entry = ((long long)b * g.hkv + h) * g.nb_cap + i;
-  const int slot = g.table[entry];
+  float* scale = (is_v ? g.v_scale : g.k_scale) + entry;
+  const KvRows& x = is_v ? vr : kr;
+  const __nv_bfloat16* src = x.p + b * x.sb + h * x.sh;
+  const bool fresh = row0 >= 0;
+  const int slot = g.table[entry];  // in flight with the rows
+  const float s_old = fresh ? 0.f : *scale;
+
+  uint4 val[PT][2];
+#pragma unroll
+  for (int j = 0; j < PT; ++j) {
+    const int vec = threadIdx.x + j * APPEND_THREADS, r = vec / VPR, c = vec % VPR, t = row0 + r;
+    val[j][0] = val[j][1] = make_uint4(0, 0, 0, 0);
+    if (r < g.tile && t >= 0 && t < n_b) {
+      const uint4* q = reinterpret_cast<const uint4*>(src + (long long)t * x.sn + c * 16);
+      val[j][0] = q[0];
+      val[j][1] = q[1];
+    }
+  }
   if (slot < 0 || slot >= g.n_slots) {
     if (threadIdx.x == 0) report(g.dev_status, VEDA_ERR_BAD_INDEX);
     return;
   }
   uint8_t* codes = (is_v ? g.v8 : g.k8) + (long long)slot * g.tile * D;
-  float* scale = (is_v ? g.v_scale : g.k_scale) + entry;
-  const KvRows& x = is_v ? vr : kr;
-  const __nv_bfloat16* src = x.p + b * x.sb + h * x.sh;
-  const bool fresh = row0 >= 0;
-  const float s_old = fresh ? 0.f : *scale;
-
-  uint4 val[PT];
-  float amax = 0.f;
-#pragma unroll
-  for (int j = 0; j < PT; ++j) {
-    const int vec = threadIdx.x + j * APPEND_THREADS, r = vec / VPR, c = vec % VPR, t = row0 + r;
-    val[j] = make_uint4(0, 0, 0, 0);
-    if (r < g.tile && t >= 0 && t < n_b) val[j] = *reinterpret_cast<const uint4*>(src + (long long)t * x.sn + c * 8);
-  }
   // the largest |x| by its bits: infinities and NaN come out above every finite value
   uint32_t top = 0;
 #pragma unroll
-  for (int j = 0; j < PT; ++j) {
-    const uint32_t w[4] = {val[j].x, val[j].y, val[j].z, val[j].w};
+  for (int j = 0; j < PT; ++j)
 #pragma unroll
-    for (int e = 0; e < 4; ++e) top = max(top, max((w[e] << 16) & 0x7fffffffu, w[e] & 0x7fff0000u));
-  }
+    for (int y = 0; y < 2; ++y)
+      top = max(top, max(max(bf16x2_top(val[j][y].x), bf16x2_top(val[j][y].y)),
+                         max(bf16x2_top(val[j][y].z), bf16x2_top(val[j][y].w))));
   __shared__ uint32_t warp_top[APPEND_THREADS / 32];
   top = __reduce_max_sync(0xffffffffu, top);
   if (threadIdx.x % 32 == 0) warp_top[threadIdx.x / 32] = top;
   __syncthreads();
 #pragma unroll
   for (int w = 0; w < APPEND_THREADS / 32; ++w) top = max(top, warp_top[w]);
-  amax = __uint_as_float(top);
-  const float s_new = scale_of(amax);
+  const float s_new = scale_of(__uint_as_float(top));
   const float s = fresh ? s_new : ((s_new != s_new || s_old != s_old) ? s_new + s_old : fmaxf(s_new, s_old));
   const bool fine = s == s;
   const float inv = fine ? 1.0f / s : 0.f;
@@ -96,20 +106,18 @@ __global__ void __launch_bounds__(APPEND_THREADS)
   for (int j = 0; j < PT; ++j) {
     const int vec = threadIdx.x + j * APPEND_THREADS, r = vec / VPR, c = vec % VPR, t = row0 + r;
     if (r >= g.tile) continue;
-    uint2* dst = reinterpret_cast<uint2*>(codes + r * D + c * 8);
+    uint4* dst = reinterpret_cast<uint4*>(codes + r * D + c * 16);
     if (t >= 0) {
-      uint2 o = make_uint2(0, 0);
+      uint4 o = make_uint4(0, 0, 0, 0);
       if (t < n_b && fine) {
-        o.x = pack_e4m3x4(bf_lo(val[j].x) * inv, bf_hi(val[j].x) * inv, bf_lo(val[j].y) * inv, bf_hi(val[j].y) * inv);
-        o.y = pack_e4m3x4(bf_lo(val[j].z) * inv, bf_hi(val[j].z) * inv, bf_lo(val[j].w) * inv, bf_hi(val[j].w) * inv);
+        const uint4 a = val[j][0], e = val[j][1];
+        o = make_uint4(codes_of(a.x, a.y, inv), codes_of(a.z, a.w, inv), codes_of(e.x, e.y, inv), codes_of(e.z, e.w, inv));
       }
       *dst = o;
     } else if (fine && s != s_old) {
       const float f = s_old * inv;
-      const uint2 w = *dst;
-      const float2 a = unpack_e4m3x2((uint16_t)w.x), e = unpack_e4m3x2((uint16_t)(w.x >> 16));
-      const float2 p = unpack_e4m3x2((uint16_t)w.y), q = unpack_e4m3x2((uint16_t)(w.y >> 16));
-      *dst = make_uint2(pack_e4m3x4(a.x * f, a.y * f, e.x * f, e.y * f), pack_e4m3x4(p.x * f, p.y * f, q.x * f, q.y * f));
+      const uint4 w = *dst;
+      *dst = make_uint4(codes_moved(w.x, f), codes_moved(w.y, f), codes_moved(w.z, f), codes_moved(w.w, f));
     }
   }
   if (threadIdx.x == 0) {
@@ -143,58 +151,74 @@ __device__ __forceinline__ uint32_t rank_key(float w) {
 }
 
 // Exclusive prefix of `flag` over the block, and its total.
+template <int THREADS>
 __device__ __forceinline__ int block_prefix(bool flag, int* warp_n, int& total) {
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const uint32_t m = __ballot_sync(0xffffffffu, flag);
   __syncthreads();  // the last call's counts have been read
   if (lane == 0) warp_n[warp] = __popc(m);
   __syncthreads();
-  int before = 0;
-  total = 0;
-#pragma unroll
-  for (int w = 0; w < EVICT_THREADS / 32; ++w) {
-    const int c = warp_n[w];
-    before += w < warp ? c : 0;
-    total += c;
-  }
+  // every warp sums the counts for itself
+  const int c = lane < THREADS / 32 ? warp_n[lane] : 0;
+  total = __reduce_add_sync(0xffffffffu, c);
+  const int before = __reduce_add_sync(0xffffffffu, lane < warp ? c : 0);
   return before + __popc(m & ((1u << lane) - 1u));
 }
 
 // One (sequence, head): the row of the table is read whole into shared
 // memory, the weight of the last tile that stays is found by radix selection
-// (8 bits at a time), and the row is written back with the tiles that stay
-// first, in their order, then those that go, then the free ones. Nothing of
-// the codes moves. A few microseconds of latency, no bandwidth to speak of.
-__global__ void __launch_bounds__(EVICT_THREADS)
+// (8 bits at a time; weights mostly share their exponents, so eight
+// histograms, by lane, keep the counters apart), and the row is written back
+// with the tiles that stay first, in their order, then those that go, then the
+// free ones. Nothing of the codes moves. Latency, not bandwidth, is the bound:
+// the block has a thread per two to four entries.
+template <int THREADS>
+__global__ void __launch_bounds__(THREADS)
     kv_evict_kernel(const KvGeom g, const KvGeom out, const KvKeep keeps, const int sink, const int recent) {
   extern __shared__ uint32_t sm[];
+  const int cap = (g.nb_cap + 3) & ~3;
   uint32_t* f_table = sm;
-  uint32_t* f_pos = sm + g.nb_cap;
-  uint32_t* f_ks = sm + 2 * g.nb_cap;
-  uint32_t* f_vs = sm + 3 * g.nb_cap;
-  uint32_t* f_w = sm + 4 * g.nb_cap;
-  __shared__ int hist[256];
-  __shared__ int warp_n[EVICT_THREADS / 32];
+  uint32_t* f_pos = sm + cap;
+  uint32_t* f_ks = sm + 2 * cap;
+  uint32_t* f_vs = sm + 3 * cap;
+  uint32_t* f_w = sm + 4 * cap;
+  __shared__ int hist[8][256];
+  __shared__ int warp_n[32];
   __shared__ uint32_t sh_prefix;
   __shared__ int sh_want;
-  const int h = blockIdx.x, b = blockIdx.y, tid = threadIdx.x;
+  const int h = blockIdx.x, b = blockIdx.y, tid = threadIdx.x, lane = tid % 32;
   const int bh = b * g.hkv + h;
   const long long row = (long long)bh * g.nb_cap;
   const int held = g.len[bh];
+  const bool same = out.table == g.table;
+  // a row starts at a multiple of 16 bytes where its length is one of 4
+  if (g.nb_cap % 4 == 0) {
+    for (int i = tid; i < g.nb_cap / 4; i += THREADS) {
+      reinterpret_cast<uint4*>(f_table)[i] = reinterpret_cast<const uint4*>(g.table + row)[i];
+      reinterpret_cast<uint4*>(f_pos)[i] = reinterpret_cast<const uint4*>(g.pos + row)[i];
+      reinterpret_cast<uint4*>(f_ks)[i] = reinterpret_cast<const uint4*>(g.k_scale + row)[i];
+      reinterpret_cast<uint4*>(f_vs)[i] = reinterpret_cast<const uint4*>(g.v_scale + row)[i];
+      reinterpret_cast<uint4*>(f_w)[i] = reinterpret_cast<const uint4*>(g.weight + row)[i];
+    }
+  } else {
+#pragma unroll 2
+    for (int i = tid; i < g.nb_cap; i += THREADS) {
+      const uint32_t a = (uint32_t)g.table[row + i], c = (uint32_t)g.pos[row + i], d = __float_as_uint(g.k_scale[row + i]),
+                     e = __float_as_uint(g.v_scale[row + i]), f = __float_as_uint(g.weight[row + i]);
+      f_table[i] = a;
+      f_pos[i] = c;
+      f_ks[i] = d;
+      f_vs[i] = e;
+      f_w[i] = f;
+    }
+  }
   const bool bad = held < 0 || (long long)held > (long long)g.nb_cap * g.tile;
   if (bad && tid == 0) report(g.dev_status, VEDA_ERR_BAD_INDEX);
   const int nb = bad ? 0 : (int)(((long long)held + g.tile - 1) / g.tile);
   const int keep = keeps.k[h];
   const bool cut = nb > keep;
-  const bool same = out.table == g.table;
   if (!cut && same) return;
-  for (int i = tid; i < g.nb_cap; i += EVICT_THREADS) {
-    f_table[i] = (uint32_t)g.table[row + i];
-    f_pos[i] = (uint32_t)g.pos[row + i];
-    f_ks[i] = __float_as_uint(g.k_scale[row + i]);
-    f_vs[i] = __float_as_uint(g.v_scale[row + i]);
-    f_w[i] = __float_as_uint(g.weight[row + i]);
-  }
+  for (int i = tid; i < 8 * 256; i += THREADS) (&hist[0][0])[i] = 0;
   __syncthreads();
   auto put = [&](int i, int to) {
     out.table[row + to] = (int32_t)f_table[i];
@@ -205,7 +229,7 @@ __global__ void __launch_bounds__(EVICT_THREADS)
   };
   if (h == 0 && tid == 0 && !same) out.next_pos[b] = g.next_pos[b];
   if (!cut) {
-    for (int i = tid; i < g.nb_cap; i += EVICT_THREADS) put(i, i);
+    for (int i = tid; i < g.nb_cap; i += THREADS) put(i, i);
     if (tid == 0) out.len[bh] = held;
     return;
   }
@@ -213,63 +237,68 @@ __global__ void __launch_bounds__(EVICT_THREADS)
   // many with exactly that key stay
   const int lo = sink, hi = nb - recent;
   int want = keep - sink - recent;
+  const bool none = want == 0;
   uint32_t prefix = 0;
-  if (want > 0) {
-    for (int shift = 24; shift >= 0; shift -= 8) {
-      for (int i = tid; i < 256; i += EVICT_THREADS) hist[i] = 0;
-      __syncthreads();
-      for (int i = lo + tid; i < hi; i += EVICT_THREADS) {
-        const uint32_t k = rank_key(__uint_as_float(f_w[i]));
-        if (shift == 24 || (k >> (shift + 8)) == (prefix >> (shift + 8))) atomicAdd(&hist[(k >> shift) & 255u], 1);
-      }
-      __syncthreads();
-      if (tid < 32) {  // bins from the top, eight per lane
-        int c[8], sum = 0;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) sum += c[e] = hist[255 - (tid * 8 + e)];
-        int incl = sum;
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-          const int v = __shfl_up_sync(0xffffffffu, incl, d);
-          if (tid >= d) incl += v;
-        }
-        int above = incl - sum;
-        if (above < want && want <= incl) {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            if (above < want && want <= above + c[e]) {
-              sh_prefix = prefix | ((uint32_t)(255 - (tid * 8 + e)) << shift);
-              sh_want = want - above;
-            }
-            above += c[e];
-          }
-        }
-      }
-      __syncthreads();
-      prefix = sh_prefix;
-      want = sh_want;
-      __syncthreads();
+  for (int shift = 24; shift >= 0 && !none; shift -= 8) {
+    for (int i = lo + tid; i < hi; i += THREADS) {
+      const uint32_t k = rank_key(__uint_as_float(f_w[i]));
+      if (shift == 24 || (k >> (shift + 8)) == (prefix >> (shift + 8))) atomicAdd(&hist[lane & 7][(k >> shift) & 255u], 1);
     }
+    __syncthreads();
+    if (tid < 256) {  // thread t has bin 255 - t, so that a prefix counts from the top
+      int c = 0;
+#pragma unroll
+      for (int y = 0; y < 8; ++y) {
+        c += hist[y][255 - tid];
+        hist[y][255 - tid] = 0;
+      }
+      int incl = c;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, incl, d);
+        if (lane >= d) incl += v;
+      }
+      if (lane == 31) warp_n[tid / 32] = incl;
+      asm volatile("bar.sync 1, 256;" ::: "memory");
+      const int w = lane < 8 ? warp_n[lane] : 0;
+      const int above = __reduce_add_sync(0xffffffffu, lane < tid / 32 ? w : 0) + incl - c;
+      if (above < want && want <= above + c) {
+        sh_prefix = prefix | ((uint32_t)(255 - tid) << shift);
+        sh_want = want - above;
+      }
+    }
+    __syncthreads();
+    prefix = sh_prefix;
+    want = sh_want;
   }
   int stays = 0, goes = 0, ties = 0;
-  for (int base = 0; base < nb; base += EVICT_THREADS) {
+  for (int base = 0; base < nb; base += THREADS) {
     const int i = base + tid;
     const bool mid = i >= lo && i < hi, in = i < nb;
     const uint32_t k = mid ? rank_key(__uint_as_float(f_w[i])) : 0;
-    const bool none = keep - sink - recent == 0;
     const bool tie = mid && !none && k == prefix;
     int n_tie, n_stay;
-    const int t = block_prefix(tie, warp_n, n_tie);
+    const int t = block_prefix<THREADS>(tie, warp_n, n_tie);
     const bool stay = in && (!mid || (!none && (k > prefix || (tie && ties + t < want))));
-    const int r = block_prefix(stay, warp_n, n_stay);
+    const int r = block_prefix<THREADS>(stay, warp_n, n_stay);
     if (in) put(i, stay ? stays + r : keep + goes + (tid - r));
     ties += n_tie;
     stays += n_stay;
-    goes += min(EVICT_THREADS, nb - base) - n_stay;
+    goes += min(THREADS, nb - base) - n_stay;
   }
   if (!same)
-    for (int i = nb + tid; i < g.nb_cap; i += EVICT_THREADS) put(i, i);
+    for (int i = nb + tid; i < g.nb_cap; i += THREADS) put(i, i);
   if (tid == 0) out.len[bh] = held - (nb - keep) * g.tile;
+}
+
+template <int THREADS>
+cudaError_t launch_evict(const KvGeom& g, const KvKeep& keeps, int sink, int recent, const KvGeom& out, cudaStream_t s) {
+  const int smem = 5 * 4 * ((g.nb_cap + 3) & ~3);  // at most 160 KB
+  const cudaError_t e =
+      cudaFuncSetAttribute(kv_evict_kernel<THREADS>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  kv_evict_kernel<THREADS><<<dim3(g.hkv, g.B), THREADS, smem, s>>>(g, out, keeps, sink, recent);
+  return cudaGetLastError();
 }
 
 }  // namespace
@@ -292,11 +321,9 @@ cudaError_t launch_kv_evict(const KvGeom& g, const int32_t* keep, int sink, int 
                             cudaStream_t s) {
   KvKeep keeps;
   for (int h = 0; h < g.hkv; ++h) keeps.k[h] = keep[h];
-  const int smem = 5 * 4 * g.nb_cap;  // at most 160 KB
-  const cudaError_t e = cudaFuncSetAttribute(kv_evict_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e != cudaSuccess) return e;
-  kv_evict_kernel<<<dim3(g.hkv, g.B), EVICT_THREADS, smem, s>>>(g, out, keeps, sink, recent);
-  return cudaGetLastError();
+  return g.nb_cap <= 1024 ? launch_evict<256>(g, keeps, sink, recent, out, s)
+                          : g.nb_cap <= 2048 ? launch_evict<512>(g, keeps, sink, recent, out, s)
+                                             : launch_evict<1024>(g, keeps, sink, recent, out, s);
 }
 
 }  // namespace veda
