@@ -551,37 +551,49 @@ __global__ void __launch_bounds__((RowsCfg<D, RP>::THREADS), 2)
   }
 }
 
+// The kernels below start while the one before them ends, and wait here for
+// its results.
+__device__ __forceinline__ void grid_dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // Joins the splits of a row: a warp per row.
 template <int D>
 __global__ void __launch_bounds__(128) kv_join_kernel(const KvGeom g, const KvAttnParams p) {
   const int lane = threadIdx.x % 32, h = blockIdx.y, b = blockIdx.z;
   const int r = blockIdx.x * 4 + threadIdx.x / 32;
+  grid_dependency_wait();
   int n_b, held, total;
   if (!kv_counts(g, b, h, p.n_q, p.n_new, p.pending, n_b, held, total)) return;
   if (r >= n_b * p.group) return;
   const int bh = b * g.hkv + h;
   const long long rows = p.rows_pad;
   const float2* ml = p.part_ml + (long long)bh * p.splits * rows + r;
-  float m = -INFINITY;
-  for (int s = 0; s < p.splits; ++s) m = fmaxf(m, ml[s * rows].x);
-  float l = 0.f, o[D / 32];
+  // a lane per part (32 at most): its factor and its share of the sum
+  float2 x = make_float2(-INFINITY, 0.f);
+  if (lane < p.splits) x = ml[lane * rows];
+  float m = x.x;
+#pragma unroll
+  for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+  const float f = x.x == -INFINITY ? (x.y == x.y ? 0.f : 1.f) : fast_exp2(x.x - m);
+  float l = x.y * f, o[D / 32];
+#pragma unroll
+  for (int d = 16; d; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
 #pragma unroll
   for (int e = 0; e < D / 32; ++e) o[e] = 0.f;
+#pragma unroll 4
   for (int s = 0; s < p.splits; ++s) {
-    const float2 x = ml[s * rows];
-    const float f = x.x == -INFINITY ? (x.y == x.y ? 0.f : 1.f) : fast_exp2(x.x - m);
-    l += x.y * f;
+    const float fs = __shfl_sync(0xffffffffu, f, s);
+    if (fs == 0.f) continue;  // a part without keys has written nothing else
     const float* src = p.part_o + (((long long)bh * p.splits + s) * rows + r) * D + lane * (D / 32);
     if constexpr (D == 128) {
       const float4 v = *reinterpret_cast<const float4*>(src);
-      o[0] += v.x * f;
-      o[1] += v.y * f;
-      o[2] += v.z * f;
-      o[3] += v.w * f;
+      o[0] += v.x * fs;
+      o[1] += v.y * fs;
+      o[2] += v.z * fs;
+      o[3] += v.w * fs;
     } else {
       const float2 v = *reinterpret_cast<const float2*>(src);
-      o[0] += v.x * f;
-      o[1] += v.y * f;
+      o[0] += v.x * fs;
+      o[1] += v.y * fs;
     }
   }
   const bool none = l == 0.f;
@@ -600,32 +612,40 @@ __global__ void __launch_bounds__(128) kv_join_kernel(const KvGeom g, const KvAt
   }
 }
 
-// weight[tile] = decay * weight[tile] + sum over rows and the tile's pieces of
-// 2^(lw - lse2): a block per tile, its sums joined in a fixed order.
-constexpr int WEIGHT_THREADS = 256;  // a row tile's rows at most
+// weight[tile] = decay * weight[tile] + sum over rows of 2^(lw - lse2): a block
+// per tile, its sums joined in a fixed order.
+constexpr int WEIGHT_THREADS = 256;  // a row tile's rows
 __global__ void __launch_bounds__(WEIGHT_THREADS) kv_weight_kernel(const KvGeom g, const KvAttnParams p) {
   __shared__ float part[WEIGHT_THREADS / 32];
   const int i = blockIdx.x, h = blockIdx.y, b = blockIdx.z, tid = threadIdx.x;
   int n_b, held, total;
-  if (!kv_counts(g, b, h, p.n_q, p.n_new, p.pending, n_b, held, total)) return;
-  const int nb = (total + g.tile - 1) / g.tile;
-  if (i >= nb || n_b == 0) return;
-  const int bh = b * g.hkv + h, ppt = g.tile / p.piece;
+  const int bh = b * g.hkv + h;
   const long long entry = (long long)bh * g.nb_cap + i;
-  const int rows = n_b * p.group, t0 = g.next_pos[b], ps = g.pos[entry];
+  const int t0 = g.next_pos[b], ps = g.pos[entry];
+  const bool fine = kv_counts(g, b, h, p.n_q, p.n_new, p.pending, n_b, held, total);
+  grid_dependency_wait();
+  const int nb = (total + g.tile - 1) / g.tile;
+  if (!fine || i >= nb || n_b == 0) return;
+  const int rows = n_b * p.group;
   const float* lse2 = p.lse2 + (long long)bh * p.rows_cap;
-  const float* lw = p.lw + ((long long)bh * p.pieces_cap + (long long)i * ppt) * p.rows_cap;
+  const float* lw = p.lw + ((long long)bh * p.pieces_cap + i) * p.rows_cap;
   float w = 0.f;
-  // row tile by row tile: only tiles that a row tile's CTA could see were visited
-#pragma unroll 4
-  for (int m0 = 0; m0 < rows; m0 += p.tile_rows) {
-    const int m1 = min(rows, m0 + p.tile_rows) - 1, r = m0 + tid;
-    if (r > m1 || !kv_tile_seen(ps, g.tile, t0 + m0 / p.group, t0 + m1 / p.group, p.causal, p.window, p.sinks)) continue;
-    const float z = lse2[r];
-    if (z == -INFINITY) continue;
-    for (int k = 0; k < ppt && i * g.tile + k * p.piece < total; ++k) {
-      const float x = lw[(long long)k * p.rows_cap + r];
-      if (x != -INFINITY) w += fast_exp2(x - z);  // none of it seen: nothing, even of a row that is NaN
+  constexpr int AHEAD = 4;  // row tiles whose loads are in flight
+  for (int m0 = 0; m0 < rows; m0 += AHEAD * WEIGHT_THREADS) {
+    float z[AHEAD], x[AHEAD];
+#pragma unroll
+    for (int u = 0; u < AHEAD; ++u) {
+      const int r = m0 + u * WEIGHT_THREADS + tid;
+      z[u] = r < rows ? lse2[r] : -INFINITY;
+      x[u] = r < rows ? lw[r] : -INFINITY;
+    }
+#pragma unroll
+    for (int u = 0; u < AHEAD; ++u) {
+      // only tiles that a row tile's CTA could see were visited
+      const int a = m0 + u * WEIGHT_THREADS, c = min(rows, a + WEIGHT_THREADS) - 1;
+      if (a > c || !kv_tile_seen(ps, g.tile, t0 + a / p.group, t0 + c / p.group, p.causal, p.window, p.sinks)) continue;
+      // none of it seen: nothing, even of a row that is NaN
+      if (z[u] != -INFINITY && x[u] != -INFINITY) w += fast_exp2(x[u] - z[u]);
     }
   }
 #pragma unroll
@@ -636,6 +656,22 @@ __global__ void __launch_bounds__(WEIGHT_THREADS) kv_weight_kernel(const KvGeom 
     for (int k = 1; k < WEIGHT_THREADS / 32; ++k) w += part[k];
     p.weight[entry] = p.decay == 0.f ? w : p.decay * p.weight[entry] + w;
   }
+}
+
+// A launch that may start before the kernel before it in the stream has ended
+// (which it waits for itself).
+cudaError_t launch_behind(void (*kernel)(const KvGeom, const KvAttnParams), dim3 grid, int threads, cudaStream_t s,
+                          const KvGeom& g, const KvAttnParams& p) {
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.stream = s;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, g, p);
 }
 
 template <int D, int RP>
@@ -730,13 +766,10 @@ cudaError_t launch_kv_attn(const KvGeom& g, KvAttnParams p, void* ws, cudaStream
   if (e != cudaSuccess) return e;
   if (p.splits > 1) {
     const dim3 jg((p.rows_cap + 3) / 4, g.hkv, g.B);
-    if (g.d == 128) kv_join_kernel<128><<<jg, 128, 0, s>>>(g, p);
-    else kv_join_kernel<64><<<jg, 128, 0, s>>>(g, p);
-    e = cudaGetLastError();
+    e = g.d == 128 ? launch_behind(kv_join_kernel<128>, jg, 128, s, g, p) : launch_behind(kv_join_kernel<64>, jg, 128, s, g, p);
   }
   if (e != cudaSuccess || !p.weight) return e;
-  kv_weight_kernel<<<dim3(g.nb_cap, g.hkv, g.B), WEIGHT_THREADS, 0, s>>>(g, p);
-  return cudaGetLastError();
+  return launch_behind(kv_weight_kernel, dim3(g.nb_cap, g.hkv, g.B), WEIGHT_THREADS, s, g, p);
 }
 
 }  // namespace veda

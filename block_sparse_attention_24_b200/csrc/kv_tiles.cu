@@ -53,11 +53,23 @@ struct TileLayout {
   static constexpr int OFF_W = OFF_V + VST * CB;
   static constexpr int OFF_META = OFF_W + WST * WB;
   static constexpr int OFF_BAR = OFF_META + MST * (int)sizeof(StepMeta);
-  static constexpr int NUM_BARS = 1 + KST + 2 * VST + WST + SDR + 2 + 2 + 2 + 1;
+  static constexpr int NUM_BARS = KST + 2 * VST + WST + SDR + 2 + 2 + 2 + 1;
   static constexpr int OFF_MISC = OFF_BAR + NUM_BARS * 8;
   static constexpr int ALLOC = OFF_MISC + 32 + 1024;
 };
 static_assert(sizeof(StepMeta) % 8 == 0, "barriers follow");
+
+// Token and head-of-group of a row, kept along as rows advance by a few.
+struct RowStep {
+  int tok, gh;
+  __device__ __forceinline__ void advance(int n, int group) {
+    gh += n;
+    while (gh >= group) {
+      gh -= group;
+      ++tok;
+    }
+  }
+};
 
 // The keys of one half that the query at position t sees, as bits.
 __device__ __forceinline__ uint64_t half_seen(const KvAttnParams& p, int t, int pos, int left) {
@@ -121,6 +133,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   const int mt = p.row_tiles - 1 - (int)(blockIdx.x / p.splits), sp = blockIdx.x % p.splits, h = blockIdx.y,
             b = blockIdx.z;
   int n_b, held, total;
+  const int t0 = g.next_pos[b];
   if (!kv_counts(g, b, h, p.n_q, p.n_new, p.pending, n_b, held, total)) return;
   const int rows = n_b * p.group;
   const int base = mt * 2 * BM;
@@ -128,12 +141,31 @@ __global__ void __launch_bounds__(THREADS, 1)
   const bool has_b = base + BM < rows;
   const int bh = b * g.hkv + h;
   const long long trow = (long long)bh * g.nb_cap;
-  const int t0 = g.next_pos[b];
   const int t_lo = t0 + base / p.group, t_hi = t0 + (min(rows, base + 2 * BM) - 1) / p.group;
 
+  // Q, a row per D/8 lanes: a warp reads and later writes whole rows. Lane
+  // group `sub` has rows sub, sub + RPI, ... of the warp's 32.
+  constexpr int LPR = D / 8, RPI = 32 / LPR, ITERS = 32 / RPI;
+  const int rt = warp / 4, wrow = base + warp * 32, sub = lane / LPR, c8 = lane % LPR;
+  int tok0 = 0, gh0 = 0;  // token and head of the group of row wrow + sub
+  uint4 qw[ITERS];
+  const bool mine = warp < 4 || (warp < 8 && has_b);
+  if (mine) {
+    tok0 = (wrow + sub) / p.group;
+    gh0 = (wrow + sub) % p.group;
+    const __nv_bfloat16* src = p.q.p + b * p.q.sb + (long long)h * p.group * p.q.sh + c8 * 8;
+    RowStep at{tok0, gh0};
+#pragma unroll
+    for (int j = 0; j < ITERS; ++j) {
+      qw[j] = make_uint4(0, 0, 0, 0);
+      if (wrow + sub + j * RPI < rows)
+        qw[j] = *reinterpret_cast<const uint4*>(src + (long long)at.tok * p.q.sn + (long long)at.gh * p.q.sh);
+      at.advance(RPI, p.group);
+    }
+  }
+
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Lay::OFF_BAR);
-  uint64_t* q_full = bars;
-  uint64_t* k_full = bars + 1;
+  uint64_t* k_full = bars;
   uint64_t* v_full = k_full + KST;
   uint64_t* v_free = v_full + VST;   // an arrival per converting warp: it has read the codes
   uint64_t* w_full = v_free + VST;   // an arrival per converting warp
@@ -145,32 +177,10 @@ __global__ void __launch_bounds__(THREADS, 1)
   StepMeta* meta = reinterpret_cast<StepMeta*>(smem + Lay::OFF_META);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Lay::OFF_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Lay::OFF_MISC + 4);
-  if (tid == 0) {
-    for (int i = 0; i < Lay::NUM_BARS; ++i) {
-      uint64_t* bar = bars + i;
-      int count = 1;
-      if (bar == q_full) count = has_b ? 256 : 128;
-      if (bar >= v_free && bar < w_full + WST) count = CONVERT_WARPS;
-      if (bar == p_full || bar == p_full + 1) count = 128;
-      mbar_init(bar, count);
-    }
-    *abort_flag = 0;
-    fence_mbar_init();
+  if (p.window > 0 || p.causal) {
+    if (tid < 3) sm_cnt[tid] = 0;
+    __syncthreads();
   }
-  if (tid < 3) sm_cnt[tid] = 0;
-  if (tid == 256) {
-    tma_prefetch_desc(&maps.k);
-    tma_prefetch_desc(&maps.v);
-  }
-  if (warp == 9) {
-    tmem_alloc(tmem_slot, 512);
-    tmem_relinquish();
-  }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
-
   const int nb = (total + g.tile - 1) / g.tile;
   const KvRange rg = kv_range(g, p, trow, nb, t_lo, t_hi, t0 + n_b - 1, sm_cnt, tid, THREADS);
   const int per_step = BN / g.tile;  // tiles per step
@@ -178,36 +188,88 @@ __global__ void __launch_bounds__(THREADS, 1)
   const int steps_all = (n_tiles + per_step - 1) / per_step;
   const int per = (steps_all + p.splits - 1) / p.splits;
   const int s_lo = min(steps_all, sp * per), n_steps = min(steps_all, s_lo + per) - s_lo;
+  if (n_steps == 0 && p.splits > 1) {  // nothing to add: the join skips this part
+    for (int r = base + tid; r < min(rows, base + 2 * BM); r += THREADS)
+      p.part_ml[((long long)bh * p.splits + sp) * p.rows_pad + r] = make_float2(-INFINITY, 0.f);
+    return;
+  }
+
+  // Each role prepares its part before the one barrier: the first copies are
+  // under way while Q is taken apart.
+  StepFeed feed;
+  int fed = 0;  // steps whose copies were issued (the producer's)
+  auto produce = [&](int e) {
+    if ((e & 15) == 0) feed.load(g, trow, rg, total, s_lo, e, n_steps, lane);
+    const int st = e % KST, vt = e % VST;
+    int row0, row1;
+    feed.put(meta[e % MST], g, p, e, t_lo, t_hi, lane, row0, row1);
+    __syncwarp();
+    if (lane == 0) {
+      const uint32_t bytes = (row0 >= 0 ? Lay::CB / 2 : 0) + (row1 >= 0 ? Lay::CB / 2 : 0);
+      uint8_t* kd = smem + Lay::OFF_K + st * Lay::CB;
+      uint8_t* vd = smem + Lay::OFF_V + vt * Lay::CB;
+      mbar_expect_tx(k_full + st, bytes);
+      if (row0 >= 0) tma_load_2d(kd, &maps.k, k_full + st, 0, row0);
+      if (row1 >= 0) tma_load_2d(kd + Lay::CB / 2, &maps.k, k_full + st, 0, row1);
+      mbar_expect_tx(v_full + vt, bytes);
+      if (row0 >= 0) tma_load_2d(vd, &maps.v, v_full + vt, 0, row0);
+      if (row1 >= 0) tma_load_2d(vd + Lay::CB / 2, &maps.v, v_full + vt, 0, row1);
+    }
+    __syncwarp();
+  };
+  uint8_t* own = smem + Lay::OFF_Q + rt * 2 * Lay::QB;  // the row tile's Q, and its O at the end
+  float qs = 0.f;
+  if (warp == 8) {
+    if (lane < Lay::NUM_BARS) {
+      uint64_t* bar = bars + lane;
+      mbar_init(bar, bar >= v_free && bar < w_full + WST ? CONVERT_WARPS : bar == p_full || bar == p_full + 1 ? 128 : 1);
+    }
+    if (lane == 0) *abort_flag = 0;
+    fence_mbar_init();
+    __syncwarp();
+    for (; fed < VST && fed < n_steps; ++fed) produce(fed);
+  } else if (warp == 9) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  } else if (mine) {
+    // Q in its two e4m3 parts
+#pragma unroll
+    for (int j = 0; j < ITERS; ++j) {
+      uint32_t top = max(max(bf16x2_top(qw[j].x), bf16x2_top(qw[j].y)), max(bf16x2_top(qw[j].z), bf16x2_top(qw[j].w)));
+#pragma unroll
+      for (int d = 1; d < LPR; d <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
+      float mul, inv;
+      q_scale<7>(top, mul, inv);
+      mul = copysignf(mul, p.scale_log2);
+      uint32_t hi[2], lo[2];
+      split_e4m3x4(qw[j].x, qw[j].y, mul, hi[0], lo[0]);
+      split_e4m3x4(qw[j].z, qw[j].w, mul, hi[1], lo[1]);
+      const int at = code_at<D>((warp % 4) * 32 + j * RPI + sub, c8 >> 1) + (c8 & 1) * 8;
+      *reinterpret_cast<uint2*>(own + at) = make_uint2(hi[0], hi[1]);
+      *reinterpret_cast<uint2*>(own + Lay::QB + at) = make_uint2(lo[0], lo[1]);
+      // the lane that owns the row keeps its factor
+      const float got = __shfl_sync(0xffffffffu, inv, (lane % RPI) * LPR);
+      if (lane / RPI == j) qs = got;
+    }
+    qs *= fabsf(p.scale_log2);
+    fence_proxy_async_smem();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
 
   if (warp >= 8) {
     regs_lower<REGS_ROLES>();
     if (warp == 8) {
       // --------------------------------------------------------- producer
-      StepFeed feed;
-      int e = 0;
-      bool ok = true;
+      int e = fed;
       for (; e < n_steps; ++e) {
-        if ((e & 15) == 0) feed.load(g, trow, rg, total, s_lo, e, n_steps, lane);
-        const int st = e % KST, vt = e % VST, ms = e % MST;
         // the description's slot is free: step_done(e - KST) follows the softmax of step e - KST - 1
-        if (e >= KST) ok = mbar_wait(step_done + (e - KST) % SDR, ((e - KST) / SDR) & 1, abort_flag, g.dev_status);
-        if (ok && e >= VST) ok = mbar_wait(v_free + vt, (e / VST - 1) & 1, abort_flag, g.dev_status);
+        bool ok = e < KST || mbar_wait(step_done + (e - KST) % SDR, ((e - KST) / SDR) & 1, abort_flag, g.dev_status);
+        ok = ok && mbar_wait(v_free + e % VST, (e / VST - 1) & 1, abort_flag, g.dev_status);
         if (!__all_sync(0xffffffffu, ok)) break;
-        int row0, row1;
-        feed.put(meta[ms], g, p, e, t_lo, t_hi, lane, row0, row1);
-        __syncwarp();
-        if (lane == 0) {
-          const uint32_t bytes = (row0 >= 0 ? Lay::CB / 2 : 0) + (row1 >= 0 ? Lay::CB / 2 : 0);
-          uint8_t* kd = smem + Lay::OFF_K + st * Lay::CB;
-          uint8_t* vd = smem + Lay::OFF_V + vt * Lay::CB;
-          mbar_expect_tx(k_full + st, bytes);
-          if (row0 >= 0) tma_load_2d(kd, &maps.k, k_full + st, 0, row0);
-          if (row1 >= 0) tma_load_2d(kd + Lay::CB / 2, &maps.k, k_full + st, 0, row1);
-          mbar_expect_tx(v_full + vt, bytes);
-          if (row0 >= 0) tma_load_2d(vd, &maps.v, v_full + vt, 0, row0);
-          if (row1 >= 0) tma_load_2d(vd + Lay::CB / 2, &maps.v, v_full + vt, 0, row1);
-        }
-        __syncwarp();
+        produce(e);
       }
       if (*abort_flag && lane == 0) {  // let every copy that was started land
         for (int x = max(0, e - KST); x < e; ++x) mbar_wait_drain(k_full + x % KST, (x / KST) & 1, VEDA_WAIT_LIMIT_NS);
@@ -221,8 +283,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       const uint64_t dQ = sdesc_codes<D>(smem_u32(smem + Lay::OFF_Q));
       const uint64_t dK = sdesc_codes<D>(smem_u32(smem + Lay::OFF_K));
       const uint64_t dW = sdesc_sw128(smem_u32(smem + Lay::OFF_W), BN * 128, 1024);
-      bool ok = n_steps == 0 || mbar_wait(q_full, 0, abort_flag, g.dev_status);
-      if (ok) tc_fence_after();
+      bool ok = true;
       const int tiles = has_b ? 2 : 1;
       auto issue_pv = [&](int r, int e) -> bool {  // P V of step e
         const int ws = e % WST;
@@ -316,53 +377,11 @@ __global__ void __launch_bounds__(THREADS, 1)
   } else {
     regs_raise<REGS_SOFTMAX>();
     // ------------------------------------------------------------ softmax
-    const int rt = warp / 4;
     const int row = base + tid;  // tid is 0..255 here
     const bool row_valid = row < rows;
-    const int t = t0 + row / p.group;
-    const int w_lo = t0 + (base + warp * 32) / p.group;
-    const int w_hi = t0 + (min(rows, base + warp * 32 + 32) - 1) / p.group;  // the warp's positions
+    const int tok = row / p.group, t = t0 + tok;
     const uint32_t lane_addr = tmem + ((uint32_t)((warp % 4) * 32) << 16);
     const uint32_t s_col = rt * BN, o_col = 2 * BN + rt * BN;
-    const bool mine = rt == 0 || has_b;
-    uint8_t* own = smem + Lay::OFF_Q + rt * 2 * Lay::QB;  // the row tile's Q, and its O at the end
-    float qs = 0.f;
-    if (mine && n_steps > 0) {
-      // Q in its two e4m3 parts: D/8 lanes read a row, so that a warp reads
-      // whole rows at once
-      constexpr int LPR = D / 8, RPI = 32 / LPR, ITERS = 32 / RPI;
-      const int wr = (warp % 4) * 32, sub = lane / LPR, c8 = lane % LPR;  // the warp's rows in the tile
-      uint4 w[ITERS];
-#pragma unroll
-      for (int j = 0; j < ITERS; ++j) {
-        const int gr = base + rt * BM + wr + j * RPI + sub;
-        w[j] = make_uint4(0, 0, 0, 0);
-        if (gr < rows)
-          w[j] = *reinterpret_cast<const uint4*>(p.q.p + b * p.q.sb + (long long)(gr / p.group) * p.q.sn +
-                                                 (long long)(h * p.group + gr % p.group) * p.q.sh + c8 * 8);
-      }
-#pragma unroll
-      for (int j = 0; j < ITERS; ++j) {
-        uint32_t top = max(max(bf16x2_top(w[j].x), bf16x2_top(w[j].y)), max(bf16x2_top(w[j].z), bf16x2_top(w[j].w)));
-#pragma unroll
-        for (int d = 1; d < LPR; d <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
-        float mul, inv;
-        q_scale<7>(top, mul, inv);
-        mul = copysignf(mul, p.scale_log2);
-        uint32_t hi[2], lo[2];
-        split_e4m3x4(w[j].x, w[j].y, mul, hi[0], lo[0]);
-        split_e4m3x4(w[j].z, w[j].w, mul, hi[1], lo[1]);
-        const int r = wr + j * RPI + sub, at = code_at<D>(r, c8 >> 1) + (c8 & 1) * 8;
-        *reinterpret_cast<uint2*>(own + at) = make_uint2(hi[0], hi[1]);
-        *reinterpret_cast<uint2*>(own + Lay::QB + at) = make_uint2(lo[0], lo[1]);
-        // the lane that owns the row keeps its factor
-        const float got = __shfl_sync(0xffffffffu, inv, (lane % RPI) * LPR);
-        if (lane / RPI == j) qs = got;
-      }
-      qs *= fabsf(p.scale_log2);
-      fence_proxy_async_smem();
-      mbar_arrive(q_full);
-    }
     float m = -INFINITY, l = 0.f;
     bool ok = true;
     for (int e = 0; mine && e < n_steps; ++e) {
@@ -429,13 +448,14 @@ __global__ void __launch_bounds__(THREADS, 1)
         float* dst = p.lw + (long long)bh * p.pieces_cap * p.rows_cap + row;
         if (per_step == 1) {
           if (sm.entry[0] >= 0) dst[(long long)sm.entry[0] * p.rows_cap] =
-              sum0 + sum1 == 0.f ? -INFINITY : log2f(sum0 + sum1) + (off - sm.ev[0]);
+              sum0 + sum1 == 0.f ? -INFINITY : __log2f(sum0 + sum1) + (off - sm.ev[0]);
         } else {
-          if (sm.entry[0] >= 0) dst[(long long)sm.entry[0] * p.rows_cap] = sum0 == 0.f ? -INFINITY : log2f(sum0) + (off - sm.ev[0]);
-          if (sm.entry[1] >= 0) dst[(long long)sm.entry[1] * p.rows_cap] = sum1 == 0.f ? -INFINITY : log2f(sum1) + (off - sm.ev[1]);
+          if (sm.entry[0] >= 0) dst[(long long)sm.entry[0] * p.rows_cap] = sum0 == 0.f ? -INFINITY : __log2f(sum0) + (off - sm.ev[0]);
+          if (sm.entry[1] >= 0) dst[(long long)sm.entry[1] * p.rows_cap] = sum1 == 0.f ? -INFINITY : __log2f(sum1) + (off - sm.ev[1]);
         }
       }
     }
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     // O / l, or this split's part of them
     const long long prow = ((long long)bh * p.splits + sp) * p.rows_pad + row;
     bool have = false;
@@ -445,7 +465,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
     if (mine) {
       const float inv = l == 0.f ? 0.f : 1.0f / l;
-      const int qh = h * p.group + row % p.group, i = row / p.group;
+      const int qh = h * p.group + row - tok * p.group;
       // rows go through the row tile's own shared memory, 2 D bytes of each at
       // a time, so that a warp writes whole rows: its bf16 row, or half of its
       // fp32 one
@@ -480,18 +500,22 @@ __global__ void __launch_bounds__(THREADS, 1)
           }
         }
         __syncwarp();
-#pragma unroll
-        for (int j = 0; j < 32; j += 32 / UNITS) {
-          const int r = j + lane / UNITS, u = lane % UNITS, gr = base + (warp / 4) * BM + (warp % 4) * 32 + r;
-          const uint4 v = *reinterpret_cast<const uint4*>(slot(r, u));
-          if (gr >= rows) continue;
-          if (passes == 2) {
-            const long long pr = ((long long)bh * p.splits + sp) * p.rows_pad + gr;
-            *reinterpret_cast<uint4*>(p.part_o + pr * D + ps * (D / 2) + u * 4) = v;
-          } else {
-            *reinterpret_cast<uint4*>(p.o + b * p.o_sb + (long long)(gr / p.group) * p.o_sn +
-                                      (long long)(h * p.group + gr % p.group) * p.o_sh + u * 8) = v;
+        static_assert(UNITS == LPR, "rows are written as Q was read");
+        RowStep at{tok0, gh0};
+#pragma unroll 4
+        for (int j = 0; j < ITERS; ++j) {
+          const int r = j * RPI + sub;
+          const uint4 v = *reinterpret_cast<const uint4*>(slot(r, c8));
+          if (wrow + r < rows) {
+            if (passes == 2) {
+              const long long pr = ((long long)bh * p.splits + sp) * p.rows_pad + wrow + r;
+              *reinterpret_cast<uint4*>(p.part_o + pr * D + ps * (D / 2) + c8 * 4) = v;
+            } else {
+              *reinterpret_cast<uint4*>(p.o + b * p.o_sb + (long long)at.tok * p.o_sn +
+                                        (long long)(h * p.group + at.gh) * p.o_sh + c8 * 8) = v;
+            }
           }
+          at.advance(RPI, p.group);
         }
         __syncwarp();
       }
@@ -500,7 +524,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           p.part_ml[prow] = make_float2(m, l);
         } else {
           const float l2 = l == 0.f ? -INFINITY : log2f(l) + (m == -INFINITY ? 0.f : m) - OFF;
-          if (p.lse) p.lse[((long long)b * p.heads + qh) * p.n_q + i] = l2 * LN2;
+          if (p.lse) p.lse[((long long)b * p.heads + qh) * p.n_q + tok] = l2 * LN2;
           if (p.lse2) p.lse2[(long long)bh * p.rows_cap + row] = l2;
         }
       }
