@@ -679,7 +679,11 @@ int veda_kv_advance(const veda_kv_cache* C, int32_t n, const int32_t* n_new, cud
 static int check_kv_heads(const veda::KvGeom& g, int heads, int n_q) {
   if (heads < 1 || heads > 4096 || heads % g.hkv)
     return fail(VEDA_ERR_INVALID_ARG, "heads=%d must be a multiple of heads_kv=%d in [1, 4096]", heads, g.hkv);
-  return check_rows(n_q, "n_q");
+  VEDA_TRY(check_rows(n_q, "n_q"));
+  const long long rows = (long long)n_q * (heads / g.hkv);
+  if (rows > 65535ll * 256)
+    return fail(VEDA_ERR_UNSUPPORTED, "n_q * heads / heads_kv = %lld exceeds %lld", rows, 65535ll * 256);
+  return VEDA_OK;
 }
 
 size_t veda_kv_attn_ws_bytes(const veda_kv_cache* C, int32_t heads, int32_t n_q, int32_t with_weight) {

@@ -129,9 +129,8 @@ __global__ void __launch_bounds__(THREADS, 1)
   __shared__ int sm_cnt[3];
   uint8_t* smem = smem_raw + (((smem_u32(smem_raw) + 1023u) & ~1023u) - smem_u32(smem_raw));
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
-  // under a causal mask the last row tiles have the most keys: they start first
-  const int mt = p.row_tiles - 1 - (int)(blockIdx.x / p.splits), sp = blockIdx.x % p.splits, h = blockIdx.y,
-            b = blockIdx.z;
+  // under a causal mask the last row tiles have the most keys: every head's start first
+  const int mt = p.row_tiles - 1 - (int)blockIdx.y, sp = blockIdx.x % p.splits, h = blockIdx.x / p.splits, b = blockIdx.z;
   int n_b, held, total;
   const int t0 = g.next_pos[b];
   if (!kv_counts(g, b, h, p.n_q, p.n_new, p.pending, n_b, held, total)) return;
@@ -548,7 +547,7 @@ cudaError_t launch(const KvGeom& g, const KvAttnParams& p, cudaStream_t s) {
   const cudaError_t e =
       cudaFuncSetAttribute(kv_attn_tiles_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, TileLayout<D>::ALLOC);
   if (e != cudaSuccess) return e;
-  kv_attn_tiles_kernel<D><<<dim3(p.row_tiles * p.splits, g.hkv, g.B), THREADS, TileLayout<D>::ALLOC, s>>>(g, p, maps);
+  kv_attn_tiles_kernel<D><<<dim3(g.hkv * p.splits, p.row_tiles, g.B), THREADS, TileLayout<D>::ALLOC, s>>>(g, p, maps);
   return cudaGetLastError();
 }
 

@@ -83,6 +83,7 @@ def test_attention_refusals():
     refused(attn(heads=4098), E, "heads=4098")
     refused(attn(n=-1), E, "n_q")
     refused(attn(n=1 << 23), V.VEDA_ERR_UNSUPPORTED, "n_q")
+    refused(attn(n=1 << 22, heads=30), V.VEDA_ERR_UNSUPPORTED, "exceeds")
     refused(attn(window=-1), E, "window")
     refused(attn(sinks=-1), E, "sinks")
     refused(attn(q=None), E, "q is NULL")
