@@ -566,10 +566,10 @@ __global__ void __launch_bounds__(128) kv_join_kernel(const KvGeom g, const KvAt
   if (r >= n_b * p.group) return;
   const int bh = b * g.hkv + h;
   const long long rows = p.rows_pad;
-  const float2* ml = p.part_ml + (long long)bh * p.splits * rows + r;
+  const float2* ml = p.part_ml + (long long)bh * p.parts * rows + r;
   // a lane per part (32 at most): its factor and its share of the sum
   float2 x = make_float2(-INFINITY, 0.f);
-  if (lane < p.splits) x = ml[lane * rows];
+  if (lane < p.parts) x = ml[lane * rows];
   float m = x.x;
 #pragma unroll
   for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
@@ -580,10 +580,10 @@ __global__ void __launch_bounds__(128) kv_join_kernel(const KvGeom g, const KvAt
 #pragma unroll
   for (int e = 0; e < D / 32; ++e) o[e] = 0.f;
 #pragma unroll 4
-  for (int s = 0; s < p.splits; ++s) {
+  for (int s = 0; s < p.parts; ++s) {
     const float fs = __shfl_sync(0xffffffffu, f, s);
     if (fs == 0.f) continue;  // a part without keys has written nothing else
-    const float* src = p.part_o + (((long long)bh * p.splits + s) * rows + r) * D + lane * (D / 32);
+    const float* src = p.part_o + (((long long)bh * p.parts + s) * rows + r) * D + lane * (D / 32);
     if constexpr (D == 128) {
       const float4 v = *reinterpret_cast<const float4*>(src);
       o[0] += v.x * fs;
@@ -711,17 +711,19 @@ size_t kv_attn_plan(const KvGeom& g, KvAttnParams& p, bool weights, uint8_t* ws)
   p.pieces_cap = g.nb_cap * (g.tile / p.piece);
   const long long ctas = (long long)g.B * g.hkv * p.row_tiles, keys = (long long)g.nb_cap * g.tile;
   p.splits = 1;
+  p.alt = 0;
   if (p.tiles) {
     // One CTA per SM: waves of CTAs, each as long as its steps and what begins
     // and ends it; what is split is written and read once more and joined.
     // Measured at d = 128: 2.1 us a step, 5 us a CTA, 8 us for the join.
     const long long see = p.window > 0 ? (long long)p.window + p.sinks + n_tok(p.tile_rows, p.group) + 2 * g.tile : keys;
-    const double steps = (double)((see < keys ? see : keys) + 127) / 128, t = 2.1 * g.d / 128;
+    p.alt = rows <= 128;
+    const double steps = (double)((see < keys ? see : keys) + 127) / 128, t = (p.alt ? 1.1 : 2.1) * g.d / 128;
     double best = 0;
-    for (int s = 1; s <= 32 && (s == 1 || steps >= 3 * s); ++s) {
+    for (int s = 1; s <= (p.alt ? 16 : 32) && (s == 1 || steps >= 3 * s); ++s) {
       const double waves = (double)((ctas * s + 147) / 148);
       const double us = waves * (ceil(steps / s) * t + 5) +
-                        (s > 1 ? 8 + (double)ctas * s * p.tile_rows * g.d * 8 / 4e6 : 0);
+                        (s > 1 ? 8 + (double)ctas * s * (p.alt ? 2 * rows : p.tile_rows) * g.d * 8 / 4e6 : 0);
       if (s == 1 || us < best) {
         best = us;
         p.splits = s;
@@ -739,9 +741,10 @@ size_t kv_attn_plan(const KvGeom& g, KvAttnParams& p, bool weights, uint8_t* ws)
     off += (bytes + 255) / 256 * 256;
     return at;
   };
-  const size_t prows = (size_t)g.B * g.hkv * p.splits * p.rows_pad;
+  p.parts = p.alt ? 2 * p.splits : p.splits;
+  const size_t prows = (size_t)g.B * g.hkv * p.parts * p.rows_pad;
   p.part_ml = reinterpret_cast<float2*>(take(prows * 8));
-  p.part_o = p.splits == 1 ? nullptr : reinterpret_cast<float*>(take(prows * g.d * 4));
+  p.part_o = p.parts == 1 ? nullptr : reinterpret_cast<float*>(take(prows * g.d * 4));
   p.lse2 = nullptr;
   p.lw = nullptr;
   if (weights) {
@@ -764,7 +767,7 @@ cudaError_t launch_kv_attn(const KvGeom& g, KvAttnParams p, void* ws, cudaStream
   if (!p.tiles) return g.d == 128 ? launch_rows<128>(g, p, s) : launch_rows<64>(g, p, s);
   cudaError_t e = launch_kv_attn_tiles(g, p, s);
   if (e != cudaSuccess) return e;
-  if (p.splits > 1) {
+  if (p.parts > 1) {
     const dim3 jg((p.rows_cap + 3) / 4, g.hkv, g.B);
     e = g.d == 128 ? launch_behind(kv_join_kernel<128>, jg, 128, s, g, p) : launch_behind(kv_join_kernel<64>, jg, 128, s, g, p);
   }

@@ -45,11 +45,12 @@ struct KvAttnParams {
   float decay;
   // workspace, and how the rows (n_q * group per K/V head) are cut
   int32_t tiles;       // 1: the tile kernel (256 rows per CTA), 0: the row kernel
-  int32_t splits, row_tiles, rows_cap, rows_pad, tile_rows;
+  int32_t alt;         // the tile kernel's B takes every second step of A's rows
+  int32_t splits, parts, row_tiles, rows_cap, rows_pad, tile_rows;  // parts: of a row, for the join
   int32_t piece, pieces_cap;  // keys per entry of lw, entries per head
-  float* part_o;   // [B, hkv, splits, rows_pad, d]
+  float* part_o;   // [B, hkv, parts, rows_pad, d]
   int32_t* arrive;
-  float2* part_ml; // [B, hkv, splits, rows_pad]: reference (log2) and sum
+  float2* part_ml; // [B, hkv, parts, rows_pad]: reference (log2) and sum
   float* lse2;     // [B, hkv, rows_cap] log2
   float* lw;       // [B, hkv, pieces_cap, rows_cap] log2 of a piece's sum
 };

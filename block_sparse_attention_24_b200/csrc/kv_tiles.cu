@@ -13,6 +13,9 @@
 //               that carries the V scale), V converted from e4m3 by two
 //               warps of their own; a second e4m3 part of P would cost the softmax
 //               warps, which bound the kernel, more than this costs those.
+// Where a head has no more rows than one tile (p.alt), B has the same rows as A
+// and takes every second step: two chains of softmax and MMAs per SM instead of
+// one, each a part of its own for the join.
 // The softmax reference is the first maximum and moves only where a step's sum
 // passes 2^15 (then P may no longer fit fp16).
 //
@@ -33,9 +36,9 @@ namespace {
 
 constexpr int BM = 128, BN = 128;
 constexpr int KST = 3, VST = 2, WST = 2;  // stages: K codes, V codes, V fp16
-// A description's slot is written again only after the softmax of the step
-// before step_done's.
-constexpr int MST = KST + 2;
+// A description's slot is written again only after step_done of four steps
+// later, whose S was issued behind the P of this step and of the row tile's next.
+constexpr int MST = KST + 4;
 constexpr int SDR = 4;                 // step-done barriers
 constexpr float OVERFLOW_SUM = 32768.f;
 constexpr int THREADS = 384, CONVERT_WARPS = 2;
@@ -129,15 +132,20 @@ __global__ void __launch_bounds__(THREADS, 1)
   __shared__ int sm_cnt[3];
   uint8_t* smem = smem_raw + (((smem_u32(smem_raw) + 1023u) & ~1023u) - smem_u32(smem_raw));
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
-  // under a causal mask the last row tiles have the most keys: every head's start first
-  const int mt = p.row_tiles - 1 - (int)blockIdx.y, sp = blockIdx.x % p.splits, h = blockIdx.x / p.splits, b = blockIdx.z;
+  // Under a causal mask the last row tiles have the most keys, so every head's
+  // start first (2,048-token prompt, 8 heads: 93 -> 77 us). Without one they are
+  // equal, and a head's row tiles run together, so that its K and V come from
+  // L2 (3,840 x 34,560, 24 heads: 1.70 against 1.64 ms the other way round).
+  const int sp = blockIdx.x % p.splits, rest = blockIdx.x / p.splits, b = blockIdx.z;
+  const int h = p.causal ? rest % g.hkv : rest / p.row_tiles;
+  const int mt = p.row_tiles - 1 - (p.causal ? rest / g.hkv : rest % p.row_tiles);
   int n_b, held, total;
   const int t0 = g.next_pos[b];
   if (!kv_counts(g, b, h, p.n_q, p.n_new, p.pending, n_b, held, total)) return;
   const int rows = n_b * p.group;
   const int base = mt * 2 * BM;
   if (base >= rows) return;
-  const bool has_b = base + BM < rows;
+  const bool alt = p.alt, has_b = base + BM < rows || alt;
   const int bh = b * g.hkv + h;
   const long long trow = (long long)bh * g.nb_cap;
   const int t_lo = t0 + base / p.group, t_hi = t0 + (min(rows, base + 2 * BM) - 1) / p.group;
@@ -145,7 +153,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   // Q, a row per D/8 lanes: a warp reads and later writes whole rows. Lane
   // group `sub` has rows sub, sub + RPI, ... of the warp's 32.
   constexpr int LPR = D / 8, RPI = 32 / LPR, ITERS = 32 / RPI;
-  const int rt = warp / 4, wrow = base + warp * 32, sub = lane / LPR, c8 = lane % LPR;
+  const int rt = warp / 4, wrow = base + (alt ? warp % 4 : warp) * 32, sub = lane / LPR, c8 = lane % LPR;
   int tok0 = 0, gh0 = 0;  // token and head of the group of row wrow + sub
   uint4 qw[ITERS];
   const bool mine = warp < 4 || (warp < 8 && has_b);
@@ -187,34 +195,34 @@ __global__ void __launch_bounds__(THREADS, 1)
   const int steps_all = (n_tiles + per_step - 1) / per_step;
   const int per = (steps_all + p.splits - 1) / p.splits;
   const int s_lo = min(steps_all, sp * per), n_steps = min(steps_all, s_lo + per) - s_lo;
-  if (n_steps == 0 && p.splits > 1) {  // nothing to add: the join skips this part
+  if (n_steps == 0 && p.parts > 1) {  // nothing to add: the join skips this part
     for (int r = base + tid; r < min(rows, base + 2 * BM); r += THREADS)
-      p.part_ml[((long long)bh * p.splits + sp) * p.rows_pad + r] = make_float2(-INFINITY, 0.f);
+      for (int x = 0; x <= alt; ++x)
+        p.part_ml[((long long)bh * p.parts + (alt ? 2 * sp + x : sp)) * p.rows_pad + r] = make_float2(-INFINITY, 0.f);
     return;
   }
 
   // Each role prepares its part before the one barrier: the first copies are
   // under way while Q is taken apart.
   StepFeed feed;
-  int fed = 0;  // steps whose copies were issued (the producer's)
-  auto produce = [&](int e) {
-    if ((e & 15) == 0) feed.load(g, trow, rg, total, s_lo, e, n_steps, lane);
-    const int st = e % KST, vt = e % VST;
-    int row0, row1;
-    feed.put(meta[e % MST], g, p, e, t_lo, t_hi, lane, row0, row1);
-    __syncwarp();
+  int fed = 0;             // steps whose K copies were issued (the producer's)
+  int v_row0 = 0, v_row1 = 0;  // pool rows of the step whose V comes next
+  auto load_half = [&](const CUtensorMap* map, uint64_t* bar, uint8_t* dst, int row0, int row1) {
     if (lane == 0) {
-      const uint32_t bytes = (row0 >= 0 ? Lay::CB / 2 : 0) + (row1 >= 0 ? Lay::CB / 2 : 0);
-      uint8_t* kd = smem + Lay::OFF_K + st * Lay::CB;
-      uint8_t* vd = smem + Lay::OFF_V + vt * Lay::CB;
-      mbar_expect_tx(k_full + st, bytes);
-      if (row0 >= 0) tma_load_2d(kd, &maps.k, k_full + st, 0, row0);
-      if (row1 >= 0) tma_load_2d(kd + Lay::CB / 2, &maps.k, k_full + st, 0, row1);
-      mbar_expect_tx(v_full + vt, bytes);
-      if (row0 >= 0) tma_load_2d(vd, &maps.v, v_full + vt, 0, row0);
-      if (row1 >= 0) tma_load_2d(vd + Lay::CB / 2, &maps.v, v_full + vt, 0, row1);
+      mbar_expect_tx(bar, (row0 >= 0 ? Lay::CB / 2 : 0) + (row1 >= 0 ? Lay::CB / 2 : 0));
+      if (row0 >= 0) tma_load_2d(dst, map, bar, 0, row0);
+      if (row1 >= 0) tma_load_2d(dst + Lay::CB / 2, map, bar, 0, row1);
     }
     __syncwarp();
+  };
+  auto produce_k = [&](int e, int& row0, int& row1) {
+    if ((e & 15) == 0) feed.load(g, trow, rg, total, s_lo, e, n_steps, lane);
+    feed.put(meta[e % MST], g, p, e, t_lo, t_hi, lane, row0, row1);
+    __syncwarp();
+    load_half(&maps.k, k_full + e % KST, smem + Lay::OFF_K + e % KST * Lay::CB, row0, row1);
+  };
+  auto produce_v = [&](int e, int row0, int row1) {
+    load_half(&maps.v, v_full + e % VST, smem + Lay::OFF_V + e % VST * Lay::CB, row0, row1);
   };
   uint8_t* own = smem + Lay::OFF_Q + rt * 2 * Lay::QB;  // the row tile's Q, and its O at the end
   float qs = 0.f;
@@ -226,7 +234,9 @@ __global__ void __launch_bounds__(THREADS, 1)
     if (lane == 0) *abort_flag = 0;
     fence_mbar_init();
     __syncwarp();
-    for (; fed < VST && fed < n_steps; ++fed) produce(fed);
+    // K runs a step ahead of V: V waits for the conversion of an earlier one
+    if (n_steps > 0) produce_k(0, v_row0, v_row1);
+    fed = 1;
   } else if (warp == 9) {
     tmem_alloc(tmem_slot, 512);
     tmem_relinquish();
@@ -262,16 +272,24 @@ __global__ void __launch_bounds__(THREADS, 1)
     regs_lower<REGS_ROLES>();
     if (warp == 8) {
       // --------------------------------------------------------- producer
-      int e = fed;
+      int e = 0;  // V copies issued; K is at fed
       for (; e < n_steps; ++e) {
-        // the description's slot is free: step_done(e - KST) follows the softmax of step e - KST - 1
-        bool ok = e < KST || mbar_wait(step_done + (e - KST) % SDR, ((e - KST) / SDR) & 1, abort_flag, g.dev_status);
-        ok = ok && mbar_wait(v_free + e % VST, (e / VST - 1) & 1, abort_flag, g.dev_status);
+        int row0 = -1, row1 = -1;
+        bool ok = true;
+        if (fed < n_steps) {
+          // the description's slot is free too, see MST
+          ok = fed < KST || mbar_wait(step_done + (fed - KST) % SDR, ((fed - KST) / SDR) & 1, abort_flag, g.dev_status);
+          if (!__all_sync(0xffffffffu, ok)) break;
+          produce_k(fed++, row0, row1);
+        }
+        ok = e < VST || mbar_wait(v_free + e % VST, (e / VST - 1) & 1, abort_flag, g.dev_status);
         if (!__all_sync(0xffffffffu, ok)) break;
-        produce(e);
+        produce_v(e, v_row0, v_row1);
+        v_row0 = row0;
+        v_row1 = row1;
       }
       if (*abort_flag && lane == 0) {  // let every copy that was started land
-        for (int x = max(0, e - KST); x < e; ++x) mbar_wait_drain(k_full + x % KST, (x / KST) & 1, VEDA_WAIT_LIMIT_NS);
+        for (int x = max(0, fed - KST); x < min(fed, n_steps); ++x) mbar_wait_drain(k_full + x % KST, (x / KST) & 1, VEDA_WAIT_LIMIT_NS);
         for (int x = max(0, e - VST); x < e; ++x) mbar_wait_drain(v_full + x % VST, (x / VST) & 1, VEDA_WAIT_LIMIT_NS);
       }
     } else if (warp == 9) {
@@ -284,17 +302,18 @@ __global__ void __launch_bounds__(THREADS, 1)
       const uint64_t dW = sdesc_sw128(smem_u32(smem + Lay::OFF_W), BN * 128, 1024);
       bool ok = true;
       const int tiles = has_b ? 2 : 1;
+      const int back = alt ? 2 : 1;  // a row tile's steps are so far apart
       auto issue_pv = [&](int r, int e) -> bool {  // P V of step e
         const int ws = e % WST;
-        if (!mbar_wait(p_full + r, e & 1, abort_flag, g.dev_status)) return false;
+        if (!mbar_wait(p_full + r, (alt ? e >> 1 : e) & 1, abort_flag, g.dev_status)) return false;
         if (!mbar_wait(w_full + ws, (e / WST) & 1, abort_flag, g.dev_status)) return false;
         tc_fence_after();
         const uint32_t o_addr = tmem + 2 * BN + r * BN, p_addr = tmem + r * BN + 64;
         const uint64_t d = dW + (uint64_t)(ws * (Lay::WB >> 4));
 #pragma unroll
         for (int kk = 0; kk < BN / 16; ++kk)
-          umma_bf16_ts(o_addr, p_addr + kk * 8, d + (uint64_t)(kk * (2048 >> 4)), idesc_o, (e > 0 || kk > 0) ? 1u : 0u);
-        if (e == n_steps - 1) umma_commit(pv_done + r);
+          umma_bf16_ts(o_addr, p_addr + kk * 8, d + (uint64_t)(kk * (2048 >> 4)), idesc_o, (e >= back || kk > 0) ? 1u : 0u);
+        if (e + back >= n_steps) umma_commit(pv_done + r);
         return true;
       };
       for (int e = 0; ok && e < n_steps; ++e) {
@@ -302,7 +321,8 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (!mbar_wait(k_full + st, (e / KST) & 1, abort_flag, g.dev_status)) break;
         tc_fence_after();
         for (int r = 0; r < tiles; ++r) {
-          if (e > 0 && !(ok = issue_pv(r, e - 1))) break;
+          if (alt && r != (e & 1)) continue;
+          if (e >= back && !(ok = issue_pv(r, e - back))) break;
           const uint64_t q = dQ + (uint64_t)(r * (2 * Lay::QB >> 4)), k = dK + (uint64_t)(st * (Lay::CB >> 4));
 #pragma unroll
           for (int part = 0; part < 2; ++part)
@@ -315,7 +335,11 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (!ok) break;
         umma_commit(step_done + e % SDR);
       }
-      for (int r = 0; r < tiles && ok && n_steps > 0 && !*abort_flag; ++r) ok = issue_pv(r, n_steps - 1);
+      // what is left: each row tile's last step
+      for (int r = 0; r < tiles && ok && !*abort_flag; ++r) {
+        const int e = alt ? n_steps - 1 - ((n_steps - 1 - r) & 1) : n_steps - 1;
+        if (e >= 0) ok = issue_pv(r, e);
+      }
       umma_commit(drain);
       mbar_wait_drain(drain, 0, VEDA_WAIT_LIMIT_NS);
       }
@@ -331,7 +355,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       bool ok = mbar_wait(v_full + vt, (e / VST) & 1, abort_flag, g.dev_status);
       // fp16 slot: P V of step e - WST has completed
       if (ok && e >= WST) {
-        const int sd = e - WST + 1;
+        const int sd = e - WST + (alt ? 2 : 1);
         ok = mbar_wait(step_done + sd % SDR, (sd / SDR) & 1, abort_flag, g.dev_status);
       }
       if (!__all_sync(0xffffffffu, ok)) break;
@@ -376,15 +400,22 @@ __global__ void __launch_bounds__(THREADS, 1)
   } else {
     regs_raise<REGS_SOFTMAX>();
     // ------------------------------------------------------------ softmax
-    const int row = base + tid;  // tid is 0..255 here
+    const int row = wrow + lane;
     const bool row_valid = row < rows;
     const int tok = row / p.group, t = t0 + tok;
     const uint32_t lane_addr = tmem + ((uint32_t)((warp % 4) * 32) << 16);
     const uint32_t s_col = rt * BN, o_col = 2 * BN + rt * BN;
     float m = -INFINITY, l = 0.f;
     bool ok = true;
-    for (int e = 0; mine && e < n_steps; ++e) {
-      if (!__all_sync(0xffffffffu, mbar_wait(s_full + rt, e & 1, abort_flag, g.dev_status))) { ok = false; break; }
+    const int first = alt ? rt : 0, stride = alt ? 2 : 1;
+    const int n_mine = mine ? (n_steps - first + stride - 1) / stride : 0;  // steps of this row tile
+    for (int j = 0; j < n_mine; ++j) {
+      const int e = first + j * stride;
+      if (!__all_sync(0xffffffffu, mbar_wait(s_full + rt, j & 1, abort_flag, g.dev_status))) { ok = false; break; }
+      if (wrow >= rows) {  // none of the warp's rows is one: its P may be anything
+        mbar_arrive(p_full + rt);
+        continue;
+      }
       tc_fence_after();
       const StepMeta& sm = meta[e % MST];
       float c0 = qs * sm.ks[0], c1 = qs * sm.ks[1], ev0 = sm.ev[0], ev1 = sm.ev[1];
@@ -456,9 +487,9 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     // O / l, or this split's part of them
-    const long long prow = ((long long)bh * p.splits + sp) * p.rows_pad + row;
+    const long long part = (long long)bh * p.parts + (alt ? 2 * sp + rt : sp), prow = part * p.rows_pad + row;
     bool have = false;
-    if (ok && mine && n_steps > 0) {
+    if (ok && n_mine > 0) {
       have = __all_sync(0xffffffffu, mbar_wait(pv_done + rt, 0, abort_flag, g.dev_status));
       tc_fence_after();
     }
@@ -471,7 +502,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       constexpr int UNITS = D / 8;  // 16-byte units per row and pass
       uint8_t* mem = own + (warp % 4) * 32 * 2 * D;
       auto slot = [&](int r, int u) { return mem + r * 2 * D + ((u ^ (r & (UNITS - 1))) << 4); };
-      const int passes = p.splits > 1 ? 2 : 1;
+      const int passes = p.parts > 1 ? 2 : 1;
       for (int ps = 0; ps < passes; ++ps) {
         const int cols = D / passes;
         for (int c = 0; c < cols; c += 32) {
@@ -507,7 +538,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           const uint4 v = *reinterpret_cast<const uint4*>(slot(r, c8));
           if (wrow + r < rows) {
             if (passes == 2) {
-              const long long pr = ((long long)bh * p.splits + sp) * p.rows_pad + wrow + r;
+              const long long pr = part * p.rows_pad + wrow + r;
               *reinterpret_cast<uint4*>(p.part_o + pr * D + ps * (D / 2) + c8 * 4) = v;
             } else {
               *reinterpret_cast<uint4*>(p.o + b * p.o_sb + (long long)at.tok * p.o_sn +
@@ -519,7 +550,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         __syncwarp();
       }
       if (row_valid) {
-        if (p.splits > 1) {
+        if (p.parts > 1) {
           p.part_ml[prow] = make_float2(m, l);
         } else {
           const float l2 = l == 0.f ? -INFINITY : log2f(l) + (m == -INFINITY ? 0.f : m) - OFF;
@@ -547,7 +578,7 @@ cudaError_t launch(const KvGeom& g, const KvAttnParams& p, cudaStream_t s) {
   const cudaError_t e =
       cudaFuncSetAttribute(kv_attn_tiles_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, TileLayout<D>::ALLOC);
   if (e != cudaSuccess) return e;
-  kv_attn_tiles_kernel<D><<<dim3(g.hkv * p.splits, p.row_tiles, g.B), THREADS, TileLayout<D>::ALLOC, s>>>(g, p, maps);
+  kv_attn_tiles_kernel<D><<<dim3(g.hkv * p.splits * p.row_tiles, 1, g.B), THREADS, TileLayout<D>::ALLOC, s>>>(g, p, maps);
   return cudaGetLastError();
 }
 
