@@ -1,0 +1,81 @@
+"""One attention layer over a stream: tokens or chunks of video arrive, attend
+to what the 8-bit K/V tile cache holds and to themselves, and join it.
+
+    append (K, V) -> attention -> [advance -> evict]
+
+The last two only where a chunk is final: while it is being denoised, step()
+with commit=False replaces the chunk's pending keys and values each time.
+Only marshalling and buffer management live here; every step is a libveda
+kernel.
+"""
+from __future__ import annotations
+
+import math
+from typing import List, Optional
+
+import torch
+
+from . import (KVCache, veda_kv_advance, veda_kv_append, veda_kv_attn, veda_kv_attn_ws_bytes, veda_kv_check_status,
+               veda_kv_evict)
+
+
+class VedaStream:
+    """heads query heads over heads_kv K/V heads of a cache of max_tokens per
+    sequence. `causal`, `window` and `sinks` as in veda_kv_attn. `keep` (tiles,
+    one number or one per K/V head): a head that holds more after a committed
+    step drops the least attended ones, all but its first `sink_tiles` and
+    last `recent_tiles`; None: nothing is dropped. Attention weights are summed
+    over committed steps, those before with a factor `decay` for every step."""
+
+    def __init__(self, B: int, heads: int, heads_kv: int, d: int, tile: int, max_tokens: int, device,
+                 causal: bool = True, window: int = 0, sinks: int = 0, keep=None, sink_tiles: int = 1,
+                 recent_tiles: int = 1, decay: float = 1.0, scale: Optional[float] = None):
+        self.cache = KVCache(B, heads_kv, d, tile, -(-max_tokens // tile), device)
+        self.heads = heads
+        self.causal, self.window, self.sinks = causal, window, sinks
+        self.scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
+        self.keep: Optional[List[int]] = None
+        if keep is not None:
+            self.keep = [int(keep)] * heads_kv if isinstance(keep, int) else [int(k) for k in keep]
+        self.sink_tiles, self.recent_tiles, self.decay = sink_tiles, recent_tiles, decay
+        self._ws = {}
+
+    def workspace(self, n: int, weight: bool) -> torch.Tensor:
+        """Scratch of a step of n tokens, allocated at the first one."""
+        key = (n, weight)
+        if key not in self._ws:
+            size = veda_kv_attn_ws_bytes(self.cache, self.heads, n, weight)
+            if size == 0:
+                raise ValueError(f"a step of {n} tokens and {self.heads} heads is outside the library's limits")
+            self._ws[key] = torch.empty(size, dtype=torch.uint8, device=self.cache.device)
+        return self._ws[key]
+
+    def step(self, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, n_new: Optional[torch.Tensor] = None,
+             commit: bool = True, out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None, stream=None):
+        """q [B, n, heads, d], k, v [B, n, heads_kv, d] bf16; n_new [B] int32:
+        the real rows of each sequence (None: all). Returns the output, like q
+        (rows that are not real are not written)."""
+        n = q.shape[1]
+        if out is None:
+            out = torch.empty_like(q, memory_format=torch.contiguous_format)
+        if n == 0:
+            return out
+        c = self.cache
+        weigh = commit and self.keep is not None
+        veda_kv_append(c, k, v, n_new=n_new, stream=stream)
+        veda_kv_attn(c, q, out, self.scale, self.workspace(n, weigh), causal=self.causal, window=self.window,
+                     sinks=self.sinks, n_new=n_new, lse=lse, weight=c.weight if weigh else None, decay=self.decay,
+                     stream=stream)
+        if commit:
+            veda_kv_advance(c, n, n_new=n_new, stream=stream)
+            if self.keep is not None:
+                veda_kv_evict(c, self.keep, self.sink_tiles, self.recent_tiles, stream=stream)
+        return out
+
+    def reset(self):
+        """Empty the cache (its next tokens are at position 0 again)."""
+        self.cache.len.zero_()
+        self.cache.next_pos.zero_()
+
+    def check_status(self, stream=None):
+        veda_kv_check_status(self.cache, stream=stream)

@@ -603,3 +603,40 @@ def test_steps_on_two_streams_at_once():
     torch.cuda.synchronize()
     for j in (0, 1):
         assert torch.equal(outs[j], outs[2 + j]) and torch.equal(caches[j].weight, caches[2 + j].weight)
+
+
+def test_stream_layer_denoises_commits_and_evicts():
+    """VedaStream: a chunk's keys are replaced while it is denoised and join
+    the cache when it is committed; the heads are cut to their tiles."""
+    from block_sparse_attention_24_b200.stream import VedaStream
+    B, heads, hkv, d, tile, n = 1, 4, 2, 64, 64, 96
+    layer = VedaStream(B, heads, hkv, d, tile, 640, DEV, causal=False, window=400, sinks=64, keep=[4, 5], decay=0.9)
+    c = layer.cache
+    for chunk in range(7):
+        for t in range(3):
+            k, v = bf16(800 + 10 * chunk + t, B, n, hkv, d), bf16(900 + 10 * chunk + t, B, n, hkv, d)
+            q = bf16(1000 + 10 * chunk + t, B, n, heads, d)
+            want = oracle_of(c)
+            want.append(host(k), host(v), [n])
+            o, lse, w, wrote, A, S, R, Q = want.attend(host(q), [n], d ** -0.5, False, 400, 64)
+            got = layer.step(q, k, v, commit=t == 2)
+            layer.check_status()
+            D = (2.0 ** -16 * (1 + S) + 2.0 ** -17 * Q).transpose(0, 2, 1)[..., None]
+            tol = (2.0 ** -11 + 4 * D) * A + 2.0 ** -8 * np.abs(o) + 640 * 2.0 ** -32 * 448 * R.transpose(0, 2, 1)[..., None]
+            assert (np.abs(host(got) - o) <= tol).all()
+            if t < 2:
+                assert_same_state(c, want)
+        want.weight = np.where(wrote, 0.9 * want.weight + w, want.weight)
+        held = host(c.weight)
+        want.advance(np.array([n]))
+        # the same tiles go by the kernel's weights, which differ by rounding
+        want.evict([4, 5], 1, 1)
+        np.testing.assert_array_equal(host(c.len), want.len)
+        np.testing.assert_array_equal(host(c.table), want.table)
+        np.testing.assert_allclose(held, want.weight, rtol=1e-3)
+        assert (host(c.len) <= np.array([4, 5]) * tile).all()
+    assert int(c.next_pos[0]) == 7 * n
+    layer.reset()
+    assert int(c.len.sum()) == 0
+    with pytest.raises(ValueError, match="multiple|limits"):
+        VedaStream(1, 3, 2, 64, 64, 128, DEV).workspace(1, False)
