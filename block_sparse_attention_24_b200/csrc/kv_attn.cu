@@ -443,6 +443,10 @@ __global__ void __launch_bounds__((RowsCfg<D, RP>::THREADS), 2)
       o[r] = fmaf(fmaf(fmaf(__uint_as_float(u[3 * R + r]), 0.0625f, __uint_as_float(u[2 * R + r])), 0.0625f,
                        __uint_as_float(u[R + r])), 0.0625f, __uint_as_float(u[r]));
     }
+    // the rows' tokens, worked out before the wait for the other parts
+    int tok[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) tok[r] = (r0 + r) / p.group;
     bool last = true;
     if (parts > 1) {
       const long long row0 = ((long long)bh * p.splits + sp) * p.rows_pad + r0;
@@ -465,16 +469,29 @@ __global__ void __launch_bounds__((RowsCfg<D, RP>::THREADS), 2)
         const float2* ml = p.part_ml + (long long)bh * p.splits * p.rows_pad;
         const float* po = p.part_o + ((long long)bh * p.splits * p.rows_pad + r0) * D + key;
         float* fac = reinterpret_cast<float*>(smem);  // [parts][RP], in the ring
+        // parts whose O is in flight, the first of them beside the factors (as registers allow)
+        constexpr int AHEAD = RP == 4 ? 8 : 16 / R;
+        float v[AHEAD][R];
+        auto fetch = [&](int s0) {
+#pragma unroll
+          for (int u = 0; u < AHEAD; ++u)
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+              v[u][r] = s0 + u < parts && r0 + r < rows && key < D ? __ldcg(po + ((long long)(s0 + u) * p.rows_pad + r) * D) : 0.f;
+        };
+        fetch(0);
         for (int r = warp; r < rows; r += SM / 32) {
-          float mx = -INFINITY, ls = 0.f;
-          for (int s = lane; s < parts; s += 32) mx = fmaxf(mx, __ldcg(&ml[(long long)s * p.rows_pad + r].x));
+          const float2 none = make_float2(-INFINITY, 0.f);
+          const float2 x0 = lane < parts ? __ldcg(&ml[(long long)lane * p.rows_pad + r]) : none;
+          float mx = x0.x, ls = 0.f;
+          for (int s = lane + 32; s < parts; s += 32) mx = fmaxf(mx, __ldcg(&ml[(long long)s * p.rows_pad + r].x));
 #pragma unroll
           for (int d = 16; d; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
           for (int s = lane; s < parts; s += 32) {
-            const float2 v = __ldcg(&ml[(long long)s * p.rows_pad + r]);
-            const float f = v.x == -INFINITY ? (v.y == v.y ? 0.f : 1.f) : fast_exp2(v.x - mx);
+            const float2 x = s == lane ? x0 : __ldcg(&ml[(long long)s * p.rows_pad + r]);
+            const float f = x.x == -INFINITY ? (x.y == x.y ? 0.f : 1.f) : fast_exp2(x.x - mx);
             fac[s * RP + r] = f;
-            ls += v.y * f;
+            ls += x.y * f;
           }
 #pragma unroll
           for (int d = 16; d; d >>= 1) ls += __shfl_xor_sync(0xffffffffu, ls, d);
@@ -490,14 +507,14 @@ __global__ void __launch_bounds__((RowsCfg<D, RP>::THREADS), 2)
           l[r] = red[RP + r0 + r];
           o[r] = 0.f;
         }
-        if (key < D)
-          for (int s = 0; s < parts; ++s) {
-            float v[R];
+        for (int s0 = 0; s0 < parts; s0 += AHEAD) {
 #pragma unroll
-            for (int r = 0; r < R; ++r) v[r] = r0 + r < rows ? __ldcg(po + ((long long)s * p.rows_pad + r) * D) : 0.f;
+          for (int u = 0; u < AHEAD; ++u)
+            if (s0 + u < parts)
 #pragma unroll
-            for (int r = 0; r < R; ++r) o[r] = fmaf(v[r], r0 + r < rows ? fac[s * RP + r0 + r] : 0.f, o[r]);
-          }
+              for (int r = 0; r < R; ++r) o[r] = fmaf(v[u][r], r0 + r < rows ? fac[(s0 + u) * RP + r0 + r] : 0.f, o[r]);
+          if (s0 + AHEAD < parts) fetch(s0 + AHEAD);
+        }
       }
     }
     if (last) {
@@ -506,13 +523,13 @@ __global__ void __launch_bounds__((RowsCfg<D, RP>::THREADS), 2)
         const int row = r0 + r;
         if (row >= rows) break;
         const bool none = l[r] == 0.f;
-        const int i = row / p.group, qh = h * p.group + row % p.group;
+        const int qh = h * p.group + row - tok[r] * p.group;
         if (key < D)
-          p.o[b * p.o_sb + (long long)i * p.o_sn + (long long)qh * p.o_sh + key] =
+          p.o[b * p.o_sb + (long long)tok[r] * p.o_sn + (long long)qh * p.o_sh + key] =
               __float2bfloat16(none ? 0.f : o[r] / l[r]);
         if (key == r) {
           const float l2 = none ? -INFINITY : log2f(l[r]) + (m[r] == -INFINITY ? 0.f : m[r]) - OFF;
-          if (p.lse) p.lse[((long long)b * p.heads + qh) * p.n_q + i] = l2 * LN2;
+          if (p.lse) p.lse[((long long)b * p.heads + qh) * p.n_q + tok[r]] = l2 * LN2;
           qs[row] = l2;
         }
       }
@@ -520,25 +537,34 @@ __global__ void __launch_bounds__((RowsCfg<D, RP>::THREADS), 2)
         softmax_sync<SM>();
         // a thread per piece, those of a tile side by side
         const int ppt = g.tile / 32, pieces = nb * ppt;
-        for (int base = 0; base < pieces; base += SM) {
-          const int pc = base + tid, i = pc / ppt;
-          float w = 0.f;
-          if (pc < pieces && pc * 32 < total &&
-              kv_tile_seen(g.pos[trow + i], g.tile, t_lo, t_hi, p.causal, p.window, p.sinks)) {
+        for (int base = 0; base < pieces; base += 2 * SM) {
+          float v[2][RP], was[2];
+          int ps[2];
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            const int pc = base + u * SM + tid;
+            const bool in = pc < pieces;
+            ps[u] = in ? g.pos[trow + pc / ppt] : 0;
+            was[u] = in && p.decay != 0.f ? p.weight[trow + pc / ppt] : 0.f;
             const float* lw = p.lw + ((long long)bh * p.pieces_cap + pc) * p.rows_cap;
-            float v[RP];
 #pragma unroll
-            for (int r = 0; r < RP; ++r) v[r] = r < rows ? __ldcg(lw + r) : -INFINITY;
-#pragma unroll
-            for (int r = 0; r < RP; ++r) {
-              const float z = r < rows ? qs[r] : 0.f;
-              // none of it seen: nothing, even of a row that is NaN
-              if (v[r] != -INFINITY && z != -INFINITY) w += fast_exp2(v[r] - z);
-            }
+            for (int r = 0; r < RP; ++r) v[u][r] = in && pc * 32 < total && r < rows ? __ldcg(lw + r) : -INFINITY;
           }
-          for (int d = 1; d < ppt; d <<= 1) w += __shfl_xor_sync(0xffffffffu, w, d);
-          if (pc < pieces && pc % ppt == 0)
-            p.weight[trow + i] = p.decay == 0.f ? w : p.decay * p.weight[trow + i] + w;
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            const int pc = base + u * SM + tid;
+            float w = 0.f;
+            if (kv_tile_seen(ps[u], g.tile, t_lo, t_hi, p.causal, p.window, p.sinks)) {
+#pragma unroll
+              for (int r = 0; r < RP; ++r) {
+                const float z = r < rows ? qs[r] : 0.f;
+                // none of it seen: nothing, even of a row that is NaN
+                if (v[u][r] != -INFINITY && z != -INFINITY) w += fast_exp2(v[u][r] - z);
+              }
+            }
+            for (int d = 1; d < ppt; d <<= 1) w += __shfl_xor_sync(0xffffffffu, w, d);
+            if (pc < pieces && pc % ppt == 0) p.weight[trow + pc / ppt] = p.decay == 0.f ? w : p.decay * was[u] + w;
+          }
         }
       }
     }
