@@ -385,8 +385,8 @@ class KVCache:
             setattr(self, name, t)
         self.device = device
         self.n_slots = n_slots
-        self.status = torch.zeros(4, dtype=torch.int32, device=device)
-        self._arrive = torch.zeros((B, heads_kv), dtype=torch.int32, device=device)
+        words = torch.zeros(4 + B * heads_kv, dtype=torch.int32, device=device)
+        self.status, self._arrive = words[:4], words[4:]
         self._c = _KvCache(B, heads_kv, d, tile, n_slots, nb_cap,
                            *[getattr(self, n).data_ptr() for n in ("k8", "v8", "table", "pos", "k_scale", "v_scale",
                                                                    "weight", "len", "next_pos", "_arrive",
