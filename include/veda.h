@@ -427,6 +427,7 @@ int veda_kv_advance(const veda_kv_cache* C, int32_t n, const int32_t* n_new, cud
  *     order.
  * Tiles that no query sees are not read. q K^T is exact products summed in
  * fp32; P is rounded to fp16, the sums and O are fp32.
+ * o may be q itself.
  * ws: veda_kv_attn_ws_bytes(C, heads, n_q, weight != NULL) bytes of device
  * scratch, not shared by calls that may run at the same time. */
 size_t veda_kv_attn_ws_bytes(const veda_kv_cache* C, int32_t heads, int32_t n_q, int32_t with_weight);

@@ -354,6 +354,58 @@ def test_tile_scales_far_apart(n):
     check_attention(c, bf16(63, 1, n, 4, 64, size=3.0))
 
 
+@pytest.mark.parametrize("n", [1, 8, 40, 150])
+def test_scales_that_are_no_powers_of_two(n):
+    """Any positive scale reads right: log2 of a V scale and its inverse are
+    then rounded, by 2^-22 each relative to 1 + |log2|, which D (2^-16) holds."""
+    c = random_cache(65, 2, 2, 64, 128, 4, [300 + n, 100 + n])
+    c.len.sub_(n)
+    c.next_pos.sub_(n)
+    g = torch.Generator().manual_seed(66)
+    for t in (c.k_scale, c.v_scale):
+        t.copy_(torch.rand(t.shape, generator=g) * 0.01 + 1e-4)
+    check_attention(c, bf16(67, 2, n, 4, 64))
+
+
+@pytest.mark.parametrize("n", [1, 20, 300])
+@pytest.mark.parametrize("scale", [0.0, -0.3, 1e-30])
+def test_any_softmax_scale(n, scale):
+    c = random_cache(68, 1, 2, 64, 64, 10, [300 + n])
+    c.len.sub_(n)
+    c.next_pos.sub_(n)
+    check_attention(c, bf16(69, 1, n, 4, 64), scale=scale)
+    check_attention(c, torch.zeros((1, n, 4, 64), dtype=torch.bfloat16, device=DEV), window=100, sinks=5, scale=scale)
+
+
+@pytest.mark.parametrize("n", [2, 40, 140])
+def test_padded_queries_over_a_cache_without_pending_tokens(n):
+    c = random_cache(73, 3, 2, 64, 64, 6, [300, 70, 0])
+    check_attention(c, bf16(74, 3, n, 4, 64), news=[n - 1, 0, n], pending=False)
+    check_attention(c, bf16(75, 3, n, 4, 64), news=[0, 0, 0], pending=False)
+
+
+def test_output_may_be_the_query_itself():
+    for n in (1, 30, 200, 700):
+        c = random_cache(76, 2, 2, 64, 64, 20, [500 + n, 300 + n])
+        c.len.sub_(n)
+        c.next_pos.sub_(n)
+        q = bf16(77, 2, n, 6, 64)
+        o = torch.empty_like(q)
+        V.veda_kv_attn(c, q, o, 0.125, workspace(c, 6, n, False))
+        V.veda_kv_attn(c, q, q, 0.125, workspace(c, 6, n, False))
+        assert torch.equal(q, o)
+
+
+@pytest.mark.parametrize("B,hkv", [(40, 8), (3, 1), (1, 100)])
+def test_more_and_fewer_heads_than_the_device_has_room_for(B, hkv):
+    """One part per head, many parts per head."""
+    lens = [(b * 37) % 400 for b in range(B)]
+    c = random_cache(78, B, hkv, 64, 64, 7, [x + 1 for x in lens])
+    c.len.sub_(1)
+    c.next_pos.sub_(1)
+    check_attention(c, bf16(79, B, 1, hkv, 64))
+
+
 @pytest.mark.parametrize("size", [2.0 ** -100, 2.0 ** -30, 2.0 ** 30, 2.0 ** 100])
 @pytest.mark.parametrize("n", [1, 150])
 def test_query_magnitudes_beyond_fp16(size, n):
