@@ -41,6 +41,11 @@ namespace {
 //                    softmax thread)
 // The CTAs that share a head's keys count themselves in `arrive`; the last one
 // joins their parts, and sums the tile weights.
+// Measured: 2 sequences x 24 heads x 80,640 keys, d = 128: 156 us, 6.35 TB/s (97%
+// of a measured copy); 16 sequences of up to 8,190 keys, 32/8 heads, with
+// weights: 47 us, 4.3 TB/s; 1,500 keys, 32/8 heads: 10.3 us, a chain of latencies.
+// Up to 16 rows: at 32 rows and 16 x 8,190 keys two passes of this kernel would
+// take 170 us, the tile kernel takes 109.
 constexpr int FEW_ROWS = 16;
 constexpr float MARGIN = 1.5f;  // P <= 2^(OFF + MARGIN) = 362 < 448
 
