@@ -61,7 +61,8 @@ struct RowsCfg {
   static constexpr int OFF_META = OFF_P + 2 * N * STEP;
   static constexpr int OFF_BAR = OFF_META + ST * (int)sizeof(StepMeta);
   static constexpr int NUM_BARS = 3 * ST + 5;                   // K, V, free per stage; S, P twice; drain
-  static constexpr int OFF_RED = OFF_BAR + NUM_BARS * 8;        // float [4][RP], then [RP] factors, int [2][RP] position bounds
+  // float [4][RP], then [RP] factors, int [2][RP] position bounds
+  static constexpr int OFF_RED = OFF_BAR + NUM_BARS * 8;
   static constexpr int OFF_MISC = OFF_RED + 7 * RP * 4;
   static constexpr int ALLOC = OFF_MISC + 32 + 1024;
   static constexpr int TMEM = 4 * N;                            // S^T twice, O^T
@@ -340,7 +341,8 @@ __global__ void __launch_bounds__((RowsCfg<D, RP>::THREADS), 2)
         over |= x[r] > m[r] + MARGIN;
       }
       if (softmax_any<SM>(over)) {
-        if (*abort_flag) {
+        // given up by all threads or by none: the barriers below count them all
+        if (softmax_any<SM>(!ok)) {
           ok = false;
           break;
         }
@@ -421,8 +423,8 @@ __global__ void __launch_bounds__((RowsCfg<D, RP>::THREADS), 2)
       }
     }
     if (n_steps > 0)  // the last P V (and with it all before), or after an abort whatever was issued
-      ok = mbar_wait(free_ + (n_steps - 1) % ST, ((n_steps - 1) / ST) & 1, abort_flag, g.dev_status) && ok;
-    __syncwarp();
+      ok = __all_sync(0xffffffffu,
+                      mbar_wait(free_ + (n_steps - 1) % ST, ((n_steps - 1) / ST) & 1, abort_flag, g.dev_status) && ok);
     tc_fence_after();
     // row sums over the keys
 #pragma unroll
@@ -482,7 +484,9 @@ __global__ void __launch_bounds__((RowsCfg<D, RP>::THREADS), 2)
           for (int u = 0; u < AHEAD; ++u)
 #pragma unroll
             for (int r = 0; r < R; ++r)
-              v[u][r] = s0 + u < parts && r0 + r < rows && key < D ? __ldcg(po + ((long long)(s0 + u) * p.rows_pad + r) * D) : 0.f;
+              v[u][r] = s0 + u < parts && r0 + r < rows && key < D
+                            ? __ldcg(po + ((long long)(s0 + u) * p.rows_pad + r) * D)
+                            : 0.f;
         };
         fetch(0);
         for (int r = warp; r < rows; r += SM / 32) {
@@ -800,7 +804,7 @@ cudaError_t launch_kv_attn(const KvGeom& g, KvAttnParams p, void* ws, cudaStream
   if (e != cudaSuccess) return e;
   if (p.parts > 1) {
     const dim3 jg((p.rows_cap + 3) / 4, g.hkv, g.B);
-    e = g.d == 128 ? launch_behind(kv_join_kernel<128>, jg, 128, s, g, p) : launch_behind(kv_join_kernel<64>, jg, 128, s, g, p);
+    e = launch_behind(g.d == 128 ? kv_join_kernel<128> : kv_join_kernel<64>, jg, 128, s, g, p);
   }
   if (e != cudaSuccess || !p.weight) return e;
   return launch_behind(kv_weight_kernel, dim3(g.nb_cap, g.hkv, g.B), WEIGHT_THREADS, s, g, p);

@@ -80,12 +80,6 @@ __device__ __forceinline__ bool kv_tile_seen(int p, int tile, int t_lo, int t_hi
   return window <= 0 || p < sinks || (long long)p + tile - 1 > (long long)t_lo - window;
 }
 
-// Whether the query at position t sees the token at position p.
-__device__ __forceinline__ bool kv_seen(int p, int t, int causal, int window, int sinks) {
-  if (causal && p > t) return false;
-  return window <= 0 || p < sinks || (long long)p > (long long)t - window;
-}
-
 // A pool as a 2D map of bytes [rows, d], box [box_rows, d], swizzled over d bytes (64 or 128).
 CUresult encode_tensor_map_2d_u8(CUtensorMap* map, const void* base, uint64_t d, uint64_t rows, uint32_t box_rows);
 

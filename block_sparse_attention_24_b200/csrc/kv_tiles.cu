@@ -30,8 +30,6 @@
 // Measured: 3,840 x 34,560, 24 heads, d = 128: 1.68 ms, 970 TFLOP/s (a step of 256
 // rows x 128 keys takes ~3,680 clocks against 2,048 of MMA; the clock is held at
 // ~1.7 GHz by power); 2,048-token causal prompt, 32/8 heads: 75 us.
-#include <type_traits>
-
 #include "kv_attn.cuh"
 
 namespace veda {
@@ -292,8 +290,10 @@ __global__ void __launch_bounds__(THREADS, 1)
         v_row1 = row1;
       }
       if (*abort_flag && lane == 0) {  // let every copy that was started land
-        for (int x = max(0, fed - KST); x < min(fed, n_steps); ++x) mbar_wait_drain(k_full + x % KST, (x / KST) & 1, VEDA_WAIT_LIMIT_NS);
-        for (int x = max(0, e - VST); x < e; ++x) mbar_wait_drain(v_full + x % VST, (x / VST) & 1, VEDA_WAIT_LIMIT_NS);
+        for (int x = max(0, fed - KST); x < min(fed, n_steps); ++x)
+          mbar_wait_drain(k_full + x % KST, (x / KST) & 1, VEDA_WAIT_LIMIT_NS);
+        for (int x = max(0, e - VST); x < e; ++x)
+          mbar_wait_drain(v_full + x % VST, (x / VST) & 1, VEDA_WAIT_LIMIT_NS);
       }
     } else if (warp == 9) {
       if (lane == 0) {
@@ -477,14 +477,18 @@ __global__ void __launch_bounds__(THREADS, 1)
       mbar_arrive(p_full + rt);
       l += (sum0 == 0.f ? 0.f : sum0 * sm.rv[0]) + (sum1 == 0.f ? 0.f : sum1 * sm.rv[1]);
       if (p.lw && row_valid) {
+        // a tile of 128 is the whole step, of 64 half of it
         const float off = (m == -INFINITY ? 0.f : m) - OFF;
         float* dst = p.lw + (long long)bh * p.pieces_cap * p.rows_cap + row;
+        auto put = [&](int x, float sum) {
+          if (sm.entry[x] >= 0)
+            dst[(long long)sm.entry[x] * p.rows_cap] = sum == 0.f ? -INFINITY : __log2f(sum) + (off - sm.ev[x]);
+        };
         if (per_step == 1) {
-          if (sm.entry[0] >= 0) dst[(long long)sm.entry[0] * p.rows_cap] =
-              sum0 + sum1 == 0.f ? -INFINITY : __log2f(sum0 + sum1) + (off - sm.ev[0]);
+          put(0, sum0 + sum1);
         } else {
-          if (sm.entry[0] >= 0) dst[(long long)sm.entry[0] * p.rows_cap] = sum0 == 0.f ? -INFINITY : __log2f(sum0) + (off - sm.ev[0]);
-          if (sm.entry[1] >= 0) dst[(long long)sm.entry[1] * p.rows_cap] = sum1 == 0.f ? -INFINITY : __log2f(sum1) + (off - sm.ev[1]);
+          put(0, sum0);
+          put(1, sum1);
         }
       }
     }
@@ -519,7 +523,8 @@ __global__ void __launch_bounds__(THREADS, 1)
           if (passes == 2) {
 #pragma unroll
             for (int y = 0; y < 8; ++y)
-              *reinterpret_cast<uint4*>(slot(lane, c / 4 + y)) = make_uint4(u[4 * y], u[4 * y + 1], u[4 * y + 2], u[4 * y + 3]);
+              *reinterpret_cast<uint4*>(slot(lane, c / 4 + y)) =
+                  make_uint4(u[4 * y], u[4 * y + 1], u[4 * y + 2], u[4 * y + 3]);
           } else {
 #pragma unroll
             for (int y = 0; y < 4; ++y) {
