@@ -751,19 +751,28 @@ size_t kv_attn_plan(const KvGeom& g, KvAttnParams& p, bool weights, uint8_t* ws)
     // One CTA per SM: waves of CTAs, each as long as its steps and what begins
     // and ends it; what is split is written and read once more and joined.
     // Measured at d = 128: 2.1 us a step, 5 us a CTA, 8 us for the join.
-    const long long see = p.window > 0 ? (long long)p.window + p.sinks + n_tok(p.tile_rows, p.group) + 2 * g.tile : keys;
+    // The workspace is asked for without a window, so one only lowers the split:
+    // fewer steps alone could raise it, as the steps of a split are rounded up.
     p.alt = rows <= 128;
-    const double steps = (double)((see < keys ? see : keys) + 127) / 128, t = (p.alt ? 1.1 : 2.1) * g.d / 128;
-    double best = 0;
-    for (int s = 1; s <= (p.alt ? 16 : 32) && (s == 1 || steps >= 3 * s); ++s) {
-      const double waves = (double)((ctas * s + 147) / 148);
-      const double us = waves * (ceil(steps / s) * t + 5) +
-                        (s > 1 ? 8 + (double)ctas * s * (p.alt ? 2 * rows : p.tile_rows) * g.d * 8 / 4e6 : 0);
-      if (s == 1 || us < best) {
-        best = us;
-        p.splits = s;
+    const double t = (p.alt ? 1.1 : 2.1) * g.d / 128;
+    auto split = [&](long long see, int most) {
+      const double steps = (double)((see + 127) / 128);
+      double best = 0;
+      int at = 1;
+      for (int s = 1; s <= most && (s == 1 || steps >= 3 * s); ++s) {
+        const double waves = (double)((ctas * s + 147) / 148);
+        const double us = waves * (ceil(steps / s) * t + 5) +
+                          (s > 1 ? 8 + (double)ctas * s * (p.alt ? 2 * rows : p.tile_rows) * g.d * 8 / 4e6 : 0);
+        if (s == 1 || us < best) {
+          best = us;
+          at = s;
+        }
       }
-    }
+      return at;
+    };
+    p.splits = split(keys, p.alt ? 16 : 32);
+    const long long see = p.window > 0 ? (long long)p.window + p.sinks + n_tok(p.tile_rows, p.group) + 2 * g.tile : keys;
+    if (see < keys) p.splits = split(see, p.splits);
   } else {
     // two CTAs per SM, each with a step at least
     const long long want = 296 / ctas, most = (keys + STEP - 1) / STEP;

@@ -339,6 +339,27 @@ def test_long_cache_is_split(n):
     check_attention(c, bf16(51, 1, n, 4, 128, size=1.5))
 
 
+@pytest.mark.parametrize("B,hkv,d,tile,nb,n,window,sinks", [
+    (5, 4, 128, 64, 59, 125, 1829, 831),
+    (11, 1, 128, 64, 95, 188, 4332, 905),
+    (9, 1, 64, 128, 65, 64, 7012, 478),
+])
+def test_a_window_needs_no_more_workspace(B, hkv, d, tile, nb, n, window, sinks):
+    """The workspace is asked for without a window. These would be split into
+    more parts by the steps that their window leaves than by all of them."""
+    c = random_cache(52, B, hkv, d, tile, nb, [nb * tile - n - 7 * b for b in range(B)])
+    q, size = bf16(53, B, n, hkv, d), V.veda_kv_attn_ws_bytes(c, hkv, n, True)
+    buf = torch.full((size + (16 << 20),), 0xff, dtype=torch.uint8, device=DEV)
+    for pending in (True, False):      # what is pending holds NaN codes, what is held does not
+        o, w = torch.empty_like(q), c.weight.clone()
+        V.veda_kv_attn(c, q, o, d ** -0.5, buf[:size], window=window, sinks=sinks, pending=pending, weight=w, decay=0.5)
+        assert bool((buf[size:] == 0xff).all())
+        got, _ = check_attention(c, q, window=window, sinks=sinks, pending=pending)
+        assert torch.equal(o.view(torch.int16), got.view(torch.int16))
+        assert torch.equal(w.view(torch.int32), c.weight.view(torch.int32))
+    assert bool(torch.isfinite(got).all())
+
+
 @pytest.mark.parametrize("n", [1, 40, 300])
 def test_tile_scales_far_apart(n):
     """K scales that give one tile all the weight or none, V scales from one
