@@ -441,6 +441,14 @@ def _kv_call(cache: KVCache, stream, fn, *args):
         _check(rc)
 
 
+def _i32(x, name: str) -> int:
+    """x as the calls take it; ctypes would drop the bits above."""
+    x = int(x)
+    if not -2 ** 31 <= x < 2 ** 31:
+        raise ValueError(f"{name}={x} does not fit 32 bits")
+    return x
+
+
 def _n_new(cache: KVCache, n_new):
     if n_new is None:
         return None
@@ -464,11 +472,11 @@ def veda_kv_append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, n_new: Opti
 
 def veda_kv_advance(cache: KVCache, n: int, n_new: Optional[torch.Tensor] = None, stream=None):
     """Take the n (or n_new[b]) pending tokens in."""
-    _kv_call(cache, stream, _lib.veda_kv_advance, cache.ref, int(n), _n_new(cache, n_new))
+    _kv_call(cache, stream, _lib.veda_kv_advance, cache.ref, _i32(n, "n"), _n_new(cache, n_new))
 
 
 def veda_kv_attn_ws_bytes(cache: KVCache, heads: int, n_q: int, with_weight: bool = False) -> int:
-    return int(_lib.veda_kv_attn_ws_bytes(cache.ref, heads, n_q, int(with_weight)))
+    return int(_lib.veda_kv_attn_ws_bytes(cache.ref, _i32(heads, "heads"), _i32(n_q, "n_q"), int(with_weight)))
 
 
 def veda_kv_attn(cache: KVCache, q: torch.Tensor, o: torch.Tensor, scale: float, ws: torch.Tensor,
@@ -497,7 +505,7 @@ def veda_kv_attn(cache: KVCache, q: torch.Tensor, o: torch.Tensor, scale: float,
     if ws.numel() * ws.element_size() < need:
         raise ValueError(f"ws holds {ws.numel() * ws.element_size()} bytes, {need} are needed")
     _kv_call(cache, stream, _lib.veda_kv_attn, cache.ref, qp, qs, heads, n, _n_new(cache, n_new), bool(pending),
-             bool(causal), int(window), int(sinks), float(scale), op, os_, lp, wp, float(decay), ws.data_ptr())
+             bool(causal), _i32(window, "window"), _i32(sinks, "sinks"), float(scale), op, os_, lp, wp, float(decay), ws.data_ptr())
 
 
 def veda_kv_evict(cache: KVCache, keep: Sequence[int], sink: int, recent: int, out: Optional[KVCache] = None,
@@ -508,7 +516,8 @@ def veda_kv_evict(cache: KVCache, keep: Sequence[int], sink: int, recent: int, o
         raise ValueError(f"keep must have {cache.heads_kv} entries, not {len(keep)}")
     if out is not None and out.device != cache.device:
         raise ValueError(f"out is on {out.device}, the cache on {cache.device}")
-    _kv_call(cache, stream, _lib.veda_kv_evict, cache.ref, (ctypes.c_int32 * len(keep))(*keep), int(sink), int(recent),
+    keeps = (ctypes.c_int32 * len(keep))(*[_i32(k, "keep") for k in keep])
+    _kv_call(cache, stream, _lib.veda_kv_evict, cache.ref, keeps, _i32(sink, "sink"), _i32(recent, "recent"),
              None if out is None else out.ref)
 
 

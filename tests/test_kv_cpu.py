@@ -169,6 +169,19 @@ def test_binding_checks_tensors():
                   v8=torch.zeros((9, 64, 64), dtype=torch.uint8).view(torch.float8_e4m3fn))
 
 
+def test_binding_refuses_numbers_past_32_bits():
+    c = V.KVCache(1, 2, 64, 64, 4, "cpu")
+    q = torch.zeros((1, 1, 2, 64), dtype=torch.bfloat16)
+    ws = torch.empty(V.veda_kv_attn_ws_bytes(c, 2, 1), dtype=torch.uint8)
+    for call in (lambda x: V.veda_kv_advance(c, x), lambda x: V.veda_kv_attn_ws_bytes(c, 2 * x, 1),
+                 lambda x: V.veda_kv_attn_ws_bytes(c, 2, x), lambda x: V.veda_kv_attn(c, q, q.clone(), 1.0, ws, window=x),
+                 lambda x: V.veda_kv_attn(c, q, q.clone(), 1.0, ws, sinks=x), lambda x: V.veda_kv_evict(c, [4, x], 1, 1),
+                 lambda x: V.veda_kv_evict(c, [4, 4], x, 1), lambda x: V.veda_kv_evict(c, [4, 4], 1, x)):
+        for x in (2 ** 31, 2 ** 32 + 4, -2 ** 31 - 1):
+            with pytest.raises(ValueError, match="32 bits"):
+                call(x)
+
+
 # ------------------------------------------------------------------ oracle
 
 def test_oracle_codes_are_torchs():
