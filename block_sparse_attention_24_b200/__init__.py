@@ -345,7 +345,7 @@ class KVCache:
     next_pos [B] (int32). Those not given are allocated: an empty cache whose
     table names slot (b * heads_kv + h) * nb_cap + i for tile i. Tensors are
     used where they are (no copy) and are the caller's to look at and to
-    change between calls."""
+    change, in place, between calls."""
 
     _META = (("table", torch.int32), ("pos", torch.int32), ("k_scale", torch.float32), ("v_scale", torch.float32),
              ("weight", torch.float32))
@@ -392,6 +392,13 @@ class KVCache:
                                                                    "weight", "len", "next_pos", "_arrive",
                                                                    "status")])
         self.ref = ctypes.byref(self._c)
+
+    def __setattr__(self, name, value):
+        # the kernels have the tensors' addresses: another tensor would be
+        # ignored, and the one they use freed
+        if "ref" in self.__dict__:
+            raise AttributeError(f"KVCache.{name} cannot be given another value; change the tensor in place")
+        object.__setattr__(self, name, value)
 
 
 def _expect(t, name: str, shape, dtype, device, contiguous: bool = True):

@@ -182,6 +182,16 @@ def test_binding_refuses_numbers_past_32_bits():
                 call(x)
 
 
+def test_cache_tensors_cannot_be_replaced():
+    c = V.KVCache(1, 2, 64, 64, 4, "cpu")
+    held = c.len
+    for name in ("len", "table", "k8", "weight", "nb_cap"):
+        with pytest.raises(AttributeError, match="in place"):
+            setattr(c, name, torch.zeros_like(c.len))
+    c.len[0, 1] = 5
+    assert c.len is held and held.tolist() == [[0, 5]]
+
+
 # ------------------------------------------------------------------ oracle
 
 def test_oracle_codes_are_torchs():
