@@ -31,30 +31,47 @@ class VedaStream:
                  causal: bool = True, window: int = 0, sinks: int = 0, keep=None, sink_tiles: int = 1,
                  recent_tiles: int = 1, decay: float = 1.0, scale: Optional[float] = None):
         self.cache = KVCache(B, heads_kv, d, tile, -(-max_tokens // tile), device)
+        if heads < 1 or heads % heads_kv:
+            raise ValueError(f"heads={heads} must be a multiple of heads_kv={heads_kv}")
+        if window < 0 or sinks < 0:
+            raise ValueError(f"window={window} and sinks={sinks} must be >= 0")
         self.heads = heads
         self.causal, self.window, self.sinks = causal, window, sinks
         self.scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
         self.keep: Optional[List[int]] = None
         if keep is not None:
             self.keep = [int(keep)] * heads_kv if isinstance(keep, int) else [int(k) for k in keep]
+            # here, not behind a step's append and attention
+            if len(self.keep) != heads_kv:
+                raise ValueError(f"keep must have {heads_kv} entries, not {len(self.keep)}")
+            if sink_tiles < 0 or recent_tiles < 1 or min(self.keep) < sink_tiles + recent_tiles:
+                raise ValueError(f"keep={self.keep} must be at least sink_tiles={sink_tiles} (>= 0) + "
+                                 f"recent_tiles={recent_tiles} (>= 1)")
         self.sink_tiles, self.recent_tiles, self.decay = sink_tiles, recent_tiles, decay
         self._ws = {}
 
     def workspace(self, n: int, weight: bool) -> torch.Tensor:
-        """Scratch of a step of n tokens, allocated at the first one."""
-        key = (n, weight)
-        if key not in self._ws:
-            size = veda_kv_attn_ws_bytes(self.cache, self.heads, n, weight)
-            if size == 0:
-                raise ValueError(f"a step of {n} tokens and {self.heads} heads is outside the library's limits")
-            self._ws[key] = torch.empty(size, dtype=torch.uint8, device=self.cache.device)
-        return self._ws[key]
+        """Scratch of a step of n tokens, allocated at the first one. Sizes are
+        powers of two, so steps of many lengths share a few; none is freed, as a
+        captured step may use it."""
+        size = veda_kv_attn_ws_bytes(self.cache, self.heads, n, weight)
+        if size == 0:
+            raise ValueError(f"a step of {n} tokens and {self.heads} heads is outside the library's limits")
+        size = 1 << (size - 1).bit_length()
+        if size not in self._ws:
+            self._ws[size] = torch.empty(size, dtype=torch.uint8, device=self.cache.device)
+        return self._ws[size]
 
     def step(self, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, n_new: Optional[torch.Tensor] = None,
              commit: bool = True, out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None, stream=None):
         """q [B, n, heads, d], k, v [B, n, heads_kv, d] bf16; n_new [B] int32:
         the real rows of each sequence (None: all). Returns the output, like q
-        (rows that are not real are not written)."""
+        (rows that are not real are not written); allocated on `stream`, if
+        `out` is not given."""
+        if stream is not None:
+            # the step's tensors belong to the stream that uses them
+            with self._on(stream):
+                return self.step(q, k, v, n_new, commit, out, lse)
         n = q.shape[1]
         if out is None:
             out = torch.empty_like(q, memory_format=torch.contiguous_format)
@@ -62,20 +79,25 @@ class VedaStream:
             return out
         c = self.cache
         weigh = commit and self.keep is not None
-        veda_kv_append(c, k, v, n_new=n_new, stream=stream)
+        veda_kv_append(c, k, v, n_new=n_new)
         veda_kv_attn(c, q, out, self.scale, self.workspace(n, weigh), causal=self.causal, window=self.window,
-                     sinks=self.sinks, n_new=n_new, lse=lse, weight=c.weight if weigh else None, decay=self.decay,
-                     stream=stream)
+                     sinks=self.sinks, n_new=n_new, lse=lse, weight=c.weight if weigh else None, decay=self.decay)
         if commit:
-            veda_kv_advance(c, n, n_new=n_new, stream=stream)
+            veda_kv_advance(c, n, n_new=n_new)
             if self.keep is not None:
-                veda_kv_evict(c, self.keep, self.sink_tiles, self.recent_tiles, stream=stream)
+                veda_kv_evict(c, self.keep, self.sink_tiles, self.recent_tiles)
         return out
 
-    def reset(self):
+    def _on(self, stream):
+        if stream is not None and stream.device != self.cache.device:
+            raise ValueError(f"the stream is on {stream.device}, the cache on {self.cache.device}")
+        return torch.cuda.stream(stream)
+
+    def reset(self, stream=None):
         """Empty the cache (its next tokens are at position 0 again)."""
-        self.cache.len.zero_()
-        self.cache.next_pos.zero_()
+        with self._on(stream):
+            self.cache.len.zero_()
+            self.cache.next_pos.zero_()
 
     def check_status(self, stream=None):
         veda_kv_check_status(self.cache, stream=stream)

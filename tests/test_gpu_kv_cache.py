@@ -713,3 +713,28 @@ def test_stream_layer_denoises_commits_and_evicts():
     assert int(c.len.sum()) == 0
     with pytest.raises(ValueError, match="multiple|limits"):
         VedaStream(1, 3, 2, 64, 64, 128, DEV).workspace(1, False)
+
+
+def test_stream_layer_allocates_on_the_stream_of_the_step():
+    """Memory that the current stream has freed may still be in use there."""
+    from block_sparse_attention_24_b200.stream import VedaStream
+    n = 1 << 13
+    q, k, v = bf16(1100, 1, n, 2, 64), bf16(1101, 1, n, 2, 64), bf16(1102, 1, n, 2, 64)
+    layers = [VedaStream(1, 2, 2, 64, 64, n, DEV, keep=5) for _ in range(2)]
+    want = layers[0].step(q, k, v)
+    torch.cuda.synchronize()
+    freed = [torch.empty_like(q), torch.empty_like(layers[0].workspace(n, True))]
+    held = [t.data_ptr() for t in freed]
+    freed.clear()
+    s = torch.cuda.Stream()
+    got = layers[1].step(q, k, v, stream=s)
+    assert got.data_ptr() not in held and layers[1].workspace(n, True).data_ptr() not in held
+    s.synchronize()
+    assert torch.equal(got, want)
+    for f in ("k8", "v8"):
+        assert torch.equal(getattr(layers[0].cache, f).view(torch.uint8), getattr(layers[1].cache, f).view(torch.uint8))
+    for f in ("table", "pos", "k_scale", "v_scale", "weight", "len", "next_pos"):
+        assert torch.equal(getattr(layers[0].cache, f), getattr(layers[1].cache, f))
+    layers[1].reset(stream=s)
+    s.synchronize()
+    assert int(layers[1].cache.len.sum()) == 0 and int(layers[1].cache.next_pos[0]) == 0

@@ -192,6 +192,33 @@ def test_cache_tensors_cannot_be_replaced():
     assert c.len is held and held.tolist() == [[0, 5]]
 
 
+def test_stream_layer_refusals():
+    from block_sparse_attention_24_b200.stream import VedaStream
+    make = lambda heads=4, **kw: VedaStream(1, heads, 2, 64, 64, 640, "cpu", **kw)
+    assert make(keep=3, sink_tiles=1, recent_tiles=2).keep == [3, 3] and make(keep=[3, 4]).keep == [3, 4]
+    with pytest.raises(ValueError, match="multiple"):
+        make(heads=3)
+    with pytest.raises(ValueError, match="window"):
+        make(window=-1)
+    with pytest.raises(ValueError, match="sinks"):
+        make(sinks=-1)
+    for bad in (dict(keep=[3]), dict(keep=[3, 1]), dict(keep=2, recent_tiles=2), dict(keep=2, recent_tiles=0),
+                dict(keep=2, sink_tiles=-1)):
+        with pytest.raises(ValueError, match="keep"):
+            make(**bad)
+
+
+def test_stream_layer_workspaces_are_few():
+    from block_sparse_attention_24_b200.stream import VedaStream
+    layer = VedaStream(1, 4, 2, 64, 64, 1280, "cpu")
+    for n in range(1, 600):
+        for weight in (False, True):
+            assert layer.workspace(n, weight).numel() >= V.veda_kv_attn_ws_bytes(layer.cache, 4, n, weight)
+    assert len(layer._ws) <= 30
+    with pytest.raises(ValueError, match="limits"):
+        layer.workspace(1 << 23, False)
+
+
 # ------------------------------------------------------------------ oracle
 
 def test_oracle_codes_are_torchs():
