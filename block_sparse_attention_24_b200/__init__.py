@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+from array import array
 from typing import Optional, Sequence, Tuple
 
 import torch
@@ -523,8 +524,11 @@ def veda_kv_evict(cache: KVCache, keep: Sequence[int], sink: int, recent: int, o
         raise ValueError(f"keep must have {cache.heads_kv} entries, not {len(keep)}")
     if out is not None and out.device != cache.device:
         raise ValueError(f"out is on {out.device}, the cache on {cache.device}")
-    keeps = (ctypes.c_int32 * len(keep))(*[_i32(k, "keep") for k in keep])
-    _kv_call(cache, stream, _lib.veda_kv_evict, cache.ref, keeps, _i32(sink, "sink"), _i32(recent, "recent"),
+    try:
+        keeps = array("i", keep)
+    except OverflowError:
+        raise ValueError("keep does not fit 32 bits") from None
+    _kv_call(cache, stream, _lib.veda_kv_evict, cache.ref, keeps.buffer_info()[0], _i32(sink, "sink"), _i32(recent, "recent"),
              None if out is None else out.ref)
 
 
