@@ -182,7 +182,7 @@ __global__ void __launch_bounds__((RowsCfg<D, RP>::THREADS), 2)
     __syncthreads();
   }
   const int nb = (total + g.tile - 1) / g.tile;
-  const KvRange rg = kv_range(g, p, trow, nb, t_lo, t_hi, t_hi, cnt, tid, THREADS);
+  const KvRange rg = kv_range(g, p, trow, nb, t_lo, t_hi, t_hi, cnt, tid, THREADS, [] { __syncthreads(); });
   const int per_step = STEP / g.tile;
   const int steps_all = (rg.count() + per_step - 1) / per_step;
   const int per = max(1, (steps_all + p.splits - 1) / p.splits);
@@ -586,110 +586,180 @@ __global__ void __launch_bounds__((RowsCfg<D, RP>::THREADS), 2)
   }
 }
 
-// The kernels below start while the one before them ends, and wait here for
-// its results.
+// Blocks sum the weights of one tile with many threads where tiles are few, and of
+// four tiles where there are enough of them for every SM: the rows' sums are read
+// once per block.
+__host__ __device__ constexpr int finish_threads(int tiles) { return tiles == 1 ? 1024 : 256; }
+
+// The kernel below starts while the one before it ends, and waits here for its
+// results.
 __device__ __forceinline__ void grid_dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
-// Joins the splits of a row: a warp per row.
-template <int D>
-__global__ void __launch_bounds__(128) kv_join_kernel(const KvGeom g, const KvAttnParams p) {
-  const int lane = threadIdx.x % 32, h = blockIdx.y, b = blockIdx.z;
-  const int r = blockIdx.x * 4 + threadIdx.x / 32;
-  grid_dependency_wait();
-  int n_b, held, total;
-  if (!kv_counts(g, b, h, p.n_q, p.n_new, p.pending, n_b, held, total)) return;
-  if (r >= n_b * p.group) return;
-  const int bh = b * g.hkv + h;
-  const long long rows = p.rows_pad;
-  const float2* ml = p.part_ml + (long long)bh * p.parts * rows + r;
-  // a lane per part (32 at most): its factor and its share of the sum
-  float2 x = make_float2(-INFINITY, 0.f);
-  if (lane < p.parts) x = ml[lane * rows];
-  float m = x.x;
+// What is left behind the tile kernel, in one launch: a launch's latency is most
+// of what either part takes (3 x 333 tokens, window 4,096: XX us with a launch
+// each, XX with one).
+
+// Parts of a row that are in flight together, and what has come of those before.
+constexpr int PARTS_AHEAD = 4;
+struct RowSum {
+  float m = -INFINITY, l = 0.f;
+
+  // Takes in the (reference, sum) pairs of parts; `mul` is what the parts before
+  // have to be scaled by, f[u] what these have.
+  __device__ __forceinline__ void add(const float2 (&x)[PARTS_AHEAD], float& mul, float (&f)[PARTS_AHEAD]) {
+    float mx = m;
 #pragma unroll
-  for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-  const float f = x.x == -INFINITY ? (x.y == x.y ? 0.f : 1.f) : fast_exp2(x.x - m);
-  float l = x.y * f, o[D / 32];
+    for (int u = 0; u < PARTS_AHEAD; ++u) mx = fmaxf(mx, x[u].x);
+    mul = mx == m ? 1.f : fast_exp2(m - mx);
+    m = mx;
+    l *= mul;
 #pragma unroll
-  for (int d = 16; d; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
-#pragma unroll
-  for (int e = 0; e < D / 32; ++e) o[e] = 0.f;
-#pragma unroll 4
-  for (int s = 0; s < p.parts; ++s) {
-    const float fs = __shfl_sync(0xffffffffu, f, s);
-    if (fs == 0.f) continue;  // a part without keys has written nothing else
-    const float* src = p.part_o + (((long long)bh * p.parts + s) * rows + r) * D + lane * (D / 32);
-    if constexpr (D == 128) {
-      const float4 v = *reinterpret_cast<const float4*>(src);
-      o[0] += v.x * fs;
-      o[1] += v.y * fs;
-      o[2] += v.z * fs;
-      o[3] += v.w * fs;
-    } else {
-      const float2 v = *reinterpret_cast<const float2*>(src);
-      o[0] += v.x * fs;
-      o[1] += v.y * fs;
+    for (int u = 0; u < PARTS_AHEAD; ++u) {
+      // a part without a reference counts only where its sum is NaN
+      f[u] = x[u].x == -INFINITY ? (x[u].y == x[u].y ? 0.f : 1.f) : fast_exp2(x[u].x - mx);
+      l += x[u].y * f[u];
     }
   }
-  const bool none = l == 0.f;
-  const float inv = none ? 0.f : 1.0f / l;
-  const int i = r / p.group, qh = h * p.group + r % p.group;
-  __nv_bfloat16* dst = p.o + b * p.o_sb + (long long)i * p.o_sn + (long long)qh * p.o_sh + lane * (D / 32);
-  uint32_t w[D / 64];
-#pragma unroll
-  for (int e = 0; e < D / 64; ++e) w[e] = pack_bf16x2_rn(o[2 * e] * inv, o[2 * e + 1] * inv);
-#pragma unroll
-  for (int e = 0; e < D / 64; ++e) reinterpret_cast<uint32_t*>(dst)[e] = w[e];
-  if (lane == 0) {
-    const float l2 = none ? -INFINITY : log2f(l) + (m == -INFINITY ? 0.f : m) - OFF;
-    if (p.lse) p.lse[((long long)b * p.heads + qh) * p.n_q + i] = l2 * LN2;
-    if (p.lse2) p.lse2[(long long)bh * p.rows_cap + r] = l2;
+  __device__ __forceinline__ float lse2() const {
+    return l == 0.f ? -INFINITY : log2f(l) + (m == -INFINITY ? 0.f : m) - OFF;
   }
+};
+__device__ __forceinline__ void load_parts(const float2* ml, long long stride, int s0, int parts,
+                                           float2 (&x)[PARTS_AHEAD]) {
+#pragma unroll
+  for (int u = 0; u < PARTS_AHEAD; ++u)
+    x[u] = s0 + u < parts ? ml[(s0 + u) * stride] : make_float2(-INFINITY, 0.f);
 }
 
-// weight[tile] = decay * weight[tile] + sum over rows of 2^(lw - lse2): a block
-// per tile, its sums joined in a fixed order.
-constexpr int WEIGHT_THREADS = 256;  // a row tile's rows
-__global__ void __launch_bounds__(WEIGHT_THREADS) kv_weight_kernel(const KvGeom g, const KvAttnParams p) {
-  __shared__ float part[WEIGHT_THREADS / 32];
-  const int i = blockIdx.x, h = blockIdx.y, b = blockIdx.z, tid = threadIdx.x;
-  int n_b, held, total;
+// Joins the parts of a row, D/4 lanes to a row.
+template <int D>
+__device__ __forceinline__ void join_row(const KvGeom& g, const KvAttnParams& p, int b, int h, int r, int c4) {
   const int bh = b * g.hkv + h;
-  const long long entry = (long long)bh * g.nb_cap + i;
-  const int t0 = g.next_pos[b], ps = g.pos[entry];
-  const bool fine = kv_counts(g, b, h, p.n_q, p.n_new, p.pending, n_b, held, total);
-  grid_dependency_wait();
-  const int nb = (total + g.tile - 1) / g.tile;
-  if (!fine || i >= nb || n_b == 0) return;
-  const int rows = n_b * p.group;
-  const float* lse2 = p.lse2 + (long long)bh * p.rows_cap;
-  const float* lw = p.lw + ((long long)bh * p.pieces_cap + i) * p.rows_cap;
-  float w = 0.f;
-  constexpr int AHEAD = 4;  // row tiles whose loads are in flight
-  for (int m0 = 0; m0 < rows; m0 += AHEAD * WEIGHT_THREADS) {
-    float z[AHEAD], x[AHEAD];
+  const long long stride = p.rows_pad;
+  const float2* ml = p.part_ml + (long long)bh * p.parts * stride + r;
+  const float* po = p.part_o + ((long long)bh * p.parts * stride + r) * D + c4 * 4;
+  RowSum sum;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int s0 = 0; s0 < p.parts; s0 += PARTS_AHEAD) {
+    float2 x[PARTS_AHEAD];
+    float4 v[PARTS_AHEAD];
+    load_parts(ml, stride, s0, p.parts, x);
+#pragma unroll
+    for (int u = 0; u < PARTS_AHEAD; ++u)  // (a part without keys has written only its sum)
+      v[u] = s0 + u < p.parts ? *reinterpret_cast<const float4*>(po + (s0 + u) * stride * D)
+                              : make_float4(0.f, 0.f, 0.f, 0.f);
+    float mul, f[PARTS_AHEAD];
+    sum.add(x, mul, f);
+    o.x *= mul;
+    o.y *= mul;
+    o.z *= mul;
+    o.w *= mul;
+#pragma unroll
+    for (int u = 0; u < PARTS_AHEAD; ++u)
+      if (f[u] != 0.f) {
+        o.x += v[u].x * f[u];
+        o.y += v[u].y * f[u];
+        o.z += v[u].z * f[u];
+        o.w += v[u].w * f[u];
+      }
+  }
+  const float inv = sum.l == 0.f ? 0.f : 1.0f / sum.l;
+  const int i = r / p.group, qh = h * p.group + r - i * p.group;
+  *reinterpret_cast<uint2*>(p.o + b * p.o_sb + (long long)i * p.o_sn + (long long)qh * p.o_sh + c4 * 4) =
+      make_uint2(pack_bf16x2_rn(o.x * inv, o.y * inv), pack_bf16x2_rn(o.z * inv, o.w * inv));
+  if (c4 == 0 && p.lse) p.lse[((long long)b * p.heads + qh) * p.n_q + i] = sum.lse2() * LN2;
+}
+
+// The row's log2 normaliser from its parts, as join_row finds it.
+__device__ __forceinline__ float row_lse2(const KvAttnParams& p, int bh, int r) {
+  const float2* ml = p.part_ml + (long long)bh * p.parts * p.rows_pad + r;
+  RowSum sum;
+  for (int s0 = 0; s0 < p.parts; s0 += PARTS_AHEAD) {
+    float2 x[PARTS_AHEAD];
+    float mul, f[PARTS_AHEAD];
+    load_parts(ml, p.rows_pad, s0, p.parts, x);
+    sum.add(x, mul, f);
+  }
+  return sum.lse2();
+}
+
+// weight[tile] = decay * weight[tile] + sum over rows of 2^(lw - lse2), for TW
+// tiles next to one another: a thread per row, the threads' sums joined in a
+// fixed order.
+template <int TW>
+__device__ __forceinline__ void sum_weights(const KvGeom& g, const KvAttnParams& p, int b, int h, int i0, int nb,
+                                            int rows, int t0, const int (&ps)[TW], float* part) {
+  const int bh = b * g.hkv + h, tid = threadIdx.x, lane = tid % 32;
+  constexpr int threads = finish_threads(TW);
+  const float* lw = p.lw + ((long long)bh * p.pieces_cap + i0) * p.rows_cap;
+  float w[TW];
+#pragma unroll
+  for (int k = 0; k < TW; ++k) w[k] = 0.f;
+  constexpr int AHEAD = TW == 1 ? 4 : 2;  // rows whose loads are in flight
+  for (int r0 = tid; r0 < rows; r0 += AHEAD * threads) {
+    float x[AHEAD][TW], z[AHEAD];
 #pragma unroll
     for (int u = 0; u < AHEAD; ++u) {
-      const int r = m0 + u * WEIGHT_THREADS + tid;
-      z[u] = r < rows ? lse2[r] : -INFINITY;
-      x[u] = r < rows ? lw[r] : -INFINITY;
+      const int r = r0 + u * threads;
+#pragma unroll
+      for (int k = 0; k < TW; ++k) x[u][k] = r < rows && i0 + k < nb ? lw[(long long)k * p.rows_cap + r] : -INFINITY;
+      z[u] = r >= rows ? -INFINITY : p.parts == 1 ? p.lse2[(long long)bh * p.rows_cap + r] : row_lse2(p, bh, r);
     }
 #pragma unroll
     for (int u = 0; u < AHEAD; ++u) {
       // only tiles that a row tile's CTA could see were visited
-      const int a = m0 + u * WEIGHT_THREADS, c = min(rows, a + WEIGHT_THREADS) - 1;
-      if (a > c || !kv_tile_seen(ps, g.tile, t0 + a / p.group, t0 + c / p.group, p.causal, p.window, p.sinks)) continue;
-      // none of it seen: nothing, even of a row that is NaN
-      if (z[u] != -INFINITY && x[u] != -INFINITY) w += fast_exp2(x[u] - z[u]);
+      const int a = (r0 + u * threads) / p.tile_rows * p.tile_rows, c = min(rows, a + p.tile_rows) - 1;
+      const int t_lo = t0 + a / p.group, t_hi = t0 + c / p.group;
+#pragma unroll
+      for (int k = 0; k < TW; ++k)
+        // none of it seen: nothing, even of a row that is NaN
+        if (z[u] != -INFINITY && x[u][k] != -INFINITY &&
+            kv_tile_seen(ps[k], g.tile, t_lo, t_hi, p.causal, p.window, p.sinks))
+          w[k] += fast_exp2(x[u][k] - z[u]);
     }
   }
 #pragma unroll
-  for (int d = 16; d; d >>= 1) w += __shfl_xor_sync(0xffffffffu, w, d);
-  if (tid % 32 == 0) part[tid / 32] = w;
+  for (int k = 0; k < TW; ++k) {
+#pragma unroll
+    for (int d = 16; d; d >>= 1) w[k] += __shfl_xor_sync(0xffffffffu, w[k], d);
+    if (lane == 0) part[tid / 32 * TW + k] = w[k];
+  }
   __syncthreads();
-  if (tid == 0) {
-    for (int k = 1; k < WEIGHT_THREADS / 32; ++k) w += part[k];
-    p.weight[entry] = p.decay == 0.f ? w : p.decay * p.weight[entry] + w;
+  if (tid < TW && i0 + tid < nb) {
+    float sum = 0.f;
+#pragma unroll
+    for (int y = 0; y < threads / 32; ++y) sum += part[y * TW + tid];
+    float* dst = p.weight + (long long)bh * g.nb_cap + i0 + tid;
+    *dst = p.decay == 0.f ? sum : p.decay * *dst + sum;
+  }
+}
+
+template <int D, int TW>
+__global__ void __launch_bounds__(finish_threads(TW), TW == 1 ? 1 : 5) kv_finish_kernel(const KvGeom g, const KvAttnParams p) {
+  __shared__ float part[finish_threads(TW) / 32 * TW];
+  const int h = blockIdx.y, b = blockIdx.z;
+  const int i0 = (int)blockIdx.x < p.weight_blocks ? (int)blockIdx.x * TW : -1;  // negative: a block that joins
+  int n_b, held, total, ps[TW];
+  const int t0 = g.next_pos[b];
+#pragma unroll
+  for (int k = 0; k < TW; ++k)
+    ps[k] = i0 >= 0 && i0 + k < g.nb_cap ? g.pos[((long long)b * g.hkv + h) * g.nb_cap + i0 + k] : 0;
+  const bool fine = kv_counts(g, b, h, p.n_q, p.n_new, p.pending, n_b, held, total);
+  grid_dependency_wait();
+  const int rows = n_b * p.group;
+  if (!fine || n_b == 0) return;
+  if (i0 < 0) {
+    constexpr int PER = finish_threads(TW) / (D / 4);  // rows at a time
+    const int r0 = (blockIdx.x - p.weight_blocks) * p.join_rounds * PER + threadIdx.x / (D / 4);
+    for (int y = 0; y < p.join_rounds && r0 + y * PER < rows; ++y)
+      join_row<D>(g, p, b, h, r0 + y * PER, threadIdx.x % (D / 4));
+  } else {
+    const int nb = (total + g.tile - 1) / g.tile;
+    bool seen = false;  // by any row
+#pragma unroll
+    for (int k = 0; k < TW; ++k)
+      seen |= i0 + k < nb && kv_tile_seen(ps[k], g.tile, t0, t0 + n_b - 1, p.causal, p.window, p.sinks);
+    if (i0 < nb) sum_weights<TW>(g, p, b, h, i0, nb, seen ? rows : 0, t0, ps, part);
   }
 }
 
@@ -811,12 +881,17 @@ cudaError_t launch_kv_attn(const KvGeom& g, KvAttnParams p, void* ws, cudaStream
   if (!p.tiles) return g.d == 128 ? launch_rows<128>(g, p, s) : launch_rows<64>(g, p, s);
   cudaError_t e = launch_kv_attn_tiles(g, p, s);
   if (e != cudaSuccess) return e;
-  if (p.parts > 1) {
-    const dim3 jg((p.rows_cap + 3) / 4, g.hkv, g.B);
-    e = launch_behind(g.d == 128 ? kv_join_kernel<128> : kv_join_kernel<64>, jg, 128, s, g, p);
-  }
-  if (e != cudaSuccess || !p.weight) return e;
-  return launch_behind(kv_weight_kernel, dim3(g.nb_cap, g.hkv, g.B), WEIGHT_THREADS, s, g, p);
+  if (p.parts == 1 && !p.weight) return cudaSuccess;
+  const bool four = (long long)g.nb_cap * g.hkv * g.B > 8 * 148;
+  const int threads = finish_threads(four ? 4 : 1), per = threads / (g.d / 4);
+  // weights first, as their blocks take longest; joins in up to 8 rounds of what the device holds
+  const long long joins = p.parts == 1 ? 0 : (p.rows_cap + per - 1) / per, rounds = joins * g.hkv * g.B / (5 * 148);
+  p.join_rounds = rounds < 1 ? 1 : rounds > 8 ? 8 : (int)rounds;
+  p.weight_blocks = !p.weight ? 0 : four ? (g.nb_cap + 3) / 4 : g.nb_cap;
+  const dim3 grid(p.weight_blocks + (unsigned)((joins + p.join_rounds - 1) / p.join_rounds), g.hkv, g.B);
+  return launch_behind(g.d == 128 ? (four ? kv_finish_kernel<128, 4> : kv_finish_kernel<128, 1>)
+                                  : (four ? kv_finish_kernel<64, 4> : kv_finish_kernel<64, 1>),
+                       grid, threads, s, g, p);
 }
 
 }  // namespace veda

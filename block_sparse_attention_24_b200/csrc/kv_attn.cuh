@@ -81,19 +81,22 @@ __device__ __forceinline__ int code_at(int r, int ch) {
 }
 
 // The tiles that queries at positions t_lo .. t_hi see: entries [0, n_first)
-// and [from, upto) of the table. Counted by the whole block from the
-// positions, which ascend, and only where the mask may hide some; `last_t` is
-// the position of the sequence's last query, `cnt` zeroed shared memory.
+// and [from, upto) of the table. Counted by `threads` threads that `sync` joins
+// from the positions, which ascend, and only where the mask may hide some;
+// `last_t` is the position of the sequence's last query, `cnt` zeroed shared
+// memory.
 struct KvRange {
   int n_first, from, upto;
   __device__ int count() const { return n_first + upto - from; }
   __device__ int tile(int vt) const { return vt < n_first ? vt : vt - n_first + from; }
 };
+template <class Sync>
 __device__ __forceinline__ KvRange kv_range(const KvGeom& g, const KvAttnParams& p, long long trow, int nb, int t_lo,
-                                            int t_hi, int last_t, int* cnt, int tid, int threads) {
+                                            int t_hi, int last_t, int* cnt, int tid, int threads, Sync sync) {
   KvRange r{0, 0, nb};
   if (p.window > 0 || (p.causal && t_hi < last_t)) {
     int a = 0, f = 0, u = 0;
+#pragma unroll 4
     for (int i = tid; i < nb; i += threads) {
       const int ps = g.pos[trow + i];
       const bool ahead = p.causal && ps > t_hi;
@@ -111,7 +114,7 @@ __device__ __forceinline__ KvRange kv_range(const KvGeom& g, const KvAttnParams&
       atomicAdd(&cnt[1], f);
       atomicAdd(&cnt[2], u);
     }
-    __syncthreads();
+    sync();
     r.upto = cnt[2];
     r.from = cnt[1];
     r.n_first = min(cnt[0], r.from);

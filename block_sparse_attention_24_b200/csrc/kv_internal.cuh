@@ -47,6 +47,7 @@ struct KvAttnParams {
   int32_t tiles;       // 1: the tile kernel (256 rows per CTA), 0: the row kernel
   int32_t alt;         // the tile kernel's B takes every second step of A's rows
   int32_t splits, parts, row_tiles, rows_cap, rows_pad, tile_rows;  // parts: of a row, for the join
+  int32_t weight_blocks, join_rounds;  // blocks of a head that sum weights, and row groups of those behind, which join
   int32_t piece, pieces_cap;  // keys per entry of lw, entries per head
   float* part_o;   // [B, hkv, parts, rows_pad, d]
   int32_t* arrive;

@@ -63,6 +63,12 @@ struct TileLayout {
 };
 static_assert(sizeof(StepMeta) % 8 == 0, "barriers follow");
 
+// 16 bytes to shared memory, zeroes where `in` is false.
+__device__ __forceinline__ void cp_async16(void* dst, const void* src, bool in) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(in ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
 // Token and head-of-group of a row, kept along as rows advance by a few.
 struct RowStep {
   int tok, gh;
@@ -130,7 +136,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     kv_attn_tiles_kernel(const KvGeom g, const KvAttnParams p, const __grid_constant__ KvMaps maps) {
   using Lay = TileLayout<D>;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ int sm_cnt[3];
+  __shared__ int sm_cnt[4];  // of kv_range, and the steps
   uint8_t* smem = smem_raw + (((smem_u32(smem_raw) + 1023u) & ~1023u) - smem_u32(smem_raw));
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
   // Under a causal mask the last row tiles have the most keys, so every head's
@@ -156,18 +162,19 @@ __global__ void __launch_bounds__(THREADS, 1)
   constexpr int LPR = D / 8, RPI = 32 / LPR, ITERS = 32 / RPI;
   const int rt = warp / 4, wrow = base + (alt ? warp % 4 : warp) * 32, sub = lane / LPR, c8 = lane % LPR;
   int tok0 = 0, gh0 = 0;  // token and head of the group of row wrow + sub
-  uint4 qw[ITERS];
+  uint8_t* own = smem + Lay::OFF_Q + rt * 2 * Lay::QB;  // the row tile's Q, and its O at the end
+  // A row's bf16 lie where its two parts will, half of them in each one's place.
+  uint8_t* q_raw = own + (c8 >= LPR / 2 ? Lay::QB : 0) + ((warp % 4) * 32 + sub) * D + c8 % (LPR / 2) * 16;
   const bool mine = warp < 4 || (warp < 8 && has_b);
   if (mine) {
     tok0 = (wrow + sub) / p.group;
     gh0 = (wrow + sub) % p.group;
     const __nv_bfloat16* src = p.q.p + b * p.q.sb + (long long)h * p.group * p.q.sh + c8 * 8;
     RowStep at{tok0, gh0};
-#pragma unroll
+#pragma unroll 1
     for (int j = 0; j < ITERS; ++j) {
-      qw[j] = make_uint4(0, 0, 0, 0);
-      if (wrow + sub + j * RPI < rows)
-        qw[j] = *reinterpret_cast<const uint4*>(src + (long long)at.tok * p.q.sn + (long long)at.gh * p.q.sh);
+      const bool in = wrow + sub + j * RPI < rows;
+      cp_async16(q_raw + j * RPI * D, in ? src + (long long)at.tok * p.q.sn + (long long)at.gh * p.q.sh : src, in);
       at.advance(RPI, p.group);
     }
   }
@@ -185,22 +192,22 @@ __global__ void __launch_bounds__(THREADS, 1)
   StepMeta* meta = reinterpret_cast<StepMeta*>(smem + Lay::OFF_META);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Lay::OFF_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Lay::OFF_MISC + 4);
-  if (p.window > 0 || p.causal) {
-    if (tid < 3) sm_cnt[tid] = 0;
-    __syncthreads();
-  }
-  const int nb = (total + g.tile - 1) / g.tile;
-  const KvRange rg = kv_range(g, p, trow, nb, t_lo, t_hi, t0 + n_b - 1, sm_cnt, tid, THREADS);
-  const int per_step = BN / g.tile;  // tiles per step
-  const int n_tiles = rg.count();
-  const int steps_all = (n_tiles + per_step - 1) / per_step;
-  const int per = (steps_all + p.splits - 1) / p.splits;
-  const int s_lo = min(steps_all, sp * per), n_steps = min(steps_all, s_lo + per) - s_lo;
-  if (n_steps == 0 && p.parts > 1) {  // nothing to add: the join skips this part
-    for (int r = base + tid; r < min(rows, base + 2 * BM); r += THREADS)
-      for (int x = 0; x <= alt; ++x)
-        p.part_ml[((long long)bh * p.parts + (alt ? 2 * sp + x : sp)) * p.rows_pad + r] = make_float2(-INFINITY, 0.f);
-    return;
+  // The steps are worked out by the warps that do not take Q apart meanwhile.
+  KvRange rg{0, 0, 0};
+  int s_lo = 0, n_steps = 0;
+  if (warp >= 8) {
+    auto sync = [] { asm volatile("bar.sync 2, 128;" ::: "memory"); };
+    if (p.window > 0 || p.causal) {
+      if (tid < 256 + 3) sm_cnt[tid - 256] = 0;
+      sync();
+    }
+    const int nb = (total + g.tile - 1) / g.tile;
+    rg = kv_range(g, p, trow, nb, t_lo, t_hi, t0 + n_b - 1, sm_cnt, tid - 256, 128, sync);
+    const int steps_all = (rg.count() * g.tile + BN - 1) / BN;
+    const int per = (steps_all + p.splits - 1) / p.splits;
+    s_lo = min(steps_all, sp * per);
+    n_steps = min(steps_all, s_lo + per) - s_lo;
+    if (tid == 256) sm_cnt[3] = n_steps;
   }
 
   // Each role prepares its part before the one barrier: the first copies are
@@ -225,7 +232,6 @@ __global__ void __launch_bounds__(THREADS, 1)
   auto produce_v = [&](int e, int row0, int row1) {
     load_half(&maps.v, v_full + e % VST, smem + Lay::OFF_V + e % VST * Lay::CB, row0, row1);
   };
-  uint8_t* own = smem + Lay::OFF_Q + rt * 2 * Lay::QB;  // the row tile's Q, and its O at the end
   float qs = 0.f;
   if (warp == 8) {
     if (lane < Lay::NUM_BARS) {
@@ -242,19 +248,25 @@ __global__ void __launch_bounds__(THREADS, 1)
     tmem_alloc(tmem_slot, 512);
     tmem_relinquish();
   } else if (mine) {
-    // Q in its two e4m3 parts
-#pragma unroll
+    // Q in its two e4m3 parts. Loops over rows stay rolled here: each instruction
+    // runs once per CTA and row, and its fetch would cost more than its execution
+    // (unrolled, this took 23k clocks of a CTA, and takes XX rolled).
+    cp_async_wait_all();
+    __syncwarp();
+#pragma unroll 2
     for (int j = 0; j < ITERS; ++j) {
-      uint32_t top = max(max(bf16x2_top(qw[j].x), bf16x2_top(qw[j].y)), max(bf16x2_top(qw[j].z), bf16x2_top(qw[j].w)));
+      const uint4 qw = *reinterpret_cast<const uint4*>(q_raw + j * RPI * D);
+      uint32_t top = max(max(bf16x2_top(qw.x), bf16x2_top(qw.y)), max(bf16x2_top(qw.z), bf16x2_top(qw.w)));
 #pragma unroll
       for (int d = 1; d < LPR; d <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
       float mul, inv;
       q_scale<7>(top, mul, inv);
       mul = copysignf(mul, p.scale_log2);
       uint32_t hi[2], lo[2];
-      split_e4m3x4(qw[j].x, qw[j].y, mul, hi[0], lo[0]);
-      split_e4m3x4(qw[j].z, qw[j].w, mul, hi[1], lo[1]);
+      split_e4m3x4(qw.x, qw.y, mul, hi[0], lo[0]);
+      split_e4m3x4(qw.z, qw.w, mul, hi[1], lo[1]);
       const int at = code_at<D>((warp % 4) * 32 + j * RPI + sub, c8 >> 1) + (c8 & 1) * 8;
+      __syncwarp();
       *reinterpret_cast<uint2*>(own + at) = make_uint2(hi[0], hi[1]);
       *reinterpret_cast<uint2*>(own + Lay::QB + at) = make_uint2(lo[0], lo[1]);
       // the lane that owns the row keeps its factor
@@ -268,6 +280,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  n_steps = sm_cnt[3];
 
   if (warp >= 8) {
     regs_lower<REGS_ROLES>();
@@ -484,7 +497,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           if (sm.entry[x] >= 0)
             dst[(long long)sm.entry[x] * p.rows_cap] = sum == 0.f ? -INFINITY : __log2f(sum) + (off - sm.ev[x]);
         };
-        if (per_step == 1) {
+        if (g.tile == BN) {
           put(0, sum0 + sum1);
         } else {
           put(0, sum0);
@@ -509,9 +522,10 @@ __global__ void __launch_bounds__(THREADS, 1)
       constexpr int UNITS = D / 8;  // 16-byte units per row and pass
       uint8_t* mem = own + (warp % 4) * 32 * 2 * D;
       auto slot = [&](int r, int u) { return mem + r * 2 * D + ((u ^ (r & (UNITS - 1))) << 4); };
-      const int passes = p.parts > 1 ? 2 : 1;
+      // a part without keys is no more than its sum, which is 0
+      const int passes = p.parts == 1 ? 1 : n_steps ? 2 : 0;
       for (int ps = 0; ps < passes; ++ps) {
-        const int cols = D / passes;
+        const int cols = D >> (passes - 1);
         for (int c = 0; c < cols; c += 32) {
           uint32_t u[32];
           if (have) {
