@@ -248,30 +248,43 @@ __global__ void __launch_bounds__(THREADS, 1)
     tmem_alloc(tmem_slot, 512);
     tmem_relinquish();
   } else if (mine) {
-    // Q in its two e4m3 parts. Loops over rows stay rolled here: each instruction
-    // runs once per CTA and row, and its fetch would cost more than its execution
-    // (unrolled, this took 23k clocks of a CTA, and takes XX rolled).
+    // Q in its two e4m3 parts, a few rows at a time: their chains of shuffles and
+    // conversions overlap.
+    constexpr int BATCH = 4;
     cp_async_wait_all();
     __syncwarp();
-#pragma unroll 2
-    for (int j = 0; j < ITERS; ++j) {
-      const uint4 qw = *reinterpret_cast<const uint4*>(q_raw + j * RPI * D);
-      uint32_t top = max(max(bf16x2_top(qw.x), bf16x2_top(qw.y)), max(bf16x2_top(qw.z), bf16x2_top(qw.w)));
+#pragma unroll 1
+    for (int j0 = 0; j0 < ITERS; j0 += BATCH) {
+      uint4 qw[BATCH];
+      uint32_t top[BATCH];
 #pragma unroll
-      for (int d = 1; d < LPR; d <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
-      float mul, inv;
-      q_scale<7>(top, mul, inv);
-      mul = copysignf(mul, p.scale_log2);
-      uint32_t hi[2], lo[2];
-      split_e4m3x4(qw.x, qw.y, mul, hi[0], lo[0]);
-      split_e4m3x4(qw.z, qw.w, mul, hi[1], lo[1]);
-      const int at = code_at<D>((warp % 4) * 32 + j * RPI + sub, c8 >> 1) + (c8 & 1) * 8;
-      __syncwarp();
-      *reinterpret_cast<uint2*>(own + at) = make_uint2(hi[0], hi[1]);
-      *reinterpret_cast<uint2*>(own + Lay::QB + at) = make_uint2(lo[0], lo[1]);
-      // the lane that owns the row keeps its factor
-      const float got = __shfl_sync(0xffffffffu, inv, (lane % RPI) * LPR);
-      if (lane / RPI == j) qs = got;
+      for (int y = 0; y < BATCH; ++y) {
+        qw[y] = *reinterpret_cast<const uint4*>(q_raw + (j0 + y) * RPI * D);
+        top[y] = max(max(bf16x2_top(qw[y].x), bf16x2_top(qw[y].y)), max(bf16x2_top(qw[y].z), bf16x2_top(qw[y].w)));
+      }
+#pragma unroll
+      for (int d = 1; d < LPR; d <<= 1)
+#pragma unroll
+        for (int y = 0; y < BATCH; ++y) top[y] = max(top[y], __shfl_xor_sync(0xffffffffu, top[y], d));
+      uint32_t hi[BATCH][2], lo[BATCH][2];
+#pragma unroll
+      for (int y = 0; y < BATCH; ++y) {
+        float mul, inv;
+        q_scale<7>(top[y], mul, inv);
+        mul = copysignf(mul, p.scale_log2);
+        split_e4m3x4(qw[y].x, qw[y].y, mul, hi[y][0], lo[y][0]);
+        split_e4m3x4(qw[y].z, qw[y].w, mul, hi[y][1], lo[y][1]);
+        // the lane that owns the row keeps its factor
+        const float got = __shfl_sync(0xffffffffu, inv, (lane % RPI) * LPR);
+        if (lane / RPI == j0 + y) qs = got;
+      }
+      __syncwarp();  // the rows have been read
+#pragma unroll
+      for (int y = 0; y < BATCH; ++y) {
+        const int at = code_at<D>((warp % 4) * 32 + (j0 + y) * RPI + sub, c8 >> 1) + (c8 & 1) * 8;
+        *reinterpret_cast<uint2*>(own + at) = make_uint2(hi[y][0], hi[y][1]);
+        *reinterpret_cast<uint2*>(own + Lay::QB + at) = make_uint2(lo[y][0], lo[y][1]);
+      }
     }
     qs *= fabsf(p.scale_log2);
     fence_proxy_async_smem();
