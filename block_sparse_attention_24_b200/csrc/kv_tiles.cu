@@ -63,21 +63,22 @@ struct TileLayout {
 };
 static_assert(sizeof(StepMeta) % 8 == 0, "barriers follow");
 
-// 16 bytes to shared memory, zeroes where `in` is false.
-__device__ __forceinline__ void cp_async16(void* dst, const void* src, bool in) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(in ? 16 : 0) : "memory");
-}
-__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
-
-// Token and head-of-group of a row, kept along as rows advance by a few.
+// Token and head-of-group of a row, kept along as rows advance by a few (without a
+// loop, so that the accesses of several rows overlap).
 struct RowStep {
-  int tok, gh;
-  __device__ __forceinline__ void advance(int n, int group) {
-    gh += n;
-    while (gh >= group) {
-      gh -= group;
-      ++tok;
-    }
+  int tok, gh, d_tok, d_gh, group;
+  __device__ __forceinline__ RowStep(int row, int by, int group_) : group(group_) {
+    tok = row / group;
+    gh = row - tok * group;
+    d_tok = by / group;
+    d_gh = by - d_tok * group;
+  }
+  __device__ __forceinline__ void advance() {
+    gh += d_gh;
+    tok += d_tok;
+    const bool over = gh >= group;
+    gh -= over ? group : 0;
+    tok += over;
   }
 };
 
@@ -161,23 +162,8 @@ __global__ void __launch_bounds__(THREADS, 1)
   // group `sub` has rows sub, sub + RPI, ... of the warp's 32.
   constexpr int LPR = D / 8, RPI = 32 / LPR, ITERS = 32 / RPI;
   const int rt = warp / 4, wrow = base + (alt ? warp % 4 : warp) * 32, sub = lane / LPR, c8 = lane % LPR;
-  int tok0 = 0, gh0 = 0;  // token and head of the group of row wrow + sub
   uint8_t* own = smem + Lay::OFF_Q + rt * 2 * Lay::QB;  // the row tile's Q, and its O at the end
-  // A row's bf16 lie where its two parts will, half of them in each one's place.
-  uint8_t* q_raw = own + (c8 >= LPR / 2 ? Lay::QB : 0) + ((warp % 4) * 32 + sub) * D + c8 % (LPR / 2) * 16;
   const bool mine = warp < 4 || (warp < 8 && has_b);
-  if (mine) {
-    tok0 = (wrow + sub) / p.group;
-    gh0 = (wrow + sub) % p.group;
-    const __nv_bfloat16* src = p.q.p + b * p.q.sb + (long long)h * p.group * p.q.sh + c8 * 8;
-    RowStep at{tok0, gh0};
-#pragma unroll 1
-    for (int j = 0; j < ITERS; ++j) {
-      const bool in = wrow + sub + j * RPI < rows;
-      cp_async16(q_raw + j * RPI * D, in ? src + (long long)at.tok * p.q.sn + (long long)at.gh * p.q.sh : src, in);
-      at.advance(RPI, p.group);
-    }
-  }
 
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Lay::OFF_BAR);
   uint64_t* k_full = bars;
@@ -249,19 +235,31 @@ __global__ void __launch_bounds__(THREADS, 1)
     tmem_relinquish();
   } else if (mine) {
     // Q in its two e4m3 parts, a few rows at a time: their chains of shuffles and
-    // conversions overlap.
+    // conversions overlap, and the next rows are on their way.
     constexpr int BATCH = 4;
-    cp_async_wait_all();
-    __syncwarp();
+    const __nv_bfloat16* src = p.q.p + b * p.q.sb + (long long)h * p.group * p.q.sh + c8 * 8;
+    RowStep at(wrow + sub, RPI, p.group);
+    uint4 next[BATCH];
+    auto load = [&](int j0) {
+#pragma unroll
+      for (int y = 0; y < BATCH; ++y) {
+        next[y] = make_uint4(0, 0, 0, 0);
+        if (wrow + sub + (j0 + y) * RPI < rows)
+          next[y] = *reinterpret_cast<const uint4*>(src + (long long)at.tok * p.q.sn + (long long)at.gh * p.q.sh);
+        at.advance();
+      }
+    };
+    load(0);
 #pragma unroll 1
     for (int j0 = 0; j0 < ITERS; j0 += BATCH) {
       uint4 qw[BATCH];
       uint32_t top[BATCH];
 #pragma unroll
       for (int y = 0; y < BATCH; ++y) {
-        qw[y] = *reinterpret_cast<const uint4*>(q_raw + (j0 + y) * RPI * D);
+        qw[y] = next[y];
         top[y] = max(max(bf16x2_top(qw[y].x), bf16x2_top(qw[y].y)), max(bf16x2_top(qw[y].z), bf16x2_top(qw[y].w)));
       }
+      if (j0 + BATCH < ITERS) load(j0 + BATCH);
 #pragma unroll
       for (int d = 1; d < LPR; d <<= 1)
 #pragma unroll
@@ -278,12 +276,11 @@ __global__ void __launch_bounds__(THREADS, 1)
         const float got = __shfl_sync(0xffffffffu, inv, (lane % RPI) * LPR);
         if (lane / RPI == j0 + y) qs = got;
       }
-      __syncwarp();  // the rows have been read
 #pragma unroll
       for (int y = 0; y < BATCH; ++y) {
-        const int at = code_at<D>((warp % 4) * 32 + (j0 + y) * RPI + sub, c8 >> 1) + (c8 & 1) * 8;
-        *reinterpret_cast<uint2*>(own + at) = make_uint2(hi[y][0], hi[y][1]);
-        *reinterpret_cast<uint2*>(own + Lay::QB + at) = make_uint2(lo[y][0], lo[y][1]);
+        const int to = code_at<D>((warp % 4) * 32 + (j0 + y) * RPI + sub, c8 >> 1) + (c8 & 1) * 8;
+        *reinterpret_cast<uint2*>(own + to) = make_uint2(hi[y][0], hi[y][1]);
+        *reinterpret_cast<uint2*>(own + Lay::QB + to) = make_uint2(lo[y][0], lo[y][1]);
       }
     }
     qs *= fabsf(p.scale_log2);
@@ -566,7 +563,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
         __syncwarp();
         static_assert(UNITS == LPR, "rows are written as Q was read");
-        RowStep at{tok0, gh0};
+        RowStep at(wrow + sub, RPI, p.group);
 #pragma unroll 4
         for (int j = 0; j < ITERS; ++j) {
           const int r = j * RPI + sub;
@@ -580,7 +577,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                                         (long long)(h * p.group + at.gh) * p.o_sh + c8 * 8) = v;
             }
           }
-          at.advance(RPI, p.group);
+          at.advance();
         }
         __syncwarp();
       }
