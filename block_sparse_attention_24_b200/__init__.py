@@ -392,6 +392,7 @@ class KVCache:
                            *[getattr(self, n).data_ptr() for n in ("k8", "v8", "table", "pos", "k_scale", "v_scale",
                                                                    "weight", "len", "next_pos", "_arrive",
                                                                    "status")])
+        self._ws_bytes = {}  # of veda_kv_attn, by (heads, n_q, with weights)
         self.ref = ctypes.byref(self._c)
 
     def __setattr__(self, name, value):
@@ -413,6 +414,13 @@ def _expect(t, name: str, shape, dtype, device, contiguous: bool = True):
         raise ValueError(f"{name} is on {t.device}, not on {device}")
     if contiguous and not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
+
+
+def _ptr(t, name: str, shape, dtype, device) -> int:
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.device == device and
+            t.is_contiguous()):
+        _expect(t, name, shape, dtype, device)
+    return t.data_ptr()
 
 
 def _rows(t: torch.Tensor, name: str, shape, cache: KVCache):
@@ -440,7 +448,7 @@ def _kv_call(cache: KVCache, stream, fn, *args):
     if stream is not None and stream.device != cache.device:
         raise ValueError(f"the stream is on {stream.device}, the cache on {cache.device}")
     raw = torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
-    if torch.cuda.current_device() == index:
+    if torch._C._cuda_getDevice() == index:
         rc = fn(*args, raw)
     else:
         with torch.cuda.device(index):
@@ -458,10 +466,7 @@ def _i32(x, name: str) -> int:
 
 
 def _n_new(cache: KVCache, n_new):
-    if n_new is None:
-        return None
-    _expect(n_new, "n_new", (cache.B,), torch.int32, cache.device)
-    return n_new.data_ptr()
+    return None if n_new is None else _ptr(n_new, "n_new", (cache.B,), torch.int32, cache.device)
 
 
 def veda_kv_append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, n_new: Optional[torch.Tensor] = None,
@@ -500,20 +505,20 @@ def veda_kv_attn(cache: KVCache, q: torch.Tensor, o: torch.Tensor, scale: float,
     shape = (cache.B, n, heads, cache.d)
     qp, qs = _rows(q, "q", shape, cache)
     op, os_ = _rows(o, "o", shape, cache)
-    lp = wp = None
-    if lse is not None:
-        _expect(lse, "lse", (cache.B, heads, n), torch.float32, cache.device)
-        lp = lse.data_ptr()
-    if weight is not None:
-        _expect(weight, "weight", (cache.B, cache.heads_kv, cache.nb_cap), torch.float32, cache.device)
-        wp = weight.data_ptr()
-    need = _lib.veda_kv_attn_ws_bytes(cache.ref, heads, n, wp is not None)
-    if not isinstance(ws, torch.Tensor) or ws.device != cache.device or not ws.is_contiguous():
+    dev = cache.device
+    lp = None if lse is None else _ptr(lse, "lse", (cache.B, heads, n), torch.float32, dev)
+    wp = None if weight is None else _ptr(weight, "weight", (cache.B, cache.heads_kv, cache.nb_cap), torch.float32, dev)
+    key = (heads, n, wp is not None)
+    need = cache._ws_bytes.get(key)
+    if need is None:
+        need = cache._ws_bytes[key] = _lib.veda_kv_attn_ws_bytes(cache.ref, *key)
+    if not isinstance(ws, torch.Tensor) or ws.device != dev or not ws.is_contiguous():
         raise ValueError("ws must be a contiguous tensor on the cache's device")
-    if ws.numel() * ws.element_size() < need:
-        raise ValueError(f"ws holds {ws.numel() * ws.element_size()} bytes, {need} are needed")
+    if ws.nbytes < need:
+        raise ValueError(f"ws holds {ws.nbytes} bytes, {need} are needed")
     _kv_call(cache, stream, _lib.veda_kv_attn, cache.ref, qp, qs, heads, n, _n_new(cache, n_new), bool(pending),
-             bool(causal), _i32(window, "window"), _i32(sinks, "sinks"), float(scale), op, os_, lp, wp, float(decay), ws.data_ptr())
+             bool(causal), _i32(window, "window"), _i32(sinks, "sinks"), float(scale), op, os_, lp, wp, float(decay),
+             ws.data_ptr())
 
 
 def veda_kv_evict(cache: KVCache, keep: Sequence[int], sink: int, recent: int, out: Optional[KVCache] = None,

@@ -299,9 +299,9 @@ __global__ void __launch_bounds__(THREADS)
 
 template <int THREADS>
 cudaError_t launch_evict(const KvGeom& g, const KvKeep& keeps, int sink, int recent, const KvGeom& out, cudaStream_t s) {
-  const int smem = 5 * 4 * ((g.nb_cap + 3) & ~3);  // at most 160 KB
-  const cudaError_t e =
-      cudaFuncSetAttribute(kv_evict_kernel<THREADS>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  static std::atomic<uint64_t> done{0};
+  const int smem = 5 * 4 * ((g.nb_cap + 3) & ~3);
+  const cudaError_t e = allow_smem((const void*)kv_evict_kernel<THREADS>, 5 * 4 * VEDA_KV_MAX_NB, done);
   if (e != cudaSuccess) return e;
   kv_evict_kernel<THREADS><<<dim3(g.hkv, g.B), THREADS, smem, s>>>(g, out, keeps, sink, recent);
   return cudaGetLastError();

@@ -5,6 +5,8 @@
 
 #include <cuda_fp16.h>
 
+#include <atomic>
+
 #include "veda_internal.cuh"
 
 #define VEDA_KV_MAX_NB 8192  // table entries per (sequence, K/V head)
@@ -83,6 +85,17 @@ __device__ __forceinline__ bool kv_tile_seen(int p, int tile, int t_lo, int t_hi
 
 // A pool as a 2D map of bytes [rows, d], box [box_rows, d], swizzled over d bytes (64 or 128).
 CUresult encode_tensor_map_2d_u8(CUtensorMap* map, const void* base, uint64_t d, uint64_t rows, uint32_t box_rows);
+
+// Lets a kernel have `bytes` of dynamic shared memory, once per device: `done`,
+// a bit per device, is the caller's own for this kernel.
+inline cudaError_t allow_smem(const void* kernel, int bytes, std::atomic<uint64_t>& done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess || (dev < 64 && (done.load(std::memory_order_relaxed) >> dev & 1))) return e;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess && dev < 64) done.fetch_or(1ull << dev, std::memory_order_relaxed);
+  return e;
+}
 
 cudaError_t launch_kv_append(const KvGeom& g, const KvRows& k, const KvRows& v, int n, const int32_t* n_new,
                              cudaStream_t s);

@@ -607,8 +607,8 @@ cudaError_t launch(const KvGeom& g, const KvAttnParams& p, cudaStream_t s) {
   if (encode_tensor_map_2d_u8(&maps.k, g.k8, D, rows, HALF) != CUDA_SUCCESS ||
       encode_tensor_map_2d_u8(&maps.v, g.v8, D, rows, HALF) != CUDA_SUCCESS)
     return cudaErrorInvalidValue;
-  const cudaError_t e =
-      cudaFuncSetAttribute(kv_attn_tiles_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, TileLayout<D>::ALLOC);
+  static std::atomic<uint64_t> done{0};
+  const cudaError_t e = allow_smem((const void*)kv_attn_tiles_kernel<D>, TileLayout<D>::ALLOC, done);
   if (e != cudaSuccess) return e;
   kv_attn_tiles_kernel<D><<<dim3(g.hkv * p.splits * p.row_tiles, 1, g.B), THREADS, TileLayout<D>::ALLOC, s>>>(g, p, maps);
   return cudaGetLastError();
