@@ -140,6 +140,7 @@ __global__ void __launch_bounds__((RowsCfg<D, RP>::THREADS), 2)
   uint8_t* smem = smem_raw + (((smem_u32(smem_raw) + 1023u) & ~1023u) - smem_u32(smem_raw));
   const int sp = blockIdx.x, h = blockIdx.y, b = blockIdx.z;
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+  after_predecessor();
   int n_b, held, total;
   const int t_lo = g.next_pos[b];
   if (!kv_counts(g, b, h, p.n_q, p.n_new, p.pending, n_b, held, total)) return;
@@ -591,9 +592,6 @@ __global__ void __launch_bounds__((RowsCfg<D, RP>::THREADS), 2)
 // once per block.
 __host__ __device__ constexpr int finish_threads(int tiles) { return tiles == 1 ? 1024 : 256; }
 
-// The kernel below starts while the one before it ends, and waits here for its
-// results.
-__device__ __forceinline__ void grid_dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // What is left behind the tile kernel, in one launch: a launch's latency is most of
 // what either part takes (3 x 333 tokens, window 4,096: 39 us with a launch each,
@@ -740,12 +738,14 @@ __global__ void __launch_bounds__(finish_threads(TW), TW == 1 ? 1 : 5) kv_finish
   const int h = blockIdx.y, b = blockIdx.z;
   const int i0 = (int)blockIdx.x < p.weight_blocks ? (int)blockIdx.x * TW : -1;  // negative: a block that joins
   int n_b, held, total, ps[TW];
+  // Before the wait: what the tile kernel, which is launched behind all that came
+  // before it, does not write.
   const int t0 = g.next_pos[b];
 #pragma unroll
   for (int k = 0; k < TW; ++k)
     ps[k] = i0 >= 0 && i0 + k < g.nb_cap ? g.pos[((long long)b * g.hkv + h) * g.nb_cap + i0 + k] : 0;
   const bool fine = kv_counts(g, b, h, p.n_q, p.n_new, p.pending, n_b, held, total);
-  grid_dependency_wait();
+  after_predecessor();
   const int rows = n_b * p.group;
   if (!fine || n_b == 0) return;
   if (i0 < 0) {
@@ -763,22 +763,6 @@ __global__ void __launch_bounds__(finish_threads(TW), TW == 1 ? 1 : 5) kv_finish
   }
 }
 
-// A launch that may start before the kernel before it in the stream has ended
-// (which it waits for itself).
-cudaError_t launch_behind(void (*kernel)(const KvGeom, const KvAttnParams), dim3 grid, int threads, cudaStream_t s,
-                          const KvGeom& g, const KvAttnParams& p) {
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(threads);
-  cfg.stream = s;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, g, p);
-}
-
 template <int D, int RP>
 cudaError_t launch_rows_t(const KvGeom& g, const KvAttnParams& p, cudaStream_t s) {
   using Cfg = RowsCfg<D, RP>;
@@ -790,8 +774,7 @@ cudaError_t launch_rows_t(const KvGeom& g, const KvAttnParams& p, cudaStream_t s
   static std::atomic<uint64_t> done{0};
   const cudaError_t e = allow_smem((const void*)kv_attn_rows_kernel<D, RP>, Cfg::ALLOC, done);
   if (e != cudaSuccess) return e;
-  kv_attn_rows_kernel<D, RP><<<dim3(p.splits, g.hkv, g.B), Cfg::THREADS, Cfg::ALLOC, s>>>(g, p, maps);
-  return cudaGetLastError();
+  return launch_chained(kv_attn_rows_kernel<D, RP>, dim3(p.splits, g.hkv, g.B), Cfg::THREADS, Cfg::ALLOC, s, g, p, maps);
 }
 
 template <int D>
@@ -889,9 +872,9 @@ cudaError_t launch_kv_attn(const KvGeom& g, KvAttnParams p, void* ws, cudaStream
   p.join_rounds = rounds < 1 ? 1 : rounds > 8 ? 8 : (int)rounds;
   p.weight_blocks = !p.weight ? 0 : four ? (g.nb_cap + 3) / 4 : g.nb_cap;
   const dim3 grid(p.weight_blocks + (unsigned)((joins + p.join_rounds - 1) / p.join_rounds), g.hkv, g.B);
-  return launch_behind(g.d == 128 ? (four ? kv_finish_kernel<128, 4> : kv_finish_kernel<128, 1>)
-                                  : (four ? kv_finish_kernel<64, 4> : kv_finish_kernel<64, 1>),
-                       grid, threads, s, g, p);
+  return launch_chained(g.d == 128 ? (four ? kv_finish_kernel<128, 4> : kv_finish_kernel<128, 1>)
+                                   : (four ? kv_finish_kernel<64, 4> : kv_finish_kernel<64, 1>),
+                        grid, threads, 0, s, g, p);
 }
 
 }  // namespace veda

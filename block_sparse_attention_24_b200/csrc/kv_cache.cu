@@ -56,6 +56,7 @@ __global__ void __launch_bounds__(APPEND_THREADS)
   constexpr int VPR = D / 16;                          // 16-value vectors per row
   constexpr int PT = 128 * VPR / APPEND_THREADS;       // vectors per thread at tile 128
   const int h = blockIdx.y >> 1, is_v = blockIdx.y & 1, b = blockIdx.z;
+  after_predecessor();
   int n_b, held, total;
   if (!kv_counts(g, b, h, n, n_new, true, n_b, held, total)) return;
   const int i = held / g.tile + blockIdx.x;            // the tile's place in the table
@@ -132,6 +133,7 @@ __global__ void __launch_bounds__(APPEND_THREADS)
 }
 
 __global__ void kv_advance_kernel(const KvGeom g, const int n, const int32_t* n_new) {
+  after_predecessor();
   const int i = blockIdx.x * blockDim.x + threadIdx.x;
   if (i >= g.B * g.hkv) return;
   const int b = i / g.hkv, h = i - b * g.hkv;
@@ -192,6 +194,7 @@ __global__ void __launch_bounds__(THREADS)
   const int h = blockIdx.x, b = blockIdx.y, tid = threadIdx.x, lane = tid % 32;
   const int bh = b * g.hkv + h;
   const long long row = (long long)bh * g.nb_cap;
+  after_predecessor();
   const int held = g.len[bh];
   const bool same = out.table == g.table;
   // a row starts at a multiple of 16 bytes where its length is one of 4
@@ -303,8 +306,7 @@ cudaError_t launch_evict(const KvGeom& g, const KvKeep& keeps, int sink, int rec
   const int smem = 5 * 4 * ((g.nb_cap + 3) & ~3);
   const cudaError_t e = allow_smem((const void*)kv_evict_kernel<THREADS>, 5 * 4 * VEDA_KV_MAX_NB, done);
   if (e != cudaSuccess) return e;
-  kv_evict_kernel<THREADS><<<dim3(g.hkv, g.B), THREADS, smem, s>>>(g, out, keeps, sink, recent);
-  return cudaGetLastError();
+  return launch_chained(kv_evict_kernel<THREADS>, dim3(g.hkv, g.B), THREADS, smem, s, g, out, keeps, sink, recent);
 }
 
 }  // namespace
@@ -313,14 +315,12 @@ cudaError_t launch_kv_append(const KvGeom& g, const KvRows& k, const KvRows& v, 
                              cudaStream_t s) {
   const long long tiles = ((long long)n + g.tile - 2) / g.tile + 1;  // n tokens from any row of a tile on
   const dim3 grid((unsigned)(tiles < g.nb_cap ? tiles : g.nb_cap), 2 * g.hkv, g.B);
-  if (g.d == 128) kv_append_kernel<128><<<grid, APPEND_THREADS, 0, s>>>(g, k, v, n, n_new);
-  else kv_append_kernel<64><<<grid, APPEND_THREADS, 0, s>>>(g, k, v, n, n_new);
-  return cudaGetLastError();
+  return launch_chained(g.d == 128 ? kv_append_kernel<128> : kv_append_kernel<64>, grid, APPEND_THREADS, 0, s, g, k, v, n,
+                        n_new);
 }
 
 cudaError_t launch_kv_advance(const KvGeom& g, int n, const int32_t* n_new, cudaStream_t s) {
-  kv_advance_kernel<<<(g.B * g.hkv + 127) / 128, 128, 0, s>>>(g, n, n_new);
-  return cudaGetLastError();
+  return launch_chained(kv_advance_kernel, dim3((g.B * g.hkv + 127) / 128), 128, 0, s, g, n, n_new);
 }
 
 cudaError_t launch_kv_evict(const KvGeom& g, const int32_t* keep, int sink, int recent, const KvGeom& out,

@@ -6,6 +6,7 @@
 #include <cuda_fp16.h>
 
 #include <atomic>
+#include <utility>
 
 #include "veda_internal.cuh"
 
@@ -85,6 +86,27 @@ __device__ __forceinline__ bool kv_tile_seen(int p, int tile, int t_lo, int t_hi
 
 // A pool as a 2D map of bytes [rows, d], box [box_rows, d], swizzled over d bytes (64 or 128).
 CUresult encode_tensor_map_2d_u8(CUtensorMap* map, const void* base, uint64_t d, uint64_t rows, uint32_t box_rows);
+
+// The kernels (but for the tile kernel, see there) are launched so that each may be
+// set up while the one before it in the stream ends: it waits here for that one's
+// results, before it reads or writes anything, and lets the next one do the same.
+__device__ __forceinline__ void after_predecessor() {
+  asm volatile("griddepcontrol.wait;\n\tgriddepcontrol.launch_dependents;" ::: "memory");
+}
+template <class... Params, class... Args>
+cudaError_t launch_chained(void (*kernel)(Params...), dim3 grid, int threads, int smem, cudaStream_t s, Args&&... args) {
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
+}
 
 // Lets a kernel have `bytes` of dynamic shared memory, once per device: `done`,
 // a bit per device, is the caller's own for this kernel.

@@ -610,6 +610,7 @@ cudaError_t launch(const KvGeom& g, const KvAttnParams& p, cudaStream_t s) {
   static std::atomic<uint64_t> done{0};
   const cudaError_t e = allow_smem((const void*)kv_attn_tiles_kernel<D>, TileLayout<D>::ALLOC, done);
   if (e != cudaSuccess) return e;
+  // not chained to its predecessor: the kernel behind it reads counts before its own wait
   kv_attn_tiles_kernel<D><<<dim3(g.hkv * p.splits * p.row_tiles, 1, g.B), THREADS, TileLayout<D>::ALLOC, s>>>(g, p, maps);
   return cudaGetLastError();
 }
