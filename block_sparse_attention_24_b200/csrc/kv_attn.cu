@@ -738,14 +738,12 @@ __global__ void __launch_bounds__(finish_threads(TW), TW == 1 ? 1 : 5) kv_finish
   const int h = blockIdx.y, b = blockIdx.z;
   const int i0 = (int)blockIdx.x < p.weight_blocks ? (int)blockIdx.x * TW : -1;  // negative: a block that joins
   int n_b, held, total, ps[TW];
-  // Before the wait: what the tile kernel, which is launched behind all that came
-  // before it, does not write.
+  after_predecessor();
   const int t0 = g.next_pos[b];
 #pragma unroll
   for (int k = 0; k < TW; ++k)
     ps[k] = i0 >= 0 && i0 + k < g.nb_cap ? g.pos[((long long)b * g.hkv + h) * g.nb_cap + i0 + k] : 0;
   const bool fine = kv_counts(g, b, h, p.n_q, p.n_new, p.pending, n_b, held, total);
-  after_predecessor();
   const int rows = n_b * p.group;
   if (!fine || n_b == 0) return;
   if (i0 < 0) {

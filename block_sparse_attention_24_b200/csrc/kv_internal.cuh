@@ -87,7 +87,7 @@ __device__ __forceinline__ bool kv_tile_seen(int p, int tile, int t_lo, int t_hi
 // A pool as a 2D map of bytes [rows, d], box [box_rows, d], swizzled over d bytes (64 or 128).
 CUresult encode_tensor_map_2d_u8(CUtensorMap* map, const void* base, uint64_t d, uint64_t rows, uint32_t box_rows);
 
-// The kernels (but for the tile kernel, see there) are launched so that each may be
+// The kernels are launched so that each may be
 // set up while the one before it in the stream ends: it waits here for that one's
 // results, before it reads or writes anything, and lets the next one do the same.
 __device__ __forceinline__ void after_predecessor() {

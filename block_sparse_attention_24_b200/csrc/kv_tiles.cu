@@ -147,6 +147,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   const int sp = blockIdx.x % p.splits, rest = blockIdx.x / p.splits, b = blockIdx.z;
   const int h = p.causal ? rest % g.hkv : rest / p.row_tiles;
   const int mt = p.row_tiles - 1 - (p.causal ? rest / g.hkv : rest % p.row_tiles);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   int n_b, held, total;
   const int t0 = g.next_pos[b];
   if (!kv_counts(g, b, h, p.n_q, p.n_new, p.pending, n_b, held, total)) return;
@@ -610,9 +611,8 @@ cudaError_t launch(const KvGeom& g, const KvAttnParams& p, cudaStream_t s) {
   static std::atomic<uint64_t> done{0};
   const cudaError_t e = allow_smem((const void*)kv_attn_tiles_kernel<D>, TileLayout<D>::ALLOC, done);
   if (e != cudaSuccess) return e;
-  // not chained to its predecessor: the kernel behind it reads counts before its own wait
-  kv_attn_tiles_kernel<D><<<dim3(g.hkv * p.splits * p.row_tiles, 1, g.B), THREADS, TileLayout<D>::ALLOC, s>>>(g, p, maps);
-  return cudaGetLastError();
+  return launch_chained(kv_attn_tiles_kernel<D>, dim3(g.hkv * p.splits * p.row_tiles, 1, g.B), THREADS,
+                        TileLayout<D>::ALLOC, s, g, p, maps);
 }
 
 }  // namespace
