@@ -416,7 +416,7 @@ def _expect(t, name: str, shape, dtype, device, contiguous: bool = True):
         raise ValueError(f"{name} must be contiguous")
 
 
-def _ptr(t, name: str, shape, dtype, device) -> int:
+def _checked(t, name: str, shape, dtype, device) -> int:
     if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.device == device and
             t.is_contiguous()):
         _expect(t, name, shape, dtype, device)
@@ -466,7 +466,7 @@ def _i32(x, name: str) -> int:
 
 
 def _n_new(cache: KVCache, n_new):
-    return None if n_new is None else _ptr(n_new, "n_new", (cache.B,), torch.int32, cache.device)
+    return None if n_new is None else _checked(n_new, "n_new", (cache.B,), torch.int32, cache.device)
 
 
 def veda_kv_append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, n_new: Optional[torch.Tensor] = None,
@@ -506,8 +506,8 @@ def veda_kv_attn(cache: KVCache, q: torch.Tensor, o: torch.Tensor, scale: float,
     qp, qs = _rows(q, "q", shape, cache)
     op, os_ = _rows(o, "o", shape, cache)
     dev = cache.device
-    lp = None if lse is None else _ptr(lse, "lse", (cache.B, heads, n), torch.float32, dev)
-    wp = None if weight is None else _ptr(weight, "weight", (cache.B, cache.heads_kv, cache.nb_cap), torch.float32, dev)
+    lp = None if lse is None else _checked(lse, "lse", (cache.B, heads, n), torch.float32, dev)
+    wp = None if weight is None else _checked(weight, "weight", (cache.B, cache.heads_kv, cache.nb_cap), torch.float32, dev)
     key = (heads, n, wp is not None)
     need = cache._ws_bytes.get(key)
     if need is None:

@@ -219,6 +219,13 @@ def test_stream_layer_workspaces_are_few():
         layer.workspace(1 << 23, False)
 
 
+def test_binding_defines_no_name_twice():
+    import ast
+    with open(V.__file__) as f:
+        names = [n.name for n in ast.parse(f.read()).body if isinstance(n, (ast.FunctionDef, ast.ClassDef))]
+    assert len(names) == len(set(names))
+
+
 # ------------------------------------------------------------------ oracle
 
 def test_oracle_codes_are_torchs():
