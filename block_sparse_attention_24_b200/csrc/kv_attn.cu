@@ -41,9 +41,12 @@ namespace {
 //                    softmax thread)
 // The CTAs that share a head's keys count themselves in `arrive`; the last one
 // joins their parts, and sums the tile weights.
-// Measured: 2 sequences x 24 heads x 80,640 keys, d = 128: 156 us, 6.35 TB/s (97%
+// Measured: 2 sequences x 24 heads x 80,640 keys, d = 128: 155 us, 6.4 TB/s (98%
 // of a measured copy); 16 sequences of up to 8,190 keys, 32/8 heads, with
-// weights: 47 us, 4.3 TB/s; 1,500 keys, 32/8 heads: 10.3 us, a chain of latencies.
+// weights: 46 us, 4.4 TB/s; 1,500 keys, 32/8 heads: 9.5 us, a chain of latencies.
+// A head's CTAs as a cluster that exchanges its parts through shared memory took
+// the same (1,500 keys) or more (window 2,048: 27 against 22 us; 80,640 keys: 223
+// against 154 us): clusters leave SM slots empty.
 // Up to 16 rows: at 32 rows and 16 x 8,190 keys two passes of this kernel would
 // take 170 us, the tile kernel takes 109.
 constexpr int FEW_ROWS = 16;

