@@ -738,3 +738,36 @@ def test_stream_layer_allocates_on_the_stream_of_the_step():
     layers[1].reset(stream=s)
     s.synchronize()
     assert int(layers[1].cache.len.sum()) == 0 and int(layers[1].cache.next_pos[0]) == 0
+
+
+@pytest.mark.parametrize("n,d,tile,heads,hkv", [(1, 64, 64, 8, 2), (1, 128, 128, 4, 4), (3, 128, 64, 12, 2), (40, 64, 64, 4, 1)])
+def test_steps_back_to_back_equal_steps_one_at_a_time(n, d, tile, heads, hkv):
+    """Kernels are set up while the one before them ends; each still sees all
+    that those before it wrote, in both directions and between kernels of other
+    kinds (the copies and fills here)."""
+    B, steps, keep = 3, 40, 4
+    got = []
+    for alone in (True, False):
+        c = V.KVCache(B, hkv, d, tile, keep + 2 + n // tile, DEV)
+        ws = workspace(c, heads, n, True)
+        news = torch.tensor([n, max(0, n - 1), n], dtype=torch.int32, device=DEV)
+        x = [bf16(1200 + i, steps, B, n, heads if i == 0 else hkv, d) for i in range(3)]
+        q = torch.empty((B, n, heads, d), dtype=torch.bfloat16, device=DEV)
+        outs = []
+        wait = torch.cuda.synchronize if alone else (lambda: None)
+        wait()
+        for t in range(steps):
+            o, lse = torch.zeros_like(q), torch.zeros((B, heads, n), device=DEV)
+            for call in (lambda: q.copy_(x[0][t]),
+                         lambda: V.veda_kv_append(c, x[1][t], x[2][t], n_new=news),
+                         lambda: V.veda_kv_attn(c, q, o, 0.1, ws, n_new=news, lse=lse, weight=c.weight, decay=0.9),
+                         lambda: q.zero_(),
+                         lambda: V.veda_kv_advance(c, n, n_new=news),
+                         lambda: V.veda_kv_evict(c, [keep] * hkv, 1, 2)):
+                call()
+                wait()
+            outs += [o, lse]
+        V.veda_kv_check_status(c)
+        got.append(outs + [c.k_scale, c.v_scale, c.table, c.pos, c.len, c.next_pos, c.weight])
+    for a, b in zip(*got):
+        assert torch.equal(a, b)
