@@ -29,7 +29,7 @@
 // Every wait is bounded, as in the other pipelines.
 // Measured: 3,840 x 34,560, 24 heads, d = 128: 1.66 ms, 980 TFLOP/s (a step of 256
 // rows x 128 keys takes ~3,680 clocks against 2,048 of MMA; the clock is held at
-// ~1.7 GHz by power); 2,048-token causal prompt, 32/8 heads: 66 us.
+// ~1.7 GHz by power); 2,048-token causal prompt, 32/8 heads: 65 us.
 #include "kv_attn.cuh"
 
 namespace veda {
@@ -57,11 +57,17 @@ struct TileLayout {
   static constexpr int OFF_W = OFF_V + VST * CB;
   static constexpr int OFF_META = OFF_W + WST * WB;
   static constexpr int OFF_BAR = OFF_META + MST * (int)sizeof(StepMeta);
-  static constexpr int NUM_BARS = KST + 2 * VST + WST + SDR + 2 + 2 + 2 + 1;
-  static constexpr int OFF_MISC = OFF_BAR + NUM_BARS * 8;
+  static constexpr int NUM_BARS = KST + 2 * VST + WST + SDR + 2 + 2 + 2 + 1;  // and one per softmax warp
+  static constexpr int OFF_MISC = OFF_BAR + (NUM_BARS + 8) * 8;
   static constexpr int ALLOC = OFF_MISC + 32 + 1024;
 };
 static_assert(sizeof(StepMeta) % 8 == 0, "barriers follow");
+
+// `bytes` (a multiple of 16) of a row to shared memory.
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, int bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                   smem_u32(dst)), "l"(src), "r"(bytes), "r"(smem_u32(bar)) : "memory");
+}
 
 // Token and head-of-group of a row, kept along as rows advance by a few (without a
 // loop, so that the accesses of several rows overlap).
@@ -137,6 +143,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     kv_attn_tiles_kernel(const KvGeom g, const KvAttnParams p, const __grid_constant__ KvMaps maps) {
   using Lay = TileLayout<D>;
   extern __shared__ uint8_t smem_raw[];
+  __shared__ int q_abort[8];
   __shared__ int sm_cnt[4];  // of kv_range, and the steps
   uint8_t* smem = smem_raw + (((smem_u32(smem_raw) + 1023u) & ~1023u) - smem_u32(smem_raw));
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
@@ -176,9 +183,33 @@ __global__ void __launch_bounds__(THREADS, 1)
   uint64_t* p_full = s_full + 2;          // [2], 128 arrivals
   uint64_t* pv_done = p_full + 2;         // [2]
   uint64_t* drain = pv_done + 2;
+  uint64_t* q_full = drain + 1;  // [8], the softmax warps' own
   StepMeta* meta = reinterpret_cast<StepMeta*>(smem + Lay::OFF_META);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Lay::OFF_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Lay::OFF_MISC + 4);
+  // A softmax warp's rows of Q, a copy each, to where V in fp16 will be: under way
+  // while the steps are found (2,048-token prompt: loads to registers, a batch of
+  // rows ahead, 66.0 us, copies 64.8).
+  uint8_t* q_raw = smem + Lay::OFF_W + warp * 32 * 2 * D;
+  bool ok = true;  // (the softmax warps')
+  if (mine) {
+    if (lane == 0) {
+      q_abort[warp] = 0;
+      mbar_init(q_full + warp, 1);
+      fence_mbar_init();
+      mbar_expect_tx(q_full + warp, max(0, min(32, rows - wrow)) * 2 * D);
+    }
+    __syncwarp();
+    if (wrow + lane < rows) {
+      const int tok = (wrow + lane) / p.group, gh = wrow + lane - tok * p.group;
+      bulk_load(q_raw + lane * 2 * D, p.q.p + b * p.q.sb + (long long)tok * p.q.sn + (long long)(h * p.group + gh) * p.q.sh,
+                2 * D, q_full + warp);
+    } else {
+#pragma unroll 1
+      for (int c = 0; c < D / 8; ++c) *reinterpret_cast<uint4*>(q_raw + lane * 2 * D + c * 16) = make_uint4(0, 0, 0, 0);
+    }
+  }
+
   // The steps are worked out by the warps that do not take Q apart meanwhile.
   KvRange rg{0, 0, 0};
   int s_lo = 0, n_steps = 0;
@@ -236,31 +267,20 @@ __global__ void __launch_bounds__(THREADS, 1)
     tmem_relinquish();
   } else if (mine) {
     // Q in its two e4m3 parts, a few rows at a time: their chains of shuffles and
-    // conversions overlap, and the next rows are on their way.
+    // conversions overlap.
     constexpr int BATCH = 4;
-    const __nv_bfloat16* src = p.q.p + b * p.q.sb + (long long)h * p.group * p.q.sh + c8 * 8;
-    RowStep at(wrow + sub, RPI, p.group);
-    uint4 next[BATCH];
-    auto load = [&](int j0) {
-#pragma unroll
-      for (int y = 0; y < BATCH; ++y) {
-        next[y] = make_uint4(0, 0, 0, 0);
-        if (wrow + sub + (j0 + y) * RPI < rows)
-          next[y] = *reinterpret_cast<const uint4*>(src + (long long)at.tok * p.q.sn + (long long)at.gh * p.q.sh);
-        at.advance();
-      }
-    };
-    load(0);
+    __syncwarp();
+    ok = __all_sync(0xffffffffu, mbar_wait(q_full + warp, 0, q_abort + warp, g.dev_status));
+    if (!ok) mbar_wait_drain(q_full + warp, 0, VEDA_WAIT_LIMIT_NS);
 #pragma unroll 1
     for (int j0 = 0; j0 < ITERS; j0 += BATCH) {
       uint4 qw[BATCH];
       uint32_t top[BATCH];
 #pragma unroll
       for (int y = 0; y < BATCH; ++y) {
-        qw[y] = next[y];
+        qw[y] = *reinterpret_cast<const uint4*>(q_raw + ((j0 + y) * RPI + sub) * 2 * D + c8 * 16);
         top[y] = max(max(bf16x2_top(qw[y].x), bf16x2_top(qw[y].y)), max(bf16x2_top(qw[y].z), bf16x2_top(qw[y].w)));
       }
-      if (j0 + BATCH < ITERS) load(j0 + BATCH);
 #pragma unroll
       for (int d = 1; d < LPR; d <<= 1)
 #pragma unroll
@@ -433,10 +453,10 @@ __global__ void __launch_bounds__(THREADS, 1)
     const uint32_t lane_addr = tmem + ((uint32_t)((warp % 4) * 32) << 16);
     const uint32_t s_col = rt * BN, o_col = 2 * BN + rt * BN;
     float m = -INFINITY, l = 0.f;
-    bool ok = true;
+    if (!ok) *abort_flag = 1;
     const int first = alt ? rt : 0, stride = alt ? 2 : 1;
     const int n_mine = mine ? (n_steps - first + stride - 1) / stride : 0;  // steps of this row tile
-    for (int j = 0; j < n_mine; ++j) {
+    for (int j = 0; ok && j < n_mine; ++j) {
       const int e = first + j * stride;
       if (!__all_sync(0xffffffffu, mbar_wait(s_full + rt, j & 1, abort_flag, g.dev_status))) { ok = false; break; }
       if (wrow >= rows) {  // none of the warp's rows is one: its P may be anything
