@@ -47,9 +47,9 @@ __device__ __forceinline__ uint32_t codes_moved(uint32_t c, float f) {
 // old codes moved to it (rounded once more where it grew), new ones quantised,
 // the rows behind the last token zeroed. The tile's bf16 rows are held in
 // registers between the maximum and the rounding, so they are read once:
-// 2 bytes in and 1 out per value. 3,840 tokens of 24 heads, d = 128: 15.2 us,
-// 4.7 TB/s (of 6.5 measured for a copy); five to seven CTAs per SM instead of
-// four, by fewer registers, took 16.5 to 22.3 us where four took 16.6.
+// 2 bytes in and 1 out per value. 3,840 tokens of 24 heads, d = 128: 14.7 us,
+// 4.8 TB/s (of 6.5 measured for a copy); five to seven CTAs per SM instead of
+// four, by fewer registers, took 16.5 to 22.3 us where four took 16.6; 128 or 512 threads take 19.
 template <int D>
 __global__ void __launch_bounds__(APPEND_THREADS)
     kv_append_kernel(const KvGeom g, const KvRows kr, const KvRows vr, const int n, const int32_t* n_new) {
@@ -77,8 +77,8 @@ __global__ void __launch_bounds__(APPEND_THREADS)
     val[j][0] = val[j][1] = make_uint4(0, 0, 0, 0);
     if (r < g.tile && t >= 0 && t < n_b) {
       const uint4* q = reinterpret_cast<const uint4*>(src + (long long)t * x.sn + c * 16);
-      val[j][0] = q[0];
-      val[j][1] = q[1];
+      val[j][0] = __ldcs(q);  // read once
+      val[j][1] = __ldcs(q + 1);
     }
   }
   if (slot < 0 || slot >= g.n_slots) {
