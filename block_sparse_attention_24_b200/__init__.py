@@ -31,7 +31,7 @@ EXPORTED = ("veda_layout", "veda_permute", "veda_trippool", "veda_permute_trippo
             "veda_topk_mask", "veda_tile_scores_topk", "veda_tile_scores_heads", "veda_topk_mask_heads", "veda_score_cache_step", "veda_score_cache_ws_bytes", "veda_sparse_attn", "veda_sparse_attn_unpermute", "veda_sparse_attn_tokens", "veda_full_attn_tilemax", "veda_full_attn_tilemax_ws_bytes", "veda_tilemap_kl", "veda_tilemap_recall",
             "veda_check_status",
             "veda_estimator_grad", "veda_estimator_grad_ws_bytes", "veda_output_sq_error", "veda_selftest_wait_timeout", "veda_last_error",
-            "veda_kv_append", "veda_kv_advance", "veda_kv_attn", "veda_kv_attn_ws_bytes", "veda_kv_evict", "veda_kv_check_status")
+            "veda_kv_append", "veda_kv_append_pending", "veda_kv_advance", "veda_kv_attn", "veda_kv_attn_ws_bytes", "veda_kv_evict", "veda_kv_check_status")
 
 
 class VedaError(RuntimeError):
@@ -63,6 +63,10 @@ class _KvCache(ctypes.Structure):
     _fields_ = ([(n, ctypes.c_int32) for n in ("B", "heads_kv", "d", "tile", "n_slots", "nb_cap")] +
                 [(n, ctypes.c_void_p) for n in ("k8", "v8", "table", "pos", "k_scale", "v_scale", "weight", "len",
                                                 "next_pos", "arrive", "dev_status")])
+
+
+class _KvTail(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("codes", "key", "scale")]
 
 
 _P = ctypes.c_void_p
@@ -100,6 +104,7 @@ _lib.veda_check_status.argtypes = [_LP, _P]
 _lib.veda_selftest_wait_timeout.argtypes = [_LP, ctypes.c_uint32, _P]
 _CP = ctypes.POINTER(_KvCache)
 _lib.veda_kv_append.argtypes = [_CP, _P, _P, _P, _P, _I, _P, _P]
+_lib.veda_kv_append_pending.argtypes = [_CP, ctypes.POINTER(_KvTail), _P, _P, _P, _P, _I, _P, _P]
 _lib.veda_kv_advance.argtypes = [_CP, _I, _P, _P]
 _lib.veda_kv_attn.argtypes = [_CP, _P, _P, _I, _I, _P, _I, _I, _I, _I, _F, _P, _P, _P, _P, _F, _P, _P]
 _lib.veda_kv_attn_ws_bytes.argtypes = [_CP, _I, _I, _I]
@@ -346,7 +351,9 @@ class KVCache:
     next_pos [B] (int32). Those not given are allocated: an empty cache whose
     table names slot (b * heads_kv + h) * nb_cap + i for tile i. Tensors are
     used where they are (no copy) and are the caller's to look at and to
-    change, in place, between calls."""
+    change, in place, between calls. tail_codes [B, heads_kv, 2, tile, d],
+    tail_key and tail_scale are the library's own: what the tail tiles were
+    before pending tokens raised their scales (veda_kv_tail)."""
 
     _META = (("table", torch.int32), ("pos", torch.int32), ("k_scale", torch.float32), ("v_scale", torch.float32),
              ("weight", torch.float32))
@@ -392,6 +399,11 @@ class KVCache:
                            *[getattr(self, n).data_ptr() for n in ("k8", "v8", "table", "pos", "k_scale", "v_scale",
                                                                    "weight", "len", "next_pos", "_arrive",
                                                                    "status")])
+        self.tail_codes = torch.zeros((B, heads_kv, 2, tile, d), dtype=torch.uint8, device=device).view(torch.float8_e4m3fn)
+        self.tail_key = torch.zeros((B, heads_kv, 2, 4), dtype=torch.int32, device=device)
+        self.tail_scale = torch.zeros((B, heads_kv, 2, 2), dtype=torch.float32, device=device)
+        self._tail = _KvTail(self.tail_codes.data_ptr(), self.tail_key.data_ptr(), self.tail_scale.data_ptr())
+        self.tail_ref = ctypes.byref(self._tail)
         self._ws_bytes = {}  # of veda_kv_attn, by (heads, n_q, with weights)
         self.ref = ctypes.byref(self._c)
 
@@ -473,14 +485,15 @@ def veda_kv_append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, n_new: Opti
                    stream=None):
     """K and V [B, n, heads_kv, d] of n new tokens into the cache, as pending
     tokens behind those it holds (n_new [B]: how many of each sequence's rows
-    are real)."""
+    are real), in the place of those that are pending."""
     if not isinstance(k, torch.Tensor) or k.dim() != 4:
         raise ValueError("k must be a [B, n, heads_kv, d] tensor")
     n = k.shape[1]
     shape = (cache.B, n, cache.heads_kv, cache.d)
     kp, ks = _rows(k, "k", shape, cache)
     vp, vs = _rows(v, "v", shape, cache)
-    _kv_call(cache, stream, _lib.veda_kv_append, cache.ref, kp, ks, vp, vs, n, _n_new(cache, n_new))
+    _kv_call(cache, stream, _lib.veda_kv_append_pending, cache.ref, cache.tail_ref, kp, ks, vp, vs, n,
+             _n_new(cache, n_new))
 
 
 def veda_kv_advance(cache: KVCache, n: int, n_new: Optional[torch.Tensor] = None, stream=None):

@@ -657,14 +657,31 @@ int veda_check_status(const veda_layer* L, cudaStream_t stream) {
 
 int veda_kv_append(const veda_kv_cache* C, const void* k, const int64_t* k_strides, const void* v,
                    const int64_t* v_strides, int32_t n, const int32_t* n_new, cudaStream_t stream) {
+  return veda_kv_append_pending(C, nullptr, k, k_strides, v, v_strides, n, n_new, stream);
+}
+
+int veda_kv_append_pending(const veda_kv_cache* C, const veda_kv_tail* tail, const void* k, const int64_t* k_strides,
+                           const void* v, const int64_t* v_strides, int32_t n, const int32_t* n_new,
+                           cudaStream_t stream) {
   veda::KvGeom g;
   VEDA_TRY(build_kv(C, &g, "cache"));
   VEDA_TRY(check_rows(n, "n"));
-  if (n == 0) return after_launch(cudaSuccess, "");
-  veda::KvRows kr, vr;
-  VEDA_TRY(kv_rows(k, k_strides, n, g.hkv, g.d, "k", &kr));
-  VEDA_TRY(kv_rows(v, v_strides, n, g.hkv, g.d, "v", &vr));
-  return after_launch(veda::launch_kv_append(g, kr, vr, n, n_new, stream), "veda_kv_append");
+  veda::KvTail t = {};
+  if (tail) {
+    VEDA_TRY(check_ptr(tail->codes, "tail codes"));
+    VEDA_TRY(check_ptr(tail->key, "tail key"));
+    VEDA_TRY(check_ptr(tail->scale, "tail scale"));
+    t.codes = static_cast<uint8_t*>(tail->codes);
+    t.key = reinterpret_cast<int4*>(tail->key);
+    t.scale = reinterpret_cast<float2*>(tail->scale);
+  }
+  if (n == 0 && !tail) return after_launch(cudaSuccess, "");
+  veda::KvRows kr = {}, vr = {};
+  if (n > 0) {
+    VEDA_TRY(kv_rows(k, k_strides, n, g.hkv, g.d, "k", &kr));
+    VEDA_TRY(kv_rows(v, v_strides, n, g.hkv, g.d, "v", &vr));
+  }
+  return after_launch(veda::launch_kv_append(g, t, kr, vr, n, n_new, stream), "veda_kv_append");
 }
 
 int veda_kv_advance(const veda_kv_cache* C, int32_t n, const int32_t* n_new, cudaStream_t stream) {

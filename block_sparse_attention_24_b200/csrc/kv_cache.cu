@@ -42,6 +42,9 @@ __device__ __forceinline__ uint32_t codes_moved(uint32_t c, float f) {
   const float2 a = unpack_e4m3x2((uint16_t)c), b = unpack_e4m3x2((uint16_t)(c >> 16));
   return pack_e4m3x4(a.x * f, a.y * f, b.x * f, b.y * f);
 }
+__device__ __forceinline__ uint4 codes_moved(uint4 w, float f) {
+  return make_uint4(codes_moved(w.x, f), codes_moved(w.y, f), codes_moved(w.z, f), codes_moved(w.w, f));
+}
 
 // One tile of K or of V of one head: scale' = max(old scale, the new tokens'),
 // old codes moved to it (rounded once more where it grew), new ones quantised,
@@ -50,9 +53,17 @@ __device__ __forceinline__ uint32_t codes_moved(uint32_t c, float f) {
 // 2 bytes in and 1 out per value. 3,840 tokens of 24 heads, d = 128: 14.7 us,
 // 4.8 TB/s (of 6.5 measured for a copy); five to seven CTAs per SM instead of
 // four, by fewer registers, took 16.5 to 22.3 us where four took 16.6; 128 or 512 threads take 19.
+//
+// The older codes of a tile that tokens join are rounded in place, and those
+// tokens are only pending: the codes and the scale as they were go to `tail`
+// (by the one CTA that has this tile), and the next append starts from them. It
+// knows them to be the tile's by the slot, the row count and next_pos, all as
+// they were, and by the scale and codes there, which must be what the raise
+// left: otherwise tokens were taken in since, or put there by the caller.
 template <int D>
 __global__ void __launch_bounds__(APPEND_THREADS)
-    kv_append_kernel(const KvGeom g, const KvRows kr, const KvRows vr, const int n, const int32_t* n_new) {
+    kv_append_kernel(const KvGeom g, const KvTail tail, const KvRows kr, const KvRows vr, const int n,
+                     const int32_t* n_new) {
   constexpr int VPR = D / 16;                          // 16-value vectors per row
   constexpr int PT = 128 * VPR / APPEND_THREADS;       // vectors per thread at tile 128
   const int h = blockIdx.y >> 1, is_v = blockIdx.y & 1, b = blockIdx.z;
@@ -61,14 +72,20 @@ __global__ void __launch_bounds__(APPEND_THREADS)
   if (!kv_counts(g, b, h, n, n_new, true, n_b, held, total)) return;
   const int i = held / g.tile + blockIdx.x;            // the tile's place in the table
   const int row0 = i * g.tile - held;                  // new token in its first row (negative: that row is older)
-  if (n_b == 0 || row0 >= n_b) return;
+  const bool fresh = row0 >= 0, first = blockIdx.x == 0 && tail.codes;
+  const long long kept = ((long long)b * g.hkv + h) * 2 + is_v;
+  if (n_b == 0 ? !first || fresh : row0 >= n_b) return;
   const long long entry = ((long long)b * g.hkv + h) * g.nb_cap + i;
   float* scale = (is_v ? g.v_scale : g.k_scale) + entry;
   const KvRows& x = is_v ? vr : kr;
   const __nv_bfloat16* src = x.p + b * x.sb + h * x.sh;
-  const bool fresh = row0 >= 0;
-  const int slot = g.table[entry];  // in flight with the rows
-  const float s_old = fresh ? 0.f : *scale;
+  // in flight with the rows
+  const int slot = g.table[entry];
+  float s_old = fresh ? 0.f : *scale;
+  const bool joins = first && !fresh;
+  const int4 key = joins ? tail.key[kept] : make_int4(0, 0, 0, 0);
+  const float2 was = joins ? tail.scale[kept] : make_float2(0.f, 0.f);
+  const int next = joins || fresh ? g.next_pos[b] : 0;
 
   uint4 val[PT][2];
 #pragma unroll
@@ -82,10 +99,25 @@ __global__ void __launch_bounds__(APPEND_THREADS)
     }
   }
   if (slot < 0 || slot >= g.n_slots) {
-    if (threadIdx.x == 0) report(g.dev_status, VEDA_ERR_BAD_INDEX);
+    if (threadIdx.x == 0 && n_b > 0) report(g.dev_status, VEDA_ERR_BAD_INDEX);
     return;
   }
   uint8_t* codes = (is_v ? g.v8 : g.k8) + (long long)slot * g.tile * D;
+  uint8_t* const kept_codes = tail.codes + kept * g.tile * D;
+  bool back = false;  // the kept codes and scale are the committed ones
+  if (joins && key.x == -row0 && key.y == slot && key.z == next && __float_as_uint(was.y) == __float_as_uint(s_old)) {
+    const float f = was.x * (1.0f / was.y);
+    bool same = true;
+#pragma unroll 1
+    for (int vec = threadIdx.x; vec < -row0 * VPR; vec += APPEND_THREADS) {
+      const uint4 w = reinterpret_cast<const uint4*>(codes)[vec];
+      uint4 m = reinterpret_cast<const uint4*>(kept_codes)[vec];
+      if (was.y == was.y) m = codes_moved(m, f);
+      same = same && w.x == m.x && w.y == m.y && w.z == m.z && w.w == m.w;
+    }
+    back = __syncthreads_and(same);
+    if (back) s_old = was.x;
+  }
   // the largest |x| by its bits: infinities and NaN come out above every finite value
   uint32_t top = 0;
 #pragma unroll
@@ -100,10 +132,13 @@ __global__ void __launch_bounds__(APPEND_THREADS)
   __syncthreads();
 #pragma unroll
   for (int w = 0; w < APPEND_THREADS / 32; ++w) top = max(top, warp_top[w]);
+  if (n_b == 0 && !back) return;
   const float s_new = scale_of(__uint_as_float(top));
-  const float s = fresh ? s_new : ((s_new != s_new || s_old != s_old) ? s_new + s_old : fmaxf(s_new, s_old));
+  float s = fresh ? s_new : ((s_new != s_new || s_old != s_old) ? s_new + s_old : fmaxf(s_new, s_old));
+  if (n_b == 0) s = s_old;
   const bool fine = s == s;
   const float inv = fine ? 1.0f / s : 0.f;
+  const bool raised = !fresh && s_old == s_old && s != s_old;
 
 #pragma unroll
   for (int j = 0; j < PT; ++j) {
@@ -117,16 +152,22 @@ __global__ void __launch_bounds__(APPEND_THREADS)
         o = make_uint4(codes_of(a.x, a.y, inv), codes_of(a.z, a.w, inv), codes_of(e.x, e.y, inv), codes_of(e.z, e.w, inv));
       }
       *dst = o;
-    } else if (fine && s != s_old) {
-      const float f = s_old * inv;
-      const uint4 w = *dst;
-      *dst = make_uint4(codes_moved(w.x, f), codes_moved(w.y, f), codes_moved(w.z, f), codes_moved(w.w, f));
+    } else if (raised || back) {
+      uint4* old = reinterpret_cast<uint4*>(kept_codes + r * D + c * 16);
+      uint4 w = back ? *old : *dst;
+      if (raised && first && !back) *old = w;
+      if (raised && fine) w = codes_moved(w, s_old * inv);
+      *dst = w;
     }
   }
   if (threadIdx.x == 0) {
     *scale = s;
+    if (first) {
+      tail.key[kept] = raised ? make_int4(-row0, slot, next, 0) : make_int4(0, 0, 0, 0);
+      if (raised) tail.scale[kept] = make_float2(s_old, s);
+    }
     if (fresh && !is_v) {
-      g.pos[entry] = g.next_pos[b] + row0;
+      g.pos[entry] = next + row0;
       if (g.weight) g.weight[entry] = 0.f;
     }
   }
@@ -311,12 +352,12 @@ cudaError_t launch_evict(const KvGeom& g, const KvKeep& keeps, int sink, int rec
 
 }  // namespace
 
-cudaError_t launch_kv_append(const KvGeom& g, const KvRows& k, const KvRows& v, int n, const int32_t* n_new,
-                             cudaStream_t s) {
+cudaError_t launch_kv_append(const KvGeom& g, const KvTail& tail, const KvRows& k, const KvRows& v, int n,
+                             const int32_t* n_new, cudaStream_t s) {
   const long long tiles = ((long long)n + g.tile - 2) / g.tile + 1;  // n tokens from any row of a tile on
   const dim3 grid((unsigned)(tiles < g.nb_cap ? tiles : g.nb_cap), 2 * g.hkv, g.B);
-  return launch_chained(g.d == 128 ? kv_append_kernel<128> : kv_append_kernel<64>, grid, APPEND_THREADS, 0, s, g, k, v, n,
-                        n_new);
+  return launch_chained(g.d == 128 ? kv_append_kernel<128> : kv_append_kernel<64>, grid, APPEND_THREADS, 0, s, g, tail, k,
+                        v, n, n_new);
 }
 
 cudaError_t launch_kv_advance(const KvGeom& g, int n, const int32_t* n_new, cudaStream_t s) {

@@ -29,6 +29,13 @@ struct KvGeom {
   int32_t* dev_status;
 };
 
+// What the tail tiles were before pending tokens raised their scales (veda_kv_tail); codes NULL: not kept.
+struct KvTail {
+  uint8_t* codes;  // [B, hkv, 2 (K, V), tile, d]
+  int4* key;       // [B, hkv, 2]: rows (0: nothing kept), slot, next_pos
+  float2* scale;   // [B, hkv, 2]: before, raised
+};
+
 // bf16 rows [B, n, heads, d] with element strides (the last dimension is contiguous).
 struct KvRows {
   const __nv_bfloat16* p;
@@ -119,8 +126,8 @@ inline cudaError_t allow_smem(const void* kernel, int bytes, std::atomic<uint64_
   return e;
 }
 
-cudaError_t launch_kv_append(const KvGeom& g, const KvRows& k, const KvRows& v, int n, const int32_t* n_new,
-                             cudaStream_t s);
+cudaError_t launch_kv_append(const KvGeom& g, const KvTail& tail, const KvRows& k, const KvRows& v, int n,
+                             const int32_t* n_new, cudaStream_t s);
 cudaError_t launch_kv_advance(const KvGeom& g, int n, const int32_t* n_new, cudaStream_t s);
 cudaError_t launch_kv_evict(const KvGeom& g, const int32_t* keep, int sink, int recent, const KvGeom& out,
                             cudaStream_t s);

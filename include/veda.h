@@ -369,7 +369,8 @@ int veda_output_sq_error(const veda_layer* L, const void* a, const void* b, floa
  * A step is append, attention, advance: the new tokens are pending (written
  * behind the len tokens and seen by attention) until veda_kv_advance takes
  * them in, so appending again replaces them, as when a chunk's K and V change
- * from one denoising step to the next.
+ * from one denoising step to the next (veda_kv_append_pending; an append of no
+ * tokens drops them).
  *
  * n_new (may be NULL = n for all): DEVICE int32 [B], the number of rows of
  * each sequence that are real in a padded batch, 0 <= n_new[b] <= n. A head
@@ -399,10 +400,28 @@ typedef struct {
  * not finite or above 448 * 2^80; codes are x / s rounded to nearest even.
  * Tokens that join a tile already begun raise its scale at most: the older
  * codes are then rounded once more, to the new scale (exact for all but
- * values near e4m3's subnormals). Rows of a touched tile behind the last
- * token become zero; a tile that is begun gets its pos, and weight 0. */
+ * values near e4m3's subnormals), and where a new token has no scale the older
+ * ones have none either. Rows of a touched tile behind the last token become
+ * zero; a tile that is begun gets its pos, and weight 0.
+ *
+ * veda_kv_append starts from the tail tile as it is, so what tokens that are
+ * replaced did to the scale of committed ones stays: it is for tokens that are
+ * taken in. veda_kv_append_pending keeps in `tail` what the tail tiles were
+ * before they were raised, and starts from that as long as the tokens have not
+ * been taken in: appended again, or dropped by an append of n = 0 or
+ * n_new[b] = 0, pending tokens leave nothing behind. (While they are pending,
+ * the committed tokens of their tile are read at the scale that fits both.)
+ * tail NULL: as veda_kv_append. */
+typedef struct {
+  void* codes;    /* [B, heads_kv, 2, tile, d]: of K and of V */
+  int32_t* key;   /* [B, heads_kv, 2, 4], zero before first use: rows, slot, next_pos */
+  float* scale;   /* [B, heads_kv, 2, 2]: before, and raised */
+} veda_kv_tail;   /* DEVICE memory, one per cache, 16-byte aligned */
 int veda_kv_append(const veda_kv_cache* C, const void* k, const int64_t* k_strides, const void* v,
                    const int64_t* v_strides, int32_t n, const int32_t* n_new, cudaStream_t stream);
+int veda_kv_append_pending(const veda_kv_cache* C, const veda_kv_tail* tail, const void* k, const int64_t* k_strides,
+                           const void* v, const int64_t* v_strides, int32_t n, const int32_t* n_new,
+                           cudaStream_t stream);
 
 /* Takes the n pending tokens in: len[b, h] += n_new[b], next_pos[b] +=
  * n_new[b]. */

@@ -34,21 +34,40 @@ def scale_of(amax: float) -> float:
 
 
 class Cache:
-    """codes k8/v8 [n_slots, tile, d] as fp64 values of the codes."""
+    """codes k8/v8 [n_slots, tile, d] as fp64 values of the codes. tail_*: of
+    each head's K and V, the codes and the scale of the tail tile's committed
+    tokens as they were before pending ones raised its scale, the raised scale,
+    and (rows, slot, next_pos, 0) to know that tile by (zeros: nothing)."""
 
-    FIELDS = ("k8", "v8", "table", "pos", "k_scale", "v_scale", "weight", "len", "next_pos")
+    FIELDS = ("k8", "v8", "table", "pos", "k_scale", "v_scale", "weight", "len", "next_pos", "tail_codes", "tail_key",
+              "tail_scale")
+    FLOATS = ("k8", "v8", "k_scale", "v_scale", "weight", "tail_codes", "tail_scale")
 
     def __init__(self, tile: int, **arrays):
         self.tile = tile
+        self.B, self.hkv, self.nb_cap = np.shape(arrays["table"])
+        tails = {"tail_codes": (tile, np.shape(arrays["k8"])[-1]), "tail_key": (4,), "tail_scale": (2,)}
+        for f, shape in tails.items():
+            arrays.setdefault(f, np.zeros((self.B, self.hkv, 2) + shape))
         for f in self.FIELDS:
-            a = np.array(arrays[f])
-            setattr(self, f, a.astype(np.float64) if f in ("k8", "v8", "k_scale", "v_scale", "weight") else
-                    a.astype(np.int64))
-        self.B, self.hkv, self.nb_cap = self.table.shape
+            setattr(self, f, np.array(arrays[f]).astype(np.float64 if f in self.FLOATS else np.int64))
 
     def count(self, b, h, n):
         t = self.len[b, h] + n
         return int(t) if 0 <= self.len[b, h] and n >= 0 and t <= self.nb_cap * self.tile else None
+
+    def committed(self, b, h, x, codes, scale):
+        """Codes of the committed rows of the head's tail tile and their scale,
+        without what pending tokens did to them; whether those had done any."""
+        i, r0 = divmod(int(self.len[b, h]), self.tile)
+        slot, now = self.table[b, h, i], scale[b, h, i]
+        (rows, at, pos, _), (was, raised) = self.tail_key[b, h, x], self.tail_scale[b, h, x]
+        if (rows, at, pos) == (r0, slot, self.next_pos[b]) and np.array_equal(raised, now, equal_nan=True):
+            kept = self.tail_codes[b, h, x, :r0]
+            moved = kept if math.isnan(raised) else nearest_e4m3(kept * (was / raised))
+            if np.array_equal(moved, codes[slot, :r0], equal_nan=True):
+                return kept, was, True
+        return codes[slot, :r0].copy(), now, False
 
     def append(self, k, v, news):
         """k, v [B, n, hkv, d] fp64."""
@@ -56,29 +75,44 @@ class Cache:
         for b in range(self.B):
             for h in range(self.hkv):
                 total = self.count(b, h, news[b])
-                if total is None or news[b] == 0 or news[b] > k.shape[1]:
+                if total is None or news[b] > k.shape[1]:
                     continue
                 held = int(self.len[b, h])
+                if news[b] == 0:
+                    i, r0 = divmod(held, T)
+                    slot = self.table[b, h, i] if r0 else -1
+                    if not 0 <= slot < len(self.k8):
+                        continue
+                    for x, codes, scale in ((0, self.k8, self.k_scale), (1, self.v8, self.v_scale)):
+                        kept, was, some = self.committed(b, h, x, codes, scale)
+                        if some:
+                            codes[slot, :r0], codes[slot, r0:], scale[b, h, i] = kept, 0.0, was
+                            self.tail_key[b, h, x] = 0
+                    continue
                 for i in range(held // T, -(-total // T)):
                     lo, hi = max(held, i * T), min(total, (i + 1) * T)
                     slot = self.table[b, h, i]
                     if not 0 <= slot < len(self.k8):
                         continue
                     fresh = lo == i * T
-                    for x, codes, scale in ((k, self.k8, self.k_scale), (v, self.v8, self.v_scale)):
-                        rows = x[b, lo - held:hi - held, h]
+                    for x, new, codes, scale in ((0, k, self.k8, self.k_scale), (1, v, self.v8, self.v_scale)):
+                        rows = new[b, lo - held:hi - held, h]
                         with np.errstate(invalid="ignore"):
                             amax = np.max(np.abs(rows))
-                        s, old = scale_of(amax), scale[b, h, i]
-                        if not fresh:
-                            s = math.nan if math.isnan(s) or math.isnan(old) else max(s, old)
+                        s = scale_of(amax)
                         r0, r1 = lo - i * T, hi - i * T
-                        if math.isnan(s):
-                            codes[slot, r0:r1] = 0.0
-                        else:
-                            if s != old and not fresh:
-                                codes[slot, :r0] = nearest_e4m3(codes[slot, :r0] * (old / s))
-                            codes[slot, r0:r1] = nearest_e4m3(rows / s)
+                        if i == held // T:
+                            key = np.zeros(4, np.int64)
+                        if not fresh:
+                            kept, old, _ = self.committed(b, h, x, codes, scale)
+                            s = math.nan if math.isnan(s) or math.isnan(old) else max(s, old)
+                            if s != old and not math.isnan(old):
+                                self.tail_codes[b, h, x, :r0], self.tail_scale[b, h, x] = kept, (old, s)
+                                key[:3] = r0, slot, self.next_pos[b]
+                            codes[slot, :r0] = kept if math.isnan(s) or s == old else nearest_e4m3(kept * (old / s))
+                        if i == held // T:
+                            self.tail_key[b, h, x] = key
+                        codes[slot, r0:r1] = 0.0 if math.isnan(s) else nearest_e4m3(rows / s)
                         codes[slot, r1:] = 0.0
                         scale[b, h, i] = s
                     if fresh:

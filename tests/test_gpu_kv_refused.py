@@ -1,0 +1,101 @@
+"""Steps that the 8-bit K/V tile cache cannot hold: refused whole, sequence by
+sequence, and without a trace."""
+import numpy as np
+import pytest
+import torch
+
+import block_sparse_attention_24_b200 as V
+from oracle.kv_oracle import Cache
+from tests.test_gpu_kv_cache import DEV, assert_same_state, bad_status, bf16, check_attention, oracle_of, random_cache, workspace
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("n,heads", [(100, 4), (3, 4)])
+def test_a_sequence_is_refused_as_a_whole(n, heads):
+    """One head of two is too full (eviction keeps more of its tiles). Were the
+    other served, or the position moved on, the heads would disagree about
+    where the next tokens stand."""
+    hkv, d, tile = 2, 64, 64
+    c = random_cache(1, 2, hkv, d, tile, 4, [254, 40])
+    V.veda_kv_evict(c, [4, 2], 1, 1)
+    assert c.len.tolist() == [[254, 126], [40, 40]]
+    want, next_pos = oracle_of(c), c.next_pos.tolist()
+    k, q = bf16(2, 2, n, hkv, d), bf16(3, 2, n, heads, d)
+    o, lse = torch.full_like(q, 5.0), torch.full((2, heads, n), 5.0, device=DEV)
+    V.veda_kv_append(c, k, k)
+    bad_status(c)
+    want.append(np.array(k.double().cpu()), np.array(k.double().cpu()), [n, n])
+    assert_same_state(c, want)
+    w = c.weight.clone()
+    V.veda_kv_attn(c, q, o, 0.125, workspace(c, heads, n, True), lse=lse, weight=c.weight)
+    bad_status(c)
+    assert (o[0] == 5).all() and (lse[0] == 5).all() and torch.equal(c.weight[0], w[0])
+    assert not (o[1] == 5).any() and not (lse[1] == 5).any()
+    V.veda_kv_advance(c, n)
+    bad_status(c)
+    assert c.len.tolist() == [[254, 126], [40 + n, 40 + n]]
+    assert c.next_pos.tolist() == [next_pos[0], next_pos[1] + n]
+    # with room made, the next tokens stand where the queries take them to be
+    V.veda_kv_evict(c, [2, 2], 1, 1)
+    V.veda_kv_append(c, k, k)
+    for b in range(2):
+        for h in range(hkv):
+            held = int(c.len[b, h])
+            assert int(c.pos[b, h, held // tile]) + held % tile == int(c.next_pos[b])
+    check_attention(c, q, window=n // 2 + 1)
+    check_attention(c, q, window=n + 5, sinks=3, causal=False)
+
+
+def test_counts_of_all_heads_decide():
+    """A head of many (more than a warp has lanes), first or last, without
+    pending tokens as well."""
+    hkv, d, tile = 100, 64, 64
+    for head in (0, 31, 32, 99):
+        c = random_cache(4, 1, hkv, d, tile, 2, [64])
+        c.len[0, head] = 128
+        k, q = bf16(5, 1, 30, hkv, d), bf16(6, 1, 30, hkv, d)
+        before = {f: getattr(c, f).clone() for f in Cache.FIELDS}
+        V.veda_kv_append(c, k, k)
+        bad_status(c)
+        V.veda_kv_advance(c, 30)
+        bad_status(c)
+        for f, t in before.items():
+            assert torch.equal(t.view(torch.uint8), getattr(c, f).view(torch.uint8)), f
+        for rows in (30, 1):
+            o = torch.full_like(q, 5.0)[:, :rows].contiguous()
+            V.veda_kv_attn(c, q[:, :rows].contiguous(), o, 0.125, workspace(c, hkv, rows, False))
+            bad_status(c)
+            assert (o == 5).all()
+            V.veda_kv_attn(c, q[:, :rows].contiguous(), o, 0.125, workspace(c, hkv, rows, False), pending=False)
+            V.veda_kv_check_status(c)
+            assert not (o == 5).any()
+        c.len[0, head] = -1
+        o = torch.full_like(q, 5.0)
+        V.veda_kv_attn(c, q, o, 0.125, workspace(c, hkv, 30, False), pending=False)
+        bad_status(c)
+        assert (o == 5).all()
+
+
+@pytest.mark.parametrize("keep", [None, 2])
+def test_a_step_past_the_capacity_returns_no_old_memory(keep):
+    from block_sparse_attention_24_b200.stream import VedaStream
+    n = 70
+    layer = VedaStream(2, 4, 2, 64, 64, 128, DEV, keep=keep, sink_tiles=0)
+    q, k = bf16(10, 2, n, 4, 64), bf16(11, 2, n, 2, 64)
+    news = torch.tensor([n, 20], dtype=torch.int32, device=DEV)
+    assert layer.step(q, k, k, n_new=news).shape == q.shape
+    layer.check_status()
+    for _ in range(2):
+        junk = [torch.full_like(q, 7.0) for _ in range(4)]
+        del junk
+        o = layer.step(q, k, k, n_new=news)
+        with pytest.raises(V.VedaError) as e:
+            layer.check_status()
+        assert e.value.code == V.VEDA_ERR_BAD_INDEX
+        assert (o[0] == 0).all()                        # refused
+        assert (o[1, 20:] == 0).all() and not (o[1, :20] == 0).all(-1).any()
+    assert layer.cache.next_pos.tolist() == [70, 60]
+    # what is given is left as it was
+    o = torch.full_like(q, 7.0)
+    assert layer.step(q, k, k, n_new=news, out=o) is o and (o[0] == 7).all() and (o[1, 20:] == 7).all()

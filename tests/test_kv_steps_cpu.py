@@ -1,0 +1,69 @@
+"""Steps of the 8-bit K/V tile cache without a GPU: what the oracle does with
+pending tokens and refused steps, and what is refused before any CUDA call."""
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+import block_sparse_attention_24_b200 as V
+from tests.test_kv_cpu import FAKE, P, cache, make_oracle, refused
+
+
+@pytest.mark.parametrize("bad", [2.0 ** 20, np.nan, np.inf])
+def test_oracle_replaced_tokens_leave_nothing_behind(bad):
+    rng = np.random.default_rng(1)
+    first, last = (rng.standard_normal((1, n, 1, 64)) for n in (70, 9))
+    wrong = rng.standard_normal((1, 30, 1, 64))
+    wrong[0, 3, 0, 5] = bad
+    a, e, dropped = make_oracle(), make_oracle(), make_oracle()
+    for c in (a, e, dropped):
+        c.append(first, -first, [70])
+        c.advance(np.array([70]))
+    held = [(c.k8[1, :6].copy(), c.k_scale[0, 0, 1]) for c in (e,)][0]
+    for _ in range(2):
+        for c in (a, dropped):
+            c.append(wrong, wrong, [30])
+            assert not c.k_scale[0, 0, 1] == held[1]
+    dropped.append(wrong, wrong, [0])
+    np.testing.assert_array_equal(dropped.k8[1, :6], held[0])
+    assert dropped.k_scale[0, 0, 1] == held[1] and (dropped.k8[1, 6:] == 0).all()
+    for c in (a, e, dropped):
+        c.append(last, last, [9])
+    for c in (a, dropped):
+        for f in ("k8", "v8", "k_scale", "v_scale"):
+            np.testing.assert_array_equal(getattr(c, f)[:2] if f[1:] == "8" else getattr(c, f)[0, 0, :2],
+                                          getattr(e, f)[:2] if f[1:] == "8" else getattr(e, f)[0, 0, :2])
+
+
+def test_oracle_taken_tokens_stay():
+    """Once they are committed, what they did to the scale is not undone."""
+    c = make_oracle()
+    x = np.ones((1, 5, 1, 64))
+    for size in (1.0, 2.0 ** 20, 1.0):
+        c.append(x * size, x * size, [5])
+        c.advance(np.array([5]))
+    assert c.k_scale[0, 0, 0] == 2.0 ** 12 and c.len[0, 0] == 15
+    assert (c.k8[0, :5] == 0).all() and (c.k8[0, 5:10] == 256).all() and (c.k8[0, 10:15] == 0).all()
+
+
+def test_append_pending_refusals():
+    c, L, E = ctypes.byref(cache()), V._lib, V.VEDA_ERR_INVALID_ARG
+    tail = lambda *p: ctypes.byref(V._KvTail(*p))
+    ok = tail(FAKE, FAKE, FAKE)
+    call = lambda t, k=FAKE, n=1, c=c: L.veda_kv_append_pending(c, t, P(k), None, P(FAKE), None, n, None, None)
+    refused(call(tail(None, FAKE, FAKE)), E, "tail codes is NULL")
+    refused(call(tail(FAKE, FAKE + 8, FAKE)), E, "tail key is not")
+    refused(call(tail(FAKE, FAKE, None), n=0), E, "tail scale is NULL")
+    refused(call(ok, k=None), E, "k is NULL")
+    refused(call(ok, n=-1), E, "negative")
+    refused(call(ok, c=None), E, "cache is NULL")
+    assert call(None, n=0) == 0                         # nothing kept, nothing to do
+
+
+def test_the_librarys_own_tensors_cannot_be_replaced():
+    c = V.KVCache(1, 2, 64, 64, 4, "cpu")
+    assert c.tail_codes.shape == (1, 2, 2, 64, 64) and not c.tail_key.any()
+    for name in ("tail_codes", "tail_key", "tail_scale"):
+        with pytest.raises(AttributeError, match="in place"):
+            setattr(c, name, torch.zeros(1))
