@@ -67,20 +67,29 @@ struct KvAttnParams {
 };
 
 // New tokens of sequence b (n_new == NULL: all n), and the tokens its head h
-// then holds; false, with VEDA_ERR_BAD_INDEX recorded, where the counts are
-// outside what the call or the cache can hold. Every kernel of a step decides
-// by this, so a head that is skipped is skipped by all of them.
+// then holds; false, with VEDA_ERR_BAD_INDEX recorded, where the counts of the
+// sequence are outside what the call or the cache can hold, for any of its heads:
+// they share their positions, so one that stayed behind would read its later
+// tokens at wrong ones. Every kernel of a step decides by this, so a sequence that
+// is skipped is skipped by all of them. Called by whole warps.
 __device__ __forceinline__ bool kv_counts(const KvGeom& g, int b, int h, int n, const int32_t* n_new, bool pending,
                                           int& n_b, int& held, int& total) {
+  const int32_t* len = g.len + (long long)b * g.hkv;
+  int most = 0, least = 0;  // over the heads, before n_new is waited for
+#pragma unroll
+  for (int x = 0; x < VEDA_MAX_HEADS; x += 32)
+    if (x + threadIdx.x % 32 < g.hkv) {
+      const int y = len[x + threadIdx.x % 32];
+      most = max(most, y);
+      least = min(least, y);
+    }
+  held = len[h];
   n_b = n_new ? n_new[b] : n;
-  held = g.len[b * g.hkv + h];
-  const long long t = (long long)held + (pending ? n_b : 0);
-  total = (int)t;
-  if (n_b < 0 || n_b > n || held < 0 || t > (long long)g.nb_cap * g.tile) {
-    report(g.dev_status, VEDA_ERR_BAD_INDEX);
-    return false;
-  }
-  return true;
+  const bool bad = __any_sync(0xffffffffu, n_b < 0 || n_b > n || least < 0 ||
+                                               (long long)most + (pending ? n_b : 0) > (long long)g.nb_cap * g.tile);
+  if (bad) report(g.dev_status, VEDA_ERR_BAD_INDEX);
+  total = held + (pending && !bad ? n_b : 0);
+  return !bad;
 }
 
 // Whether any query at a position in [t_lo, t_hi] sees any token of a tile

@@ -373,11 +373,11 @@ int veda_output_sq_error(const veda_layer* L, const void* a, const void* b, floa
  * tokens drops them).
  *
  * n_new (may be NULL = n for all): DEVICE int32 [B], the number of rows of
- * each sequence that are real in a padded batch, 0 <= n_new[b] <= n. A head
- * whose counts are outside their range, or whose tiles cannot hold the new
- * tokens, is left as it is by every call, and a table entry outside [0,
- * n_slots) is treated as an absent tile; both record VEDA_ERR_BAD_INDEX in
- * dev_status.
+ * each sequence that are real in a padded batch, 0 <= n_new[b] <= n. A sequence
+ * whose counts are outside their range, or of which one head's tiles cannot hold
+ * the new tokens, is left as it is by append, attention and advance, and a table
+ * entry outside [0, n_slots) is treated as an absent tile; both record
+ * VEDA_ERR_BAD_INDEX in dev_status.
  *
  * Strides (may be NULL = contiguous): HOST int64 [3], elements between batch
  * elements, tokens and heads of a [B, n, heads, d] bf16 tensor; multiples of

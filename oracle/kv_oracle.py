@@ -53,8 +53,11 @@ class Cache:
             setattr(self, f, np.array(arrays[f]).astype(np.float64 if f in self.FLOATS else np.int64))
 
     def count(self, b, h, n):
-        t = self.len[b, h] + n
-        return int(t) if 0 <= self.len[b, h] and n >= 0 and t <= self.nb_cap * self.tile else None
+        """Tokens of the head with n more; None where the sequence is refused:
+        one of its heads cannot hold them."""
+        held = self.len[b]
+        fits = n >= 0 and (held >= 0).all() and (held + n <= self.nb_cap * self.tile).all()
+        return int(held[h] + n) if fits else None
 
     def committed(self, b, h, x, codes, scale):
         """Codes of the committed rows of the head's tail tile and their scale,
@@ -121,11 +124,9 @@ class Cache:
 
     def advance(self, news):
         for b in range(self.B):
-            for h in range(self.hkv):
-                total = self.count(b, h, news[b])
-                if total is not None:
-                    self.len[b, h] = total
-            self.next_pos[b] += news[b]
+            if self.count(b, 0, news[b]) is not None:
+                self.len[b] += news[b]
+                self.next_pos[b] += news[b]
 
     def keys(self, b, h, total):
         """(K, V, positions) of the head's first `total` tokens; tiles with a

@@ -1,0 +1,77 @@
+"""Steps that the 8-bit K/V tile cache cannot hold: refused whole, sequence by
+sequence, and without a trace."""
+import pytest
+import torch
+
+import block_sparse_attention_24_b200 as V
+from oracle.kv_oracle import Cache
+from tests.test_gpu_kv_cache import (DEV, assert_same_state, bad_status, bf16, check_attention, host, oracle_of,
+                                     random_cache, workspace)
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("n,heads", [(100, 4), (3, 4)])
+def test_a_sequence_is_refused_as_a_whole(n, heads):
+    """One head of two is too full (eviction keeps more of its tiles). Were the
+    other served, or the position moved on, the heads would disagree about
+    where the next tokens stand."""
+    hkv, d, tile = 2, 64, 64
+    c = random_cache(1, 2, hkv, d, tile, 4, [254, 40])
+    V.veda_kv_evict(c, [4, 2], 1, 1)
+    assert c.len.tolist() == [[254, 126], [40, 40]]
+    want, next_pos = oracle_of(c), c.next_pos.tolist()
+    k, q = bf16(2, 2, n, hkv, d), bf16(3, 2, n, heads, d)
+    o, lse = torch.full_like(q, 5.0), torch.full((2, heads, n), 5.0, device=DEV)
+    V.veda_kv_append(c, k, k)
+    bad_status(c)
+    want.append(host(k), host(k), [n, n])
+    assert_same_state(c, want)
+    w = c.weight.clone()
+    V.veda_kv_attn(c, q, o, 0.125, workspace(c, heads, n, True), lse=lse, weight=c.weight)
+    bad_status(c)
+    assert (o[0] == 5).all() and (lse[0] == 5).all() and torch.equal(c.weight[0], w[0])
+    assert not (o[1] == 5).all(-1).any() and not (lse[1] == 5).any()
+    V.veda_kv_advance(c, n)
+    bad_status(c)
+    assert c.len.tolist() == [[254, 126], [40 + n, 40 + n]]
+    assert c.next_pos.tolist() == [next_pos[0], next_pos[1] + n]
+    # with room made, the next tokens stand where the queries take them to be
+    V.veda_kv_evict(c, [2, 2], 1, 1)
+    V.veda_kv_append(c, k, k)
+    for b in range(2):
+        for h in range(hkv):
+            held = int(c.len[b, h])
+            assert int(c.pos[b, h, held // tile]) + held % tile == int(c.next_pos[b])
+    check_attention(c, q, window=n // 2 + 1)
+    check_attention(c, q, window=n + 5, sinks=3, causal=False)
+
+
+def test_counts_of_all_heads_decide():
+    """A head of many (more than a warp has lanes), first or last, without
+    pending tokens as well."""
+    hkv, d, tile = 100, 64, 64
+    for head in (0, 31, 32, 99):
+        c = random_cache(4, 1, hkv, d, tile, 2, [64])
+        c.len[0, head] = 128
+        k, q = bf16(5, 1, 30, hkv, d), bf16(6, 1, 30, hkv, d)
+        before = {f: getattr(c, f).clone() for f in Cache.FIELDS}
+        V.veda_kv_append(c, k, k)
+        bad_status(c)
+        V.veda_kv_advance(c, 30)
+        bad_status(c)
+        for f, t in before.items():
+            assert torch.equal(t.view(torch.uint8), getattr(c, f).view(torch.uint8)), f
+        for rows in (30, 1):
+            o = torch.full_like(q, 5.0)[:, :rows].contiguous()
+            V.veda_kv_attn(c, q[:, :rows].contiguous(), o, 0.125, workspace(c, hkv, rows, False))
+            bad_status(c)
+            assert (o == 5).all()
+            V.veda_kv_attn(c, q[:, :rows].contiguous(), o, 0.125, workspace(c, hkv, rows, False), pending=False)
+            V.veda_kv_check_status(c)
+            assert not (o == 5).all(-1).any()                # no row is left as it was (a value may be 5)
+        c.len[0, head] = -1
+        o = torch.full_like(q, 5.0)
+        V.veda_kv_attn(c, q, o, 0.125, workspace(c, hkv, 30, False), pending=False)
+        bad_status(c)
+        assert (o == 5).all()

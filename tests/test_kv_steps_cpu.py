@@ -47,6 +47,19 @@ def test_oracle_taken_tokens_stay():
     assert (c.k8[0, :5] == 0).all() and (c.k8[0, 5:10] == 256).all() and (c.k8[0, 10:15] == 0).all()
 
 
+def test_oracle_refuses_a_sequence_as_a_whole():
+    c = make_oracle(B=2, hkv=2, nb=2)
+    x = np.ones((2, 100, 2, 64))
+    c.append(x, x, [100, 100])
+    c.advance(np.array([100, 100]))
+    c.len[0, 1] = 36                                    # a tile of this head has been evicted
+    before = c.k8.copy()
+    c.append(x, x, [50, 28])                            # 150 of 128; exactly full
+    c.advance(np.array([50, 28]))
+    assert c.len.tolist() == [[100, 36], [128, 128]] and c.next_pos.tolist() == [100, 128]
+    np.testing.assert_array_equal(c.k8[:4], before[:4])
+
+
 def test_append_pending_refusals():
     c, L, E = ctypes.byref(cache()), V._lib, V.VEDA_ERR_INVALID_ARG
     tail = lambda *p: ctypes.byref(V._KvTail(*p))
