@@ -107,16 +107,13 @@ __global__ void __launch_bounds__(APPEND_THREADS)
       val[j][1] = __ldcs(q + 1);
     }
   }
-  if (slot < 0 || slot >= g.n_slots) {
-    if (threadIdx.x == 0 && n_b > 0) report(g.dev_status, VEDA_ERR_BAD_INDEX);
-    return;
-  }
+  const bool absent = slot < 0 || slot >= g.n_slots;
   uint8_t* codes = (is_v ? g.v8 : g.k8) + (long long)slot * g.tile * D;
   uint8_t* const kept_codes = tail.codes + kept * g.tile * D;
   // the tail may be what a raise left of the kept codes: both are looked at, in
   // the registers of the rows that are not new (in a loop and registers of their
   // own the frame took 15.5 us instead of 14.7, one token 4.3 instead of 3.5)
-  const bool raise_left = joins && key.x == -row0 && key.y == slot && key.z == next &&
+  const bool raise_left = joins && !absent && key.x == -row0 && key.y == slot && key.z == next &&
                           __float_as_uint(was.y) == __float_as_uint(s_old);
   bool back = raise_left;  // the kept codes and scale are the committed ones
   if (raise_left) {
@@ -159,6 +156,13 @@ __global__ void __launch_bounds__(APPEND_THREADS)
 #pragma unroll
   for (int w = 0; w < APPEND_THREADS / 32; ++w) top = max(top, warp_top[w]);
   if (n_b == 0 && !back) return;
+  if (absent) {  // no codes, but a place in the stream like any tile
+    if (threadIdx.x == 0) {
+      report(g.dev_status, VEDA_ERR_BAD_INDEX);
+      if (fresh && !is_v) g.pos[entry] = g.next_pos[b] + row0;
+    }
+    return;
+  }
   const float s_new = scale_of(__uint_as_float(top));
   float s = fresh ? s_new : ((s_new != s_new || s_old != s_old) ? s_new + s_old : fmaxf(s_new, s_old));
   if (n_b == 0) s = s_old;

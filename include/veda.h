@@ -402,7 +402,8 @@ typedef struct {
  * codes are then rounded once more, to the new scale (exact for all but
  * values near e4m3's subnormals), and where a new token has no scale the older
  * ones have none either. Rows of a touched tile behind the last token become
- * zero; a tile that is begun gets its pos, and weight 0.
+ * zero; a tile that is begun gets its pos, and weight 0 (one without a slot
+ * only its pos).
  *
  * veda_kv_append starts from the tail tile as it is, so what tokens that are
  * replaced did to the scale of committed ones stays: it is for tokens that are

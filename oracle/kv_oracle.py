@@ -95,9 +95,11 @@ class Cache:
                 for i in range(held // T, -(-total // T)):
                     lo, hi = max(held, i * T), min(total, (i + 1) * T)
                     slot = self.table[b, h, i]
-                    if not 0 <= slot < len(self.k8):
-                        continue
                     fresh = lo == i * T
+                    if not 0 <= slot < len(self.k8):
+                        if fresh:
+                            self.pos[b, h, i] = self.next_pos[b] + lo - held
+                        continue
                     for x, new, codes, scale in ((0, k, self.k8, self.k_scale), (1, v, self.v8, self.v_scale)):
                         rows = new[b, lo - held:hi - held, h]
                         with np.errstate(invalid="ignore"):

@@ -1,5 +1,6 @@
 """Steps that the 8-bit K/V tile cache cannot hold: refused whole, sequence by
 sequence, and without a trace."""
+import numpy as np
 import pytest
 import torch
 
@@ -75,3 +76,25 @@ def test_counts_of_all_heads_decide():
         V.veda_kv_attn(c, q, o, 0.125, workspace(c, hkv, 30, False), pending=False)
         bad_status(c)
         assert (o == 5).all()
+
+
+@pytest.mark.parametrize("n", [1, 20])
+def test_a_tile_without_a_slot_still_has_its_position(n):
+    """Absent, but at its place in the stream: windows find the tiles around it
+    by the positions, which ascend."""
+    hkv, d, tile = 2, 64, 64
+    c = V.KVCache(1, hkv, d, tile, 6, DEV)
+    c.table[0, 0, 3], c.table[0, 1, 2] = -1, c.n_slots
+    k, v, q = bf16(20, 1, 250, hkv, d), bf16(21, 1, 250, hkv, d), bf16(22, 1, n, 4, d)
+    V.veda_kv_append(c, k, v)
+    bad_status(c)
+    V.veda_kv_advance(c, 250)
+    assert c.pos[0, :, :4].tolist() == [[0, 64, 128, 192]] * 2
+    for window, sinks in ((64, 0), (130, 0), (100, 64)):
+        want = oracle_of(c).attend(host(q), [n], 0.125, True, window, sinks, pending=False)
+        o, lse = torch.empty_like(q), torch.empty((1, 4, n), device=DEV)
+        V.veda_kv_attn(c, q, o, 0.125, workspace(c, 4, n, False), window=window, sinks=sinks, pending=False, lse=lse)
+        bad_status(c)
+        # as in test_table_entries_outside_the_pool_are_absent_tiles: a value and its bf16 rounding, with room
+        np.testing.assert_allclose(host(o), want[0], rtol=2.0 ** -7, atol=2.0 ** -6)
+        np.testing.assert_allclose(host(lse), want[1], rtol=0, atol=2.0 ** -10)
