@@ -72,7 +72,7 @@ class VedaStream:
             # the step's tensors belong to the stream that uses them
             with self._on(stream):
                 return self.step(q, k, v, n_new, commit, out, lse)
-        n = q.shape[1]
+        n = self._tokens(q, k, v)
         if out is None:
             out = torch.empty_like(q, memory_format=torch.contiguous_format)
         if n == 0:
@@ -87,6 +87,16 @@ class VedaStream:
             if self.keep is not None:
                 veda_kv_evict(c, self.keep, self.sink_tiles, self.recent_tiles)
         return out
+
+    def _tokens(self, q, k, v) -> int:
+        """The tokens of a step: append, attention and advance have to agree."""
+        c = self.cache
+        for t, name, heads in ((q, "q", self.heads), (k, "k", c.heads_kv), (v, "v", c.heads_kv)):
+            if not isinstance(t, torch.Tensor) or t.dim() != 4 or t.shape[::2] != (c.B, heads) or t.shape[3] != c.d:
+                raise ValueError(f"{name} must be a [{c.B}, n, {heads}, {c.d}] tensor")
+        if not q.shape[1] == k.shape[1] == v.shape[1]:
+            raise ValueError(f"q, k and v must have as many tokens each, not {q.shape[1]}, {k.shape[1]} and {v.shape[1]}")
+        return q.shape[1]
 
     def _on(self, stream):
         if stream is not None and stream.device != self.cache.device:

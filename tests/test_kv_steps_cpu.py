@@ -80,3 +80,27 @@ def test_the_librarys_own_tensors_cannot_be_replaced():
     for name in ("tail_codes", "tail_key", "tail_scale"):
         with pytest.raises(AttributeError, match="in place"):
             setattr(c, name, torch.zeros(1))
+
+
+def test_stream_layer_refuses_tokens_that_do_not_match(monkeypatch):
+    """Before the first kernel: k and v with more or fewer tokens than q (rows
+    that nothing has written would be taken in, or surplus ones dropped)."""
+    from block_sparse_attention_24_b200 import stream
+    calls = []
+    for name in ("veda_kv_append", "veda_kv_attn", "veda_kv_advance", "veda_kv_evict"):
+        monkeypatch.setattr(stream, name, lambda *a, _n=name, **kw: calls.append(_n))
+    layer = stream.VedaStream(2, 4, 2, 64, 64, 640, "cpu")
+    bf = lambda *s: torch.zeros(s, dtype=torch.bfloat16)
+    q, k = bf(2, 5, 4, 64), bf(2, 5, 2, 64)
+    for a, b, c in ((q, bf(2, 4, 2, 64), k), (q, k, bf(2, 6, 2, 64)), (q, k[:, :0], k[:, :0]), (q[:, :0], k, k),
+                    (bf(2, 1, 4, 64), k, k)):
+        with pytest.raises(ValueError, match="as many tokens"):
+            layer.step(a, b, c)
+    for a, b, c in ((bf(2, 5, 2, 64), k, k), (q, bf(2, 5, 4, 64), k), (q, k, bf(1, 5, 2, 64)), (q, k, bf(2, 5, 2, 128)),
+                    (q[0], k, k), (q, k[0], k), (q, k, None)):
+        with pytest.raises(ValueError, match="must be a"):
+            layer.step(a, b, c)
+    assert calls == []
+    layer.step(q, k, k)
+    layer.step(q[:, :0], k[:, :0], k[:, :0])
+    assert calls == ["veda_kv_append", "veda_kv_attn", "veda_kv_advance"]
