@@ -31,7 +31,7 @@ EXPORTED = ("veda_layout", "veda_permute", "veda_trippool", "veda_permute_trippo
             "veda_topk_mask", "veda_tile_scores_topk", "veda_tile_scores_heads", "veda_topk_mask_heads", "veda_score_cache_step", "veda_score_cache_ws_bytes", "veda_sparse_attn", "veda_sparse_attn_unpermute", "veda_sparse_attn_tokens", "veda_full_attn_tilemax", "veda_full_attn_tilemax_ws_bytes", "veda_tilemap_kl", "veda_tilemap_recall",
             "veda_check_status",
             "veda_estimator_grad", "veda_estimator_grad_ws_bytes", "veda_output_sq_error", "veda_selftest_wait_timeout", "veda_last_error",
-            "veda_kv_append", "veda_kv_append_pending", "veda_kv_advance", "veda_kv_attn", "veda_kv_attn_ws_bytes", "veda_kv_evict", "veda_kv_check_status")
+            "veda_kv_append", "veda_kv_append_pending", "veda_kv_advance", "veda_kv_attn", "veda_kv_attn_fill", "veda_kv_attn_ws_bytes", "veda_kv_evict", "veda_kv_check_status")
 
 
 class VedaError(RuntimeError):
@@ -107,6 +107,7 @@ _lib.veda_kv_append.argtypes = [_CP, _P, _P, _P, _P, _I, _P, _P]
 _lib.veda_kv_append_pending.argtypes = [_CP, ctypes.POINTER(_KvTail), _P, _P, _P, _P, _I, _P, _P]
 _lib.veda_kv_advance.argtypes = [_CP, _I, _P, _P]
 _lib.veda_kv_attn.argtypes = [_CP, _P, _P, _I, _I, _P, _I, _I, _I, _I, _F, _P, _P, _P, _P, _F, _P, _P]
+_lib.veda_kv_attn_fill.argtypes = _lib.veda_kv_attn.argtypes
 _lib.veda_kv_attn_ws_bytes.argtypes = [_CP, _I, _I, _I]
 _lib.veda_kv_attn_ws_bytes.restype = ctypes.c_size_t
 _lib.veda_kv_evict.argtypes = [_CP, _P, _I, _I, _CP, _P]
@@ -508,10 +509,11 @@ def veda_kv_attn_ws_bytes(cache: KVCache, heads: int, n_q: int, with_weight: boo
 def veda_kv_attn(cache: KVCache, q: torch.Tensor, o: torch.Tensor, scale: float, ws: torch.Tensor,
                  causal: bool = True, window: int = 0, sinks: int = 0, n_new: Optional[torch.Tensor] = None,
                  pending: bool = True, lse: Optional[torch.Tensor] = None, weight: Optional[torch.Tensor] = None,
-                 decay: float = 1.0, stream=None):
+                 decay: float = 1.0, fill: bool = False, stream=None):
     """Attention of q [B, n_q, heads, d] over the cache, into o. ws: device
     scratch of veda_kv_attn_ws_bytes(cache, heads, n_q, weight is not None)
-    bytes. weight: [B, heads_kv, nb_cap], e.g. cache.weight."""
+    bytes. weight: [B, heads_kv, nb_cap], e.g. cache.weight. fill: rows of o and
+    lse without a query get zeros and -inf, else they are left as they are."""
     if not isinstance(q, torch.Tensor) or q.dim() != 4:
         raise ValueError("q must be a [B, n_q, heads, d] tensor")
     _, n, heads, _ = q.shape
@@ -529,7 +531,7 @@ def veda_kv_attn(cache: KVCache, q: torch.Tensor, o: torch.Tensor, scale: float,
         raise ValueError("ws must be a contiguous tensor on the cache's device")
     if ws.nbytes < need:
         raise ValueError(f"ws holds {ws.nbytes} bytes, {need} are needed")
-    _kv_call(cache, stream, _lib.veda_kv_attn, cache.ref, qp, qs, heads, n, _n_new(cache, n_new), bool(pending),
+    _kv_call(cache, stream, _lib.veda_kv_attn_fill if fill else _lib.veda_kv_attn, cache.ref, qp, qs, heads, n, _n_new(cache, n_new), bool(pending),
              bool(causal), _i32(window, "window"), _i32(sinks, "sinks"), float(scale), op, os_, lp, wp, float(decay),
              ws.data_ptr())
 

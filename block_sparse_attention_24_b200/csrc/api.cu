@@ -709,10 +709,10 @@ size_t veda_kv_attn_ws_bytes(const veda_kv_cache* C, int32_t heads, int32_t n_q,
   return veda::kv_attn_ws_bytes(g, heads, n_q, with_weight != 0);
 }
 
-int veda_kv_attn(const veda_kv_cache* C, const void* q, const int64_t* q_strides, int32_t heads, int32_t n_q,
-                 const int32_t* n_new, int32_t pending, int32_t causal, int32_t window, int32_t sinks, float scale,
-                 void* o, const int64_t* o_strides, float* lse, float* weight, float decay, void* ws,
-                 cudaStream_t stream) {
+static int kv_attn(const veda_kv_cache* C, const void* q, const int64_t* q_strides, int32_t heads, int32_t n_q,
+                   const int32_t* n_new, int32_t pending, int32_t causal, int32_t window, int32_t sinks, float scale,
+                   void* o, const int64_t* o_strides, float* lse, float* weight, float decay, void* ws, bool fill,
+                   cudaStream_t stream) {
   veda::KvGeom g;
   VEDA_TRY(build_kv(C, &g, "cache"));
   VEDA_TRY(check_kv_heads(g, heads, n_q));
@@ -740,12 +740,29 @@ int veda_kv_attn(const veda_kv_cache* C, const void* q, const int64_t* q_strides
   p.causal = causal != 0;
   p.window = window;
   p.sinks = sinks;
+  p.fill = fill;
   p.scale_log2 = scale * 1.4426950408889634f;
   p.lse = lse;
   p.weight = weight;
   p.decay = decay;
   p.arrive = g.arrive;
   return after_launch(veda::launch_kv_attn(g, p, ws, stream), "veda_kv_attn");
+}
+
+int veda_kv_attn(const veda_kv_cache* C, const void* q, const int64_t* q_strides, int32_t heads, int32_t n_q,
+                 const int32_t* n_new, int32_t pending, int32_t causal, int32_t window, int32_t sinks, float scale,
+                 void* o, const int64_t* o_strides, float* lse, float* weight, float decay, void* ws,
+                 cudaStream_t stream) {
+  return kv_attn(C, q, q_strides, heads, n_q, n_new, pending, causal, window, sinks, scale, o, o_strides, lse, weight,
+                 decay, ws, false, stream);
+}
+
+int veda_kv_attn_fill(const veda_kv_cache* C, const void* q, const int64_t* q_strides, int32_t heads, int32_t n_q,
+                      const int32_t* n_new, int32_t pending, int32_t causal, int32_t window, int32_t sinks,
+                      float scale, void* o, const int64_t* o_strides, float* lse, float* weight, float decay, void* ws,
+                      cudaStream_t stream) {
+  return kv_attn(C, q, q_strides, heads, n_q, n_new, pending, causal, window, sinks, scale, o, o_strides, lse, weight,
+                 decay, ws, true, stream);
 }
 
 int veda_kv_evict(const veda_kv_cache* C, const int32_t* keep, int32_t sink, int32_t recent,

@@ -146,8 +146,9 @@ __global__ void __launch_bounds__((RowsCfg<D, RP>::THREADS), 2)
   after_predecessor();
   int n_b, held, total;
   const int t_lo = g.next_pos[b];
-  if (!kv_counts(g, b, h, p.n_q, p.n_new, p.pending, n_b, held, total)) return;
-  const int rows = n_b * p.group;
+  const bool fits = kv_counts(g, b, h, p.n_q, p.n_new, p.pending, n_b, held, total);
+  const int rows = fits ? n_b * p.group : 0;
+  if (p.fill && sp == 0) fill_rows<D>(p, b, h, rows, p.rows_cap, tid, THREADS);
   if (rows == 0) return;
   const int bh = b * g.hkv + h;
   const long long trow = (long long)bh * g.nb_cap;

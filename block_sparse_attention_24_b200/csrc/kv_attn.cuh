@@ -122,6 +122,26 @@ __device__ __forceinline__ KvRange kv_range(const KvGeom& g, const KvAttnParams&
   return r;
 }
 
+// Zeros, and lse = -inf, for the rows of a head that no query is in (p.fill):
+// rows lo .. hi-1, by `threads` threads. Not inlined, as the kernels' registers
+// then go to it too (32 x 2 tokens of 16 rows, window 2,048: 20.2 us, not 19.7).
+template <int D>
+__device__ __noinline__ void fill_rows_at(__nv_bfloat16* o, long long sn, long long sh, float* lse, int n_q, int group,
+                                          int lo, int hi, int x0, int threads) {
+#pragma unroll 1
+  for (long long x = (long long)lo * (D / 8) + x0; x < (long long)hi * (D / 8); x += threads) {
+    const int r = (int)(x / (D / 8)), c8 = (int)(x % (D / 8)), i = r / group, y = r - i * group;
+    *reinterpret_cast<uint4*>(o + i * sn + y * sh + c8 * 8) = make_uint4(0, 0, 0, 0);
+    if (c8 == 0 && lse) lse[(long long)y * n_q + i] = -INFINITY;
+  }
+}
+template <int D>
+__device__ __forceinline__ void fill_rows(const KvAttnParams& p, int b, int h, int lo, int hi, int tid, int threads) {
+  const int qh = h * p.group;
+  fill_rows_at<D>(p.o + b * p.o_sb + qh * p.o_sh, p.o_sn, p.o_sh,
+                  p.lse ? p.lse + ((long long)b * p.heads + qh) * p.n_q : nullptr, p.n_q, p.group, lo, hi, tid, threads);
+}
+
 // ------------------------------------------------------- steps of 128 keys
 constexpr int STEP = 128, HALF = 64;  // a step is two halves of 64 keys, each a TMA box of its own
 

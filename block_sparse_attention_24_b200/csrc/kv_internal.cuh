@@ -48,7 +48,7 @@ struct KvAttnParams {
   int64_t o_sb, o_sn, o_sh;
   int32_t heads, group, n_q;
   const int32_t* n_new;
-  int32_t pending, causal, window, sinks;
+  int32_t pending, causal, window, sinks, fill;
   float scale_log2;
   float* lse;     // [B, heads, n_q] natural log, or NULL
   float* weight;  // [B, hkv, nb_cap] or NULL

@@ -157,9 +157,10 @@ __global__ void __launch_bounds__(THREADS, 1)
   asm volatile("griddepcontrol.wait;" ::: "memory");
   int n_b, held, total;
   const int t0 = g.next_pos[b];
-  if (!kv_counts(g, b, h, p.n_q, p.n_new, p.pending, n_b, held, total)) return;
-  const int rows = n_b * p.group;
+  const bool fits = kv_counts(g, b, h, p.n_q, p.n_new, p.pending, n_b, held, total);
+  const int rows = fits ? n_b * p.group : 0;
   const int base = mt * 2 * BM;
+  if (p.fill && sp == 0) fill_rows<D>(p, b, h, max(base, rows), min(base + 2 * BM, p.rows_cap), tid, THREADS);
   if (base >= rows) return;
   const bool alt = p.alt, has_b = base + BM < rows || alt;
   const int bh = b * g.hkv + h;

@@ -25,7 +25,11 @@ class VedaStream:
     one number or one per K/V head): a head that holds more after a committed
     step drops the least attended ones, all but its first `sink_tiles` and
     last `recent_tiles`; None: nothing is dropped. Attention weights are summed
-    over committed steps, those before with a factor `decay` for every step."""
+    over committed steps, those before with a factor `decay` for every step.
+
+    max_tokens has to hold what is kept and a step's tokens together: a step
+    that finds less room in any head of a sequence leaves that sequence as it
+    was and gives it zeros. Only the device knows; check_status() tells."""
 
     def __init__(self, B: int, heads: int, heads_kv: int, d: int, tile: int, max_tokens: int, device,
                  causal: bool = True, window: int = 0, sinks: int = 0, keep=None, sink_tiles: int = 1,
@@ -65,23 +69,26 @@ class VedaStream:
     def step(self, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, n_new: Optional[torch.Tensor] = None,
              commit: bool = True, out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None, stream=None):
         """q [B, n, heads, d], k, v [B, n, heads_kv, d] bf16; n_new [B] int32:
-        the real rows of each sequence (None: all). Returns the output, like q
-        (rows that are not real are not written); allocated on `stream`, if
-        `out` is not given."""
+        the real rows of each sequence (None: all). Returns the output, like q:
+        `out`, whose rows (and those of lse) that are not real, or not of a
+        sequence that fits, are left as they are; or if it is not given a tensor
+        allocated on `stream`, where they are zero (and -inf in lse)."""
         if stream is not None:
             # the step's tensors belong to the stream that uses them
             with self._on(stream):
                 return self.step(q, k, v, n_new, commit, out, lse)
-        n = self._tokens(q, k, v)
-        if out is None:
+        n, c = self._tokens(q, k, v), self.cache
+        if n_new is None and n > c.nb_cap * c.tile:
+            raise ValueError(f"a step of {n} tokens does not fit a cache of {c.nb_cap * c.tile}")
+        fill = out is None
+        if fill:
             out = torch.empty_like(q, memory_format=torch.contiguous_format)
         if n == 0:
             return out
-        c = self.cache
         weigh = commit and self.keep is not None
         veda_kv_append(c, k, v, n_new=n_new)
         veda_kv_attn(c, q, out, self.scale, self.workspace(n, weigh), causal=self.causal, window=self.window,
-                     sinks=self.sinks, n_new=n_new, lse=lse, weight=c.weight if weigh else None, decay=self.decay)
+                     sinks=self.sinks, n_new=n_new, lse=lse, weight=c.weight if weigh else None, decay=self.decay, fill=fill)
         if commit:
             veda_kv_advance(c, n, n_new=n_new)
             if self.keep is not None:
@@ -91,12 +98,15 @@ class VedaStream:
     def _tokens(self, q, k, v) -> int:
         """The tokens of a step: append, attention and advance have to agree."""
         c = self.cache
-        for t, name, heads in ((q, "q", self.heads), (k, "k", c.heads_kv), (v, "v", c.heads_kv)):
-            if not isinstance(t, torch.Tensor) or t.dim() != 4 or t.shape[::2] != (c.B, heads) or t.shape[3] != c.d:
+        shapes = [t.shape if isinstance(t, torch.Tensor) else () for t in (q, k, v)]
+        n = shapes[0][1] if len(shapes[0]) == 4 else 0
+        kv = (c.B, n, c.heads_kv, c.d)
+        if shapes == [(c.B, n, self.heads, c.d), kv, kv]:
+            return n
+        for shape, name, heads in zip(shapes, "qkv", (self.heads, c.heads_kv, c.heads_kv)):
+            if len(shape) != 4 or (shape[0], shape[2], shape[3]) != (c.B, heads, c.d):
                 raise ValueError(f"{name} must be a [{c.B}, n, {heads}, {c.d}] tensor")
-        if not q.shape[1] == k.shape[1] == v.shape[1]:
-            raise ValueError(f"q, k and v must have as many tokens each, not {q.shape[1]}, {k.shape[1]} and {v.shape[1]}")
-        return q.shape[1]
+        raise ValueError(f"q, k and v must have as many tokens each, not {[s[1] for s in shapes]}")
 
     def _on(self, stream):
         if stream is not None and stream.device != self.cache.device:

@@ -438,7 +438,9 @@ int veda_kv_advance(const veda_kv_cache* C, int32_t n, const int32_t* n_new, cud
  *   causal != 0:  the positions p <= t only;
  *   window > 0:   the positions p > t - window or p < sinks only.
  * A query that sees nothing gets zeros and lse = -inf. Rows i >= n_new[b] of
- * o and lse are not written.
+ * o and lse, and all rows of a sequence that is refused, are not written by
+ * veda_kv_attn and get zeros and -inf from veda_kv_attn_fill (for outputs that
+ * hold nothing yet).
  *   lse (may be NULL) [B, heads, n_q] fp32: natural-log softmax normaliser.
  *   weight (may be NULL) [B, heads_kv, nb_cap] fp32, e.g. C->weight: for each
  *     tile in use weight = decay * weight + (the softmax weight that this
@@ -455,6 +457,10 @@ int veda_kv_attn(const veda_kv_cache* C, const void* q, const int64_t* q_strides
                  const int32_t* n_new, int32_t pending, int32_t causal, int32_t window, int32_t sinks, float scale,
                  void* o, const int64_t* o_strides, float* lse, float* weight, float decay, void* ws,
                  cudaStream_t stream);
+int veda_kv_attn_fill(const veda_kv_cache* C, const void* q, const int64_t* q_strides, int32_t heads, int32_t n_q,
+                      const int32_t* n_new, int32_t pending, int32_t causal, int32_t window, int32_t sinks,
+                      float scale, void* o, const int64_t* o_strides, float* lse, float* weight, float decay, void* ws,
+                      cudaStream_t stream);
 
 /* Drops the tiles that received the least attention: of a head with more than
  * keep[h] tiles in use (keep: HOST array [heads_kv], keep[h] >= sink +

@@ -98,3 +98,56 @@ def test_a_tile_without_a_slot_still_has_its_position(n):
         # as in test_table_entries_outside_the_pool_are_absent_tiles: a value and its bf16 rounding, with room
         np.testing.assert_allclose(host(o), want[0], rtol=2.0 ** -7, atol=2.0 ** -6)
         np.testing.assert_allclose(host(lse), want[1], rtol=0, atol=2.0 ** -10)
+
+
+@pytest.mark.parametrize("keep", [None, 2])
+def test_a_step_past_the_capacity_returns_no_old_memory(keep):
+    from block_sparse_attention_24_b200.stream import VedaStream
+    n = 70
+    layer = VedaStream(2, 4, 2, 64, 64, 128, DEV, keep=keep, sink_tiles=0)
+    q, k = bf16(10, 2, n, 4, 64), bf16(11, 2, n, 2, 64)
+    news = torch.tensor([n, 20], dtype=torch.int32, device=DEV)
+    assert layer.step(q, k, k, n_new=news).shape == q.shape
+    layer.check_status()
+    for _ in range(2):
+        junk = [torch.full_like(q, 7.0) for _ in range(4)]
+        del junk
+        o = layer.step(q, k, k, n_new=news)
+        with pytest.raises(V.VedaError) as e:
+            layer.check_status()
+        assert e.value.code == V.VEDA_ERR_BAD_INDEX
+        assert (o[0] == 0).all()                        # refused
+        assert (o[1, 20:] == 0).all() and not (o[1, :20] == 0).all(-1).any()
+    assert layer.cache.next_pos.tolist() == [70, 60]
+    # what is given is left as it was
+    o = torch.full_like(q, 7.0)
+    assert layer.step(q, k, k, n_new=news, out=o) is o and (o[0] == 7).all() and (o[1, 20:] == 7).all()
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("n,heads", [(1, 2), (3, 6), (8, 4), (20, 2), (70, 12), (600, 4)])
+def test_rows_without_a_query_are_filled(n, heads, d):
+    """Padded rows and those of refused sequences, by both kernels and with
+    split heads; all others as without."""
+    hkv, tile, nb = 2, 64, 20
+    c = random_cache(30, 5, hkv, d, tile, nb, [600 + n] * 5)
+    c.len.sub_(n)
+    c.next_pos.sub_(n)
+    c.len[3, 1] = nb * tile                             # full
+    news = torch.tensor([n, n // 2, 0, n, n + 1], dtype=torch.int32, device=DEV)
+    q, got = bf16(31, 5, n, heads, d), []
+    for fill in (False, True):
+        room = torch.full((5, heads, n + 2, d), 9.0, dtype=torch.bfloat16, device=DEV)
+        o, lse, w = room.transpose(1, 2)[:, 1:n + 1], torch.full((5, heads, n), 9.0, device=DEV), c.weight.clone()
+        V.veda_kv_attn(c, q, o, 0.125, workspace(c, heads, n, True), n_new=news, lse=lse, weight=w, fill=fill)
+        bad_status(c)
+        assert (room[:, :, 0] == 9).all() and (room[:, :, n + 1:] == 9).all()
+        got.append((o, lse, w))
+    (o, lse, w), (fo, flse, fw) = got
+    assert torch.equal(w, fw)
+    for b, m in enumerate((n, n // 2, 0, 0, 0)):
+        assert torch.equal(o[b, :m], fo[b, :m]) and torch.equal(lse[b, :, :m], flse[b, :, :m])
+        assert (o[b, m:] == 9).all() and (lse[b, :, m:] == 9).all()
+        assert (fo[b, m:] == 0).all() and (flse[b, :, m:] == -float("inf")).all()
+    V.veda_kv_attn(c, q, q, 0.125, workspace(c, heads, n, False), n_new=news, fill=True)     # over the query
+    assert torch.equal(q, fo)

@@ -74,6 +74,18 @@ def test_append_pending_refusals():
     assert call(None, n=0) == 0                         # nothing kept, nothing to do
 
 
+def test_attention_that_fills_refuses_what_attention_does():
+    def call(c=None, heads=6, n=2, window=0, o=FAKE):
+        return V._lib.veda_kv_attn_fill(ctypes.byref(cache() if c is None else c), P(FAKE), None, heads, n, None, 1, 1,
+                                        window, 0, 0.125, P(o), None, None, None, 1.0, P(FAKE), None)
+    E = V.VEDA_ERR_INVALID_ARG
+    refused(call(c=cache(pos=None)), E, "pos")
+    refused(call(heads=4), E, "multiple of heads_kv")
+    refused(call(window=-1), E, "window")
+    refused(call(o=FAKE + 8), E, "o is not")
+    assert call(n=0) == 0
+
+
 def test_the_librarys_own_tensors_cannot_be_replaced():
     c = V.KVCache(1, 2, 64, 64, 4, "cpu")
     assert c.tail_codes.shape == (1, 2, 2, 64, 64) and not c.tail_key.any()
@@ -104,3 +116,14 @@ def test_stream_layer_refuses_tokens_that_do_not_match(monkeypatch):
     layer.step(q, k, k)
     layer.step(q[:, :0], k[:, :0], k[:, :0])
     assert calls == ["veda_kv_append", "veda_kv_attn", "veda_kv_advance"]
+
+
+def test_stream_layer_refuses_a_step_past_the_capacity():
+    from block_sparse_attention_24_b200.stream import VedaStream
+    layer = VedaStream(1, 2, 2, 64, 64, 100, "cpu")         # two tiles
+    step = lambda n, **kw: layer.step(*[torch.zeros((1, n, 2, 64), dtype=torch.bfloat16)] * 3, **kw)
+    with pytest.raises(ValueError, match="129 tokens does not fit a cache of 128"):
+        step(129)
+    for call in (lambda: step(128), lambda: step(129, n_new=torch.tensor([100], dtype=torch.int32))):
+        with pytest.raises(ValueError, match="CUDA"):       # the padding does not have to fit
+            call()
