@@ -408,6 +408,11 @@ class KVCache:
         self._ws_bytes = {}  # of veda_kv_attn, by (heads, n_q, with weights)
         self.ref = ctypes.byref(self._c)
 
+    def tensors(self):
+        """All the device memory that a call on the cache may use."""
+        return [getattr(self, n) for n in ("k8", "v8", "table", "pos", "k_scale", "v_scale", "weight", "len", "next_pos",
+                                           "status", "tail_codes", "tail_key", "tail_scale")]
+
     def __setattr__(self, name, value):
         # the kernels have the tensors' addresses: another tensor would be
         # ignored, and the one they use freed

@@ -29,7 +29,10 @@ class VedaStream:
 
     max_tokens has to hold what is kept and a step's tokens together: a step
     that finds less room in any head of a sequence leaves that sequence as it
-    was and gives it zeros. Only the device knows; check_status() tells."""
+    was and gives it zeros. Only the device knows; check_status() tells.
+
+    A captured step uses the layer's memory: the layer has to live as long as
+    the graph."""
 
     def __init__(self, B: int, heads: int, heads_kv: int, d: int, tile: int, max_tokens: int, device,
                  causal: bool = True, window: int = 0, sinks: int = 0, keep=None, sink_tiles: int = 1,
@@ -53,6 +56,7 @@ class VedaStream:
                                  f"recent_tiles={recent_tiles} (>= 1)")
         self.sink_tiles, self.recent_tiles, self.decay = sink_tiles, recent_tiles, decay
         self._ws = {}
+        self._recorded = set()
 
     def workspace(self, n: int, weight: bool) -> torch.Tensor:
         """Scratch of a step of n tokens, allocated at the first one. Sizes are
@@ -86,8 +90,10 @@ class VedaStream:
         if n == 0:
             return out
         weigh = commit and self.keep is not None
+        ws = self.workspace(n, weigh)
+        self._record(ws)
         veda_kv_append(c, k, v, n_new=n_new)
-        veda_kv_attn(c, q, out, self.scale, self.workspace(n, weigh), causal=self.causal, window=self.window,
+        veda_kv_attn(c, q, out, self.scale, ws, causal=self.causal, window=self.window,
                      sinks=self.sinks, n_new=n_new, lse=lse, weight=c.weight if weigh else None, decay=self.decay, fill=fill)
         if commit:
             veda_kv_advance(c, n, n_new=n_new)
@@ -108,6 +114,19 @@ class VedaStream:
                 raise ValueError(f"{name} must be a [{c.B}, n, {heads}, {c.d}] tensor")
         raise ValueError(f"q, k and v must have as many tokens each, not {[s[1] for s in shapes]}")
 
+    def _record(self, ws: Optional[torch.Tensor] = None):
+        """The current stream uses the layer's memory: dropped meanwhile, it is
+        not to be handed out again before that stream is through."""
+        c = self.cache
+        if c.device.type != "cuda":
+            return
+        key = (torch._C._cuda_getCurrentRawStream(c.device.index), None if ws is None else ws.nbytes)
+        if key not in self._recorded:
+            stream = torch.cuda.current_stream(c.device)
+            for t in c.tensors() if ws is None else [*c.tensors(), ws]:
+                t.record_stream(stream)
+            self._recorded.add(key)
+
     def _on(self, stream):
         if stream is not None and stream.device != self.cache.device:
             raise ValueError(f"the stream is on {stream.device}, the cache on {self.cache.device}")
@@ -116,6 +135,7 @@ class VedaStream:
     def reset(self, stream=None):
         """Empty the cache (its next tokens are at position 0 again)."""
         with self._on(stream):
+            self._record()
             self.cache.len.zero_()
             self.cache.next_pos.zero_()
 

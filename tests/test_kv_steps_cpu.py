@@ -127,3 +127,14 @@ def test_stream_layer_refuses_a_step_past_the_capacity():
     for call in (lambda: step(128), lambda: step(129, n_new=torch.tensor([100], dtype=torch.int32))):
         with pytest.raises(ValueError, match="CUDA"):       # the padding does not have to fit
             call()
+
+
+def test_a_cache_names_all_its_memory():
+    """Every pointer that the kernels get is of one of tensors()."""
+    c = V.KVCache(2, 3, 64, 64, 4, "cpu")
+    spans = [(t.untyped_storage().data_ptr(), t.untyped_storage().data_ptr() + t.untyped_storage().nbytes())
+             for t in c.tensors()]
+    for struct in (c._c, c._tail):
+        for name, kind in struct._fields_:
+            if kind is ctypes.c_void_p:
+                assert any(a <= getattr(struct, name) < b for a, b in spans), name
