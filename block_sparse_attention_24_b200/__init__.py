@@ -544,7 +544,9 @@ def veda_kv_attn(cache: KVCache, q: torch.Tensor, o: torch.Tensor, scale: float,
 def veda_kv_evict(cache: KVCache, keep: Sequence[int], sink: int, recent: int, out: Optional[KVCache] = None,
                   stream=None):
     """Drop each head's least attended tiles, down to keep[h] (one per K/V
-    head), in place or into `out`, whose arrays of tiles are others."""
+    head), in place or into `out`, whose arrays of tiles are others. Their
+    slots are the next to be written to: entries behind the tiles in use whose
+    slot is shared have to be given another before the next append."""
     if len(keep) != cache.heads_kv:
         raise ValueError(f"keep must have {cache.heads_kv} entries, not {len(keep)}")
     if out is not None and out.device != cache.device:

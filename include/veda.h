@@ -363,8 +363,10 @@ int veda_output_sq_error(const veda_layer* L, const void* a, const void* b, floa
  * All pointers are DEVICE memory, 16-byte aligned, all arrays contiguous;
  * nb_cap <= 8192, heads_kv <= 128, B <= 65535, positions below 2^31 - tile.
  * A tile that append writes to has a slot of its own; tiles that are only
- * read may share one. Calls on one cache are ordered by the caller (one
- * stream, or events between streams).
+ * read may share one (a prefix of several sequences). So an entry behind the
+ * tiles in use, which a later append begins, names no slot that is shared (see
+ * veda_kv_evict). Calls on one cache are ordered by the caller (one stream, or
+ * events between streams).
  *
  * A step is append, attention, advance: the new tokens are pending (written
  * behind the len tokens and seen by attention) until veda_kv_advance takes
@@ -468,8 +470,10 @@ int veda_kv_attn_fill(const veda_kv_cache* C, const void* q, const int64_t* q_st
  * others the keep[h] - sink - recent with the largest weight (ties: the lower
  * index; NaN ranks first). The entries of table, pos, k_scale, v_scale and
  * weight are permuted: tiles that stay first, in their order, then the ones
- * that go, in theirs (their slots are free again), then the free ones as they
- * were; len is reduced by whole tiles. Pending tokens must have been taken in
+ * that go, in theirs, then the free ones as they were. The next tokens go to
+ * the slots of those that went, so where such a slot is shared with another
+ * sequence or cache (or with the one that `out` was made from), the caller
+ * puts a slot of this head's own into its entry before the next append. len is reduced by whole tiles. Pending tokens must have been taken in
  * (veda_kv_advance). `out` (NULL = in place): a cache of the same geometry
  * whose table, pos, scales, weight, len and next_pos receive the result while
  * C's stay; its arrays are all others than C's. Pools are not touched. */

@@ -151,3 +151,32 @@ def test_rows_without_a_query_are_filled(n, heads, d):
         assert (fo[b, m:] == 0).all() and (flse[b, :, m:] == -float("inf")).all()
     V.veda_kv_attn(c, q, q, 0.125, workspace(c, heads, n, False), n_new=news, fill=True)     # over the query
     assert torch.equal(q, fo)
+
+
+def test_evicted_tiles_of_a_shared_prefix():
+    """Two sequences read one prefix, one of them drops some of it and goes on:
+    with slots of its own in the entries that it gave up, the other's tokens
+    stay as they are. (The slots: those that the prefix stands in for.)"""
+    hkv, d, tile = 1, 64, 64
+    c = random_cache(40, 2, hkv, d, tile, 6, [256, 256])
+    own = c.table[1, 0, :3].clone()
+    c.table[1, 0, :3] = c.table[0, 0, :3]
+    c.len[0] = 100                                      # (fewer tiles than are kept: nothing leaves)
+    c.next_pos[0] = 100
+    c.weight[1, 0, :4] = torch.tensor([9.0, 1.0, 8.0, 1.0], device=DEV)
+    V.veda_kv_evict(c, [3], 1, 1)
+    shared = c.table[0, 0, :2].tolist()
+    assert c.len.tolist() == [[100], [192]] and int(c.table[1, 0, 3]) == shared[1]
+    c.table[1, 0, 3] = own[1]
+    k, v, q = bf16(41, 2, 70, hkv, d), bf16(42, 2, 70, hkv, d), bf16(43, 2, 70, 2, d)
+    nn = torch.tensor([0, 70], dtype=torch.int32, device=DEV)
+    before = [t.view(torch.uint8)[shared].clone() for t in (c.k8, c.v8)]
+    want = oracle_of(c)
+    V.veda_kv_append(c, k, v, n_new=nn)
+    want.append(host(k), host(v), [0, 70])
+    assert_same_state(c, want)
+    for x, t in zip(before, (c.k8, c.v8)):
+        assert torch.equal(x, t.view(torch.uint8)[shared])
+    check_attention(c, q, news=[0, 70])
+    V.veda_kv_advance(c, 70, n_new=nn)
+    check_attention(c, q, pending=False)
