@@ -245,8 +245,8 @@ __device__ __forceinline__ int block_prefix(bool flag, int* warp_n, int& total) 
 // histograms, by lane, keep the counters apart), and the row is written back
 // with the tiles that stay first, in their order, then those that go, then the
 // free ones. Nothing of the codes moves. Latency, not bandwidth, is the bound,
-// so the block has a thread per two to eight entries: 24 rows of 300 entries
-// take 5.6 us, 256 rows of 2,047 take 9.4 us.
+// so the block has a thread per entry or few (eight at most): 24 rows of 300
+// entries take 5.6 us, 256 rows of 2,047 take 9.4 us.
 template <int THREADS>
 __global__ void __launch_bounds__(THREADS)
     kv_evict_kernel(const KvGeom g, const KvGeom out, const KvKeep keeps, const int sink, const int recent) {

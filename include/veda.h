@@ -350,7 +350,8 @@ int veda_output_sq_error(const veda_layer* L, const void* a, const void* b, floa
  *   tile, d], of which table[b, h, i] names the slot of the i-th tile of
  *   sequence b and K/V head h, and one positive fp32 scale per (b, h, tile)
  *   for K and one for V. A scale that is NaN makes every value of its tile
- *   NaN.
+ *   NaN. The codes are finite: append writes no others, and a NaN code that the
+ *   caller puts in may reach queries whose mask hides its token.
  *   len[b, h]    tokens that the head holds: its first ceil(len / tile) table
  *                entries, the last of them filled up to len
  *   pos[b, h, i] position in the stream of a tile's first token; the tile's
@@ -449,8 +450,16 @@ int veda_kv_advance(const veda_kv_cache* C, int32_t n, const int32_t* n_new, cud
  *     call's queries, over the head's whole group, gave its tokens); decay 0
  *     overwrites. Sequences without new rows keep theirs. Summed in a fixed
  *     order.
- * Tiles that no query sees are not read. q K^T is exact products summed in
- * fp32; P is rounded to fp16, the sums and O are fp32.
+ * Tiles that no query sees are not read. K and V are read exactly. What is
+ * rounded goes by the query rows per K/V head, n_q * heads / heads_kv:
+ *   up to 16: each q row times a power of two is the sum of four e4m3 parts,
+ *     which leave out at most 2^-29 of the row's largest |q|; P is four e4m3
+ *     parts, exact to 2^-16 of itself or 2^-29 of the row's largest p times its
+ *     tile's V scale, whichever is more.
+ *   above: q is two e4m3 parts, which leave out at most 2^-17 of the row's
+ *     largest |q|; P is fp16 (2^-11 of itself, or 2^-32 of that largest).
+ * Products are summed in fp32; the softmax's sums, lse, the weights and O are
+ * fp32, and o is rounded to bf16 once.
  * o may be q itself.
  * ws: veda_kv_attn_ws_bytes(C, heads, n_q, weight != NULL) bytes of device
  * scratch, not shared by calls that may run at the same time. */
