@@ -394,24 +394,26 @@ class KVCache:
             setattr(self, name, t)
         self.device = device
         self.n_slots = n_slots
-        words = torch.zeros(4 + B * heads_kv, dtype=torch.int32, device=device)
-        self.status, self._arrive = words[:4], words[4:]
+        # one allocation, its parts at multiples of 16 bytes
+        bh = B * heads_kv
+        words = torch.zeros(4 + 13 * bh, dtype=torch.int32, device=device)
+        self.status, self.tail_key = words[:4], words[4:4 + 8 * bh].view(B, heads_kv, 2, 4)
+        self.tail_scale = words[4 + 8 * bh:4 + 12 * bh].view(torch.float32).view(B, heads_kv, 2, 2)
+        self._arrive = words[4 + 12 * bh:]
+        self.tail_codes = torch.zeros((B, heads_kv, 2, tile, d), dtype=torch.uint8, device=device).view(torch.float8_e4m3fn)
+        self._tail = _KvTail(self.tail_codes.data_ptr(), self.tail_key.data_ptr(), self.tail_scale.data_ptr())
+        self.tail_ref = ctypes.byref(self._tail)
         self._c = _KvCache(B, heads_kv, d, tile, n_slots, nb_cap,
                            *[getattr(self, n).data_ptr() for n in ("k8", "v8", "table", "pos", "k_scale", "v_scale",
                                                                    "weight", "len", "next_pos", "_arrive",
                                                                    "status")])
-        self.tail_codes = torch.zeros((B, heads_kv, 2, tile, d), dtype=torch.uint8, device=device).view(torch.float8_e4m3fn)
-        self.tail_key = torch.zeros((B, heads_kv, 2, 4), dtype=torch.int32, device=device)
-        self.tail_scale = torch.zeros((B, heads_kv, 2, 2), dtype=torch.float32, device=device)
-        self._tail = _KvTail(self.tail_codes.data_ptr(), self.tail_key.data_ptr(), self.tail_scale.data_ptr())
-        self.tail_ref = ctypes.byref(self._tail)
         self._ws_bytes = {}  # of veda_kv_attn, by (heads, n_q, with weights)
         self.ref = ctypes.byref(self._c)
 
     def tensors(self):
         """All the device memory that a call on the cache may use."""
         return [getattr(self, n) for n in ("k8", "v8", "table", "pos", "k_scale", "v_scale", "weight", "len", "next_pos",
-                                           "status", "tail_codes", "tail_key", "tail_scale")]
+                                           "status", "tail_codes")]  # (with status all counters)
 
     def __setattr__(self, name, value):
         # the kernels have the tensors' addresses: another tensor would be
