@@ -48,7 +48,7 @@ namespace {
 // the same (1,500 keys) or more (window 2,048: 27 against 22 us; 80,640 keys: 223
 // against 154 us): clusters leave SM slots empty.
 // Up to 16 rows: at 32 rows and 16 x 8,190 keys two passes of this kernel would
-// take 170 us, the tile kernel takes 109.
+// take 170 us, the tile kernel takes 93.
 constexpr int FEW_ROWS = 16;
 constexpr float MARGIN = 1.5f;  // P <= 2^(OFF + MARGIN) = 362 < 448
 

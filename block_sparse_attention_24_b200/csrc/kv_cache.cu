@@ -51,9 +51,10 @@ __device__ __forceinline__ uint4 codes_moved(uint4 w, float f) {
 // old codes moved to it (rounded once more where it grew), new ones quantised,
 // the rows behind the last token zeroed. The tile's bf16 rows are held in
 // registers between the maximum and the rounding, so they are read once:
-// 2 bytes in and 1 out per value. 3,840 tokens of 24 heads, d = 128: 14.7 us,
-// 4.8 TB/s (of 6.5 measured for a copy); five to seven CTAs per SM instead of
-// four, by fewer registers, took 16.5 to 22.3 us where four took 16.6; 128 or 512 threads take 19.
+// 2 bytes in and 1 out per value. 3,840 tokens of 24 heads, d = 128: 14.9 us,
+// 4.7 TB/s (of 6.5 measured for a copy). In earlier forms of this kernel five to
+// seven CTAs per SM instead of four, by fewer registers, took 16.5 to 22.3 us
+// where four took 16.6, and 128 or 512 threads 19 where 256 took 15.1.
 //
 // The older codes of a tile that tokens join are rounded in place, and those
 // tokens are only pending: the codes and the scale as they were go to `tail`
@@ -112,7 +113,7 @@ __global__ void __launch_bounds__(APPEND_THREADS)
   uint8_t* const kept_codes = tail.codes + kept * g.tile * D;
   // the tail may be what a raise left of the kept codes: both are looked at, in
   // the registers of the rows that are not new (in a loop and registers of their
-  // own the frame took 15.5 us instead of 14.7, one token 4.3 instead of 3.5)
+  // own the frame took 15.5 us where it took 14.7, one token 4.3 where it took 3.5)
   const bool raise_left = joins && !absent && key.x == -row0 && key.y == slot && key.z == next &&
                           __float_as_uint(was.y) == __float_as_uint(s_old);
   bool back = raise_left;  // the kept codes and scale are the committed ones

@@ -27,7 +27,7 @@
 //   warp 9           MMA issuer (one thread)
 //   warps 10, 11     V: e4m3 tile -> fp16 tile
 // Every wait is bounded, as in the other pipelines.
-// Measured: 3,840 x 34,560, 24 heads, d = 128: 1.66 ms, 980 TFLOP/s (a step of 256
+// Measured: 3,840 x 34,560, 24 heads, d = 128: 1.68 ms, 970 TFLOP/s (a step of 256
 // rows x 128 keys takes ~3,680 clocks against 2,048 of MMA; the clock is held at
 // ~1.7 GHz by power); 2,048-token causal prompt, 32/8 heads: 65 us.
 #include "kv_attn.cuh"
