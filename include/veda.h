@@ -483,7 +483,7 @@ int veda_kv_attn_fill(const veda_kv_cache* C, const void* q, const int64_t* q_st
  * the slots of those that went, so where such a slot is shared with another
  * sequence or cache (or with the one that `out` was made from), the caller
  * puts a slot of this head's own into its entry before the next append. len is reduced by whole tiles. Pending tokens must have been taken in
- * (veda_kv_advance). `out` (NULL = in place): a cache of the same geometry
+ * (veda_kv_advance) or dropped. `out` (NULL = in place): a cache of the same geometry
  * whose table, pos, scales, weight, len and next_pos receive the result while
  * C's stay; its arrays are all others than C's. Pools are not touched. */
 int veda_kv_evict(const veda_kv_cache* C, const int32_t* keep, int32_t sink, int32_t recent,
